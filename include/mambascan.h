@@ -437,6 +437,180 @@ size_t mss_ssd_bwd_workspace_size(int64_t batch, int64_t seqlen, int64_t nheads,
                                   int64_t ngroups, int64_t dstate, mss_dtype in_dtype);
 
 /* ------------------------------------------------------------------------ */
+/* Norm before a block, fused with its residual.                             */
+/*                                                                          */
+/* A layer is a mixer between projections, with a residual path around it    */
+/* ("Mamba-1/2/3 visual guide", section 2 block diagram).  Per row (one      */
+/* token; RMS(v) = v / sqrt(mean(v^2) + eps)), m_c = scale * gamma[c]        */
+/* (gamma NULL: scale):                                                      */
+/*   x' = RMS(x) * post_weight  (post_weight NULL: x' = x; else the previous */
+/*        block's output is normed before it joins the residual)             */
+/*   r = residual + m x'        (residual NULL: r = m x')                    */
+/*   residual_out = r rounded to res_dtype;  out = RMS(r) * weight           */
+/* out is formed from r in fp32, before it is rounded for residual_out.      */
+/* One row is the form for a generated token.                                */
+/*                                                                          */
+/* Layouts: x, out [rows, cols] io_dtype; residual, residual_out [rows,      */
+/*   cols] res_dtype, each with its own row stride (elements, at least cols) */
+/*   and any alignment of its element type; weight, post_weight, gamma       */
+/*   [cols] fp32.                                                            */
+/* out_q, out_scale (both or neither): the 8-bit form of out as stored, see  */
+/*   mss_pack8.                                                              */
+/* Supported: io and res both fp32, both bf16, or io bf16 with res fp32;     */
+/* cols up to 16384 (else MSS_ERR_UNSUPPORTED); eps > 0 (else                */
+/* MSS_ERR_UNSUPPORTED); rows * stride below 2^47 (else MSS_ERR_SHAPE).      */
+/* `flags` must be 0.  Outputs must not overlap inputs or each other (rows   */
+/* of one wider buffer, with the same stride, may interleave).               */
+/* ------------------------------------------------------------------------ */
+mss_status mss_add_norm_fwd(const void* x, int64_t x_stride, const void* residual,
+                            int64_t residual_stride, const float* weight, const float* post_weight,
+                            const float* gamma, float scale, float eps, void* out,
+                            int64_t out_stride, void* residual_out, int64_t residual_out_stride,
+                            int8_t* out_q, uint8_t* out_scale, int64_t rows, int64_t cols,
+                            mss_dtype io_dtype, mss_dtype res_dtype, uint32_t flags,
+                            void* hip_stream);
+
+/* ------------------------------------------------------------------------ */
+/* Its backward: the gradients of a loss given dout = dloss/dout and         */
+/* dresidual_out = dloss/dresidual_out (NULL = zero), at the stored residual */
+/* r (= residual_out of the forward).  With g = dout * weight:               */
+/*   dr = rstd g - r rstd^3 mean(g r) + dresidual_out;  dresidual = dr       */
+/*   dweight = sum_rows dout RMS(r);  dgamma = scale * sum_rows dr x'        */
+/*   dx = m dr, or through RMS(x) * post_weight; dpost_weight likewise.      */
+/* Sums over rows run in fp32 in a fixed order: bitwise repeatable.          */
+/*                                                                          */
+/* dout, dx, x io_dtype; dresidual_out, dresidual, r res_dtype; strides as   */
+/* in the forward.  dx and dresidual may each be NULL (not computed).        */
+/* x is needed (and read) exactly with post_weight or gamma (else            */
+/* MSS_ERR_NULL without it; pass NULL otherwise).  dpost_weight and dgamma   */
+/* are given exactly when post_weight and gamma are (else MSS_ERR_NULL).     */
+/* r_scale, x_scale: when r_scale is given, r holds the 8-bit form's q       */
+/* (mss_pack8; its stride is ignored) and x, if needed, its own q with       */
+/* x_scale; both are in the 8-bit form or neither (else                      */
+/* MSS_ERR_UNSUPPORTED).  q 16-byte aligned (else MSS_ERR_ALIGN).            */
+/* Limits as in the forward.  `workspace` needs                              */
+/* mss_add_norm_bwd_workspace_size() bytes, 16-byte aligned, ngrads the      */
+/* number of weight gradients (1 + post_weight + gamma).                     */
+/* ------------------------------------------------------------------------ */
+mss_status mss_add_norm_bwd(const void* dout, int64_t dout_stride, const void* dresidual_out,
+                            int64_t dresidual_out_stride, const void* r, int64_t r_stride,
+                            const uint8_t* r_scale, const void* x, int64_t x_stride,
+                            const uint8_t* x_scale, const float* weight, const float* post_weight,
+                            const float* gamma, float scale, float eps, void* dx, int64_t dx_stride,
+                            void* dresidual, int64_t dresidual_stride, float* dweight,
+                            float* dpost_weight, float* dgamma, int64_t rows, int64_t cols,
+                            mss_dtype io_dtype, mss_dtype res_dtype, uint32_t flags,
+                            void* workspace, size_t workspace_bytes, void* hip_stream);
+
+/* Bytes of device workspace mss_add_norm_bwd needs (0 when unsupported). */
+size_t mss_add_norm_bwd_workspace_size(int64_t rows, int64_t cols, int64_t ngrads);
+
+/* The gate after the norm instead of before it (mss_gated_norm_fwd, _bwd). */
+#define MSS_FLAG_NORM_FIRST 0x20u
+
+/* ------------------------------------------------------------------------ */
+/* Norm after a mixer, fused with its gate.                                  */
+/*                                                                          */
+/* The mixer's output is multiplied by a gate branch ("Mamba-1/2/3 visual    */
+/* guide", section 2 block diagram); the norm lies between it and the output */
+/* projection.  Per row and group of cols / ngroups columns:                 */
+/*   out = RMS(y * silu(z)) * weight                                         */
+/*   out = RMS(y) * weight * silu(z)      with MSS_FLAG_NORM_FIRST           */
+/*   out = RMS(y) * weight                when z is NULL                     */
+/* One row is the form for a generated token.                                */
+/*                                                                          */
+/* y [rows, cols] y_dtype; z, out [rows, cols] io_dtype; row strides and     */
+/* alignment as in mss_add_norm_fwd (z may be a slice of a projection's      */
+/* output); weight [cols] fp32.                                              */
+/* y_q, y_scale (and z_q, z_scale exactly when z is given): the 8-bit forms  */
+/* of y and z, for mss_gated_norm_bwd; out_q, out_scale: that of out as      */
+/* stored (each NULL: not written; see mss_pack8).                           */
+/* Supported: y and io both fp32, both bf16, or y fp32 with io bf16; ngroups */
+/* dividing cols, at most 65535; cols / ngroups up to 16384, and a multiple  */
+/* of 32 when an 8-bit form is asked for and ngroups > 1 (else               */
+/* MSS_ERR_UNSUPPORTED); eps > 0; rows * stride below 2^47.  Outputs must    */
+/* not overlap inputs or each other.                                         */
+/* ------------------------------------------------------------------------ */
+mss_status mss_gated_norm_fwd(const void* y, int64_t y_stride, const void* z, int64_t z_stride,
+                              const float* weight, float eps, void* out, int64_t out_stride,
+                              int8_t* y_q, uint8_t* y_scale, int8_t* z_q, uint8_t* z_scale,
+                              int8_t* out_q, uint8_t* out_scale, int64_t rows, int64_t cols,
+                              int64_t ngroups, mss_dtype y_dtype, mss_dtype io_dtype,
+                              uint32_t flags, void* hip_stream);
+
+/* ------------------------------------------------------------------------ */
+/* Its backward, given dout: dy (y_dtype), dz (io_dtype; exactly when z is   */
+/* given), dweight.  When y_scale is given y holds the 8-bit form's q (its   */
+/* stride is ignored), and so does z with z_scale; the gradient is the one   */
+/* at the values that the forms stand for.  Sums over rows run in fp32 in a  */
+/* fixed order: bitwise repeatable.  Limits as in the forward; `workspace`   */
+/* needs mss_gated_norm_bwd_workspace_size() bytes, 16-byte aligned.         */
+/* ------------------------------------------------------------------------ */
+mss_status mss_gated_norm_bwd(const void* dout, int64_t dout_stride, const void* y,
+                              int64_t y_stride, const uint8_t* y_scale, const void* z,
+                              int64_t z_stride, const uint8_t* z_scale, const float* weight,
+                              float eps, void* dy, int64_t dy_stride, void* dz, int64_t dz_stride,
+                              float* dweight, int64_t rows, int64_t cols, int64_t ngroups,
+                              mss_dtype y_dtype, mss_dtype io_dtype, uint32_t flags,
+                              void* workspace, size_t workspace_bytes, void* hip_stream);
+
+/* Bytes of device workspace mss_gated_norm_bwd needs (0 when unsupported). */
+size_t mss_gated_norm_bwd_workspace_size(int64_t rows, int64_t cols, int64_t ngroups);
+
+/* ------------------------------------------------------------------------ */
+/* 8-bit activation checkpoints: a tensor that a backward pass will need,    */
+/* held in 8.25 bits an element.                                             */
+/*                                                                          */
+/* Per row and block of 32 columns, scale s = 2^(e - 127): the smallest      */
+/* power of two with max|x| / s < 127.5; q = x / s rounded to nearest, ties  */
+/* to even.  The value it stands for, q s, is within s / 2 of x and exact in */
+/* bf16 and fp32.  1 <= e <= 248 (blocks of zeros or of values below 2^-120  */
+/* have e = 1; values that would reach 2^128 saturate at 127 * 2^121).  A    */
+/* block that holds an infinity or NaN has e = 255 and q = 0, and reads back */
+/* as NaN.                                                                   */
+/*   q     [rows, pitch] int8, pitch = cols rounded up to a multiple of 32   */
+/*         (the columns past cols hold 0), 16-byte aligned;                  */
+/*   scale [rows, pitch / 32] bytes e.                                       */
+/* x [rows, cols] dtype with a row stride, any alignment of its type.        */
+/* mss_unpack8 writes q s, for the backward passes that take 16- or 32-bit   */
+/* inputs; columns past cols are not written.                                */
+/* Supported: cols below 2^30; rows * stride below 2^47 and rows * pitch     */
+/* below 2^36 (else MSS_ERR_SHAPE).  Outputs must not overlap inputs or each */
+/* other.                                                                    */
+/* ------------------------------------------------------------------------ */
+mss_status mss_pack8(const void* x, int64_t x_stride, int8_t* q, uint8_t* scale, int64_t rows,
+                     int64_t cols, mss_dtype dtype, void* hip_stream);
+mss_status mss_unpack8(const int8_t* q, const uint8_t* scale, void* x, int64_t x_stride,
+                       int64_t rows, int64_t cols, mss_dtype dtype, void* hip_stream);
+
+/* dw is added to instead of written (mss_wgrad8). */
+#define MSS_FLAG_ACCUMULATE 0x40u
+
+/* ------------------------------------------------------------------------ */
+/* Weight gradient of a linear layer Y = X W^T whose input X was kept in the */
+/* 8-bit form, on the matrix cores:                                          */
+/*   dw[o, i] = sum_t dy[t, o] * q[t, i] * 2^(scale[t, i / 32] - 127)        */
+/* (plus dw[o, i] with MSS_FLAG_ACCUMULATE).  Products of the exact bf16     */
+/* values, sums in fp32 in an order that depends on the shape alone: bitwise */
+/* repeatable.                                                               */
+/*   dy [tokens, outs] bf16 with a row stride, any alignment of its type;    */
+/*   q, scale: the form of mss_pack8 of a [tokens, ins] tensor;              */
+/*   dw [outs, ins] dw_dtype.                                                */
+/* Supported: outs and ins up to 2^20, outs * ins up to 2^34, tokens up to   */
+/* 2^36, tokens * dy_stride below 2^47 (else MSS_ERR_SHAPE); dy_dtype        */
+/* MSS_BF16 (else MSS_ERR_UNSUPPORTED: fp32 gradients would have to be       */
+/* rounded).  dw 16-byte aligned; it must not overlap an input.  `workspace` */
+/* needs mss_wgrad8_workspace_size() bytes, 16-byte aligned.                 */
+/* ------------------------------------------------------------------------ */
+mss_status mss_wgrad8(const void* dy, int64_t dy_stride, const int8_t* q, const uint8_t* scale,
+                      void* dw, int64_t tokens, int64_t outs, int64_t ins, mss_dtype dy_dtype,
+                      mss_dtype dw_dtype, uint32_t flags, void* workspace, size_t workspace_bytes,
+                      void* hip_stream);
+
+/* Bytes of device workspace mss_wgrad8 needs (0 when unsupported). */
+size_t mss_wgrad8_workspace_size(int64_t tokens, int64_t outs, int64_t ins);
+
+/* ------------------------------------------------------------------------ */
 /* Status of a call that used `workspace`.                                   */
 /*                                                                          */
 /* The selective scan (forward, fused, backward) hands states between        */

@@ -18,6 +18,11 @@ Operations (see the header for the exact definitions and layouts):
   mamba3_state_update one Mamba-3 generation step (trapezoid input, complex
                       state, MIMO rank R as options), state updated in place
   ssd_chunk_fwd       Mamba-2 SSD layer, chunked, dense products on MFMA
+Around the mixer (norms.py):
+  add_norm_fwd, add_norm_bwd      norm before a block with its residual
+  gated_norm_fwd, gated_norm_bwd  norm after a mixer with its gate
+  pack8, unpack8, Packed8         8-bit activation checkpoints
+  wgrad8              weight gradient from an 8-bit checkpoint, on MFMA
 """
 from __future__ import annotations
 
@@ -36,6 +41,8 @@ MSS_FLAG_DECAY_GENERAL = 0x1
 MSS_FLAG_CONV_SILU = 0x2
 MSS_FLAG_DELTA_SOFTPLUS = 0x4
 MSS_FLAG_COMPLEX_STATE = 0x10
+MSS_FLAG_NORM_FIRST = 0x20
+MSS_FLAG_ACCUMULATE = 0x40
 
 STATUS_NAMES = {0: "MSS_OK", 1: "MSS_ERR_NULL", 2: "MSS_ERR_SHAPE", 3: "MSS_ERR_DTYPE", 4: "MSS_ERR_ALIGN",
                 5: "MSS_ERR_UNSUPPORTED", 6: "MSS_ERR_WORKSPACE", 7: "MSS_ERR_ALIAS", 8: "MSS_ERR_HIP",
@@ -50,6 +57,9 @@ EXPORTS = ("mss_selective_scan_fwd", "mss_selective_scan_fwd_noalloc", "mss_sele
            "mss_selective_scan_fused_bwd_workspace_size", "mss_state_update",
            "mss_mamba3_state_update",
            "mss_ssd_chunk_fwd", "mss_ssd_workspace_size", "mss_ssd_chunk_bwd", "mss_ssd_bwd_workspace_size",
+           "mss_add_norm_fwd", "mss_add_norm_bwd", "mss_add_norm_bwd_workspace_size",
+           "mss_gated_norm_fwd", "mss_gated_norm_bwd", "mss_gated_norm_bwd_workspace_size",
+           "mss_pack8", "mss_unpack8", "mss_wgrad8", "mss_wgrad8_workspace_size",
            "mss_workspace_status", "mss_status_string",
            "mss_last_hip_error", "mss_abi_version")
 
@@ -112,6 +122,31 @@ def lib() -> ctypes.CDLL:
     L.mss_ssd_chunk_bwd.restype = ctypes.c_int
     L.mss_ssd_bwd_workspace_size.argtypes = [i64, i64, i64, i64, i64, i64, ctypes.c_int]
     L.mss_ssd_bwd_workspace_size.restype = sz
+    ci, cf = ctypes.c_int, ctypes.c_float
+    L.mss_add_norm_fwd.argtypes = [vp, i64, vp, i64, fp, fp, fp, cf, cf, vp, i64, vp, i64, vp, vp, i64, i64, ci, ci,
+                                   u32, vp]
+    L.mss_add_norm_fwd.restype = ci
+    L.mss_add_norm_bwd.argtypes = [vp, i64, vp, i64, vp, i64, vp, vp, i64, vp, fp, fp, fp, cf, cf, vp, i64, vp, i64,
+                                   fp, fp, fp, i64, i64, ci, ci, u32, vp, sz, vp]
+    L.mss_add_norm_bwd.restype = ci
+    L.mss_add_norm_bwd_workspace_size.argtypes = [i64, i64, i64]
+    L.mss_add_norm_bwd_workspace_size.restype = sz
+    L.mss_gated_norm_fwd.argtypes = [vp, i64, vp, i64, fp, cf, vp, i64, vp, vp, vp, vp, vp, vp, i64, i64, i64, ci, ci,
+                                     u32, vp]
+    L.mss_gated_norm_fwd.restype = ci
+    L.mss_gated_norm_bwd.argtypes = [vp, i64, vp, i64, vp, vp, i64, vp, fp, cf, vp, i64, vp, i64, fp, i64, i64, i64,
+                                     ci, ci, u32, vp, sz, vp]
+    L.mss_gated_norm_bwd.restype = ci
+    L.mss_gated_norm_bwd_workspace_size.argtypes = [i64, i64, i64]
+    L.mss_gated_norm_bwd_workspace_size.restype = sz
+    L.mss_pack8.argtypes = [vp, i64, vp, vp, i64, i64, ci, vp]
+    L.mss_pack8.restype = ci
+    L.mss_unpack8.argtypes = [vp, vp, vp, i64, i64, i64, ci, vp]
+    L.mss_unpack8.restype = ci
+    L.mss_wgrad8.argtypes = [vp, i64, vp, vp, vp, i64, i64, i64, ci, ci, u32, vp, sz, vp]
+    L.mss_wgrad8.restype = ci
+    L.mss_wgrad8_workspace_size.argtypes = [i64, i64, i64]
+    L.mss_wgrad8_workspace_size.restype = sz
     L.mss_workspace_status.argtypes = [vp, vp]
     L.mss_workspace_status.restype = ctypes.c_int
     L.mss_status_string.argtypes = [ctypes.c_int]
@@ -587,3 +622,7 @@ def ssd_chunk_bwd(x, delta, A, B, C, D=None, z=None, h0=None, *, dy, dh_last=Non
                                  _stream(stream))
     _raise(st, "mss_ssd_chunk_bwd")
     return g
+
+
+from .norms import (Packed8, add_norm_bwd, add_norm_fwd, gated_norm_bwd, gated_norm_fwd, pack8,  # noqa: E402
+                    unpack8, wgrad8)

@@ -1,0 +1,324 @@
+// Norm before a block, fused with the residual (gfx950): forward and backward.
+//
+// Per row, with RMS(v) = v rstd(v), rstd(v) = 1 / sqrt(mean(v^2) + eps) and
+// m_c = scale * gamma_c:
+//   x' = post ? RMS(x) post : x;  r = residual + m x';  out = RMS(r) w.
+// Backward at the stored r, with g = dout w:
+//   dr = rstd g - r rstd^3 mean(g r) + dresidual_out      (dresidual)
+//   dw = sum_rows dout r rstd;  dgamma = scale sum_rows dr x'
+//   dx = m dr, or with post, n = RMS(x), g2 = m dr post:
+//   dpost = sum_rows m dr n;  dx = rstd_x g2 - x rstd_x^3 mean(g2 x).
+// rstd is formed again from r in the backward: sum(r^2) and sum(g r) are one
+// reduction, so it costs nothing and needs no tensor of its own.
+//
+// Every element is read once and written once, nothing else: both directions
+// are bound by HBM.  Rows are laid over lanes as norm_common.hpp describes.
+#include <type_traits>
+
+#include "norm_common.hpp"
+
+namespace mss {
+namespace {
+
+struct FwdArgs {
+  AddNormFwdParams p;
+  int pitch;
+};
+
+template <bool RES32, bool IO32, bool POST, int LANES, int K>
+__global__ void __launch_bounds__(LANES ? 256 : 1024) add_norm_fwd_kernel(FwdArgs a) {
+  constexpr int SR = RES32 ? kSrcF32 : kSrcBf16, SX = IO32 ? kSrcF32 : kSrcBf16;
+  __shared__ float lds[LANES ? 1 : kRowSumFloats];
+  int half = 0;
+  const Place<LANES> at;
+  const int cols = (int)a.p.cols;
+  const float inv = 1.0f / (float)cols;
+  int col[K], n[K];
+  float w[K][8], post[K][8], m[K][8];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    col[k] = at.col(k);
+    n[k] = cols - col[k];
+    load_w(a.p.weight, col[k], n[k], w[k]);
+    if constexpr (POST) load_w(a.p.post_weight, col[k], n[k], post[k]);
+    if (a.p.gamma != nullptr) {
+      load_w(a.p.gamma, col[k], n[k], m[k]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m[k][j] *= a.p.scale;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m[k][j] = a.p.scale;
+    }
+  }
+  const int64_t step = (int64_t)gridDim.x * at.nseg;
+  int64_t row = (int64_t)blockIdx.x * at.nseg + at.seg;
+  Raw<SX> nx[K];
+  Raw<SR> nr[K];
+  auto fetch = [&](int64_t i) {
+    const char* xr = static_cast<const char*>(a.p.x) + i * a.p.x_stride * (IO32 ? 4 : 2);
+    const char* rr = static_cast<const char*>(a.p.residual) + i * a.p.residual_stride * (RES32 ? 4 : 2);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      nx[k] = load_raw<SX>(xr, nullptr, col[k], n[k]);
+      nr[k] = load_raw<SR>(rr, nullptr, col[k], a.p.residual != nullptr ? n[k] : 0);
+    }
+  };
+  if (row < a.p.rows) fetch(row);
+  for (; row < a.p.rows; row += step) {
+    float x[K][8], r[K][8];
+#pragma unroll
+    for (int k = 0; k < K; ++k) widen<SX>(nx[k], x[k]), widen<SR>(nr[k], r[k]);
+    if (row + step < a.p.rows) fetch(row + step);
+    float sum[1];
+    if constexpr (POST) {
+      sum[0] = 0.f;
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum[0] = __builtin_fmaf(x[k][j], x[k][j], sum[0]);
+      row_sums<LANES>(sum, lds, half);
+      const float rx = rsqrtf(__builtin_fmaf(sum[0], inv, a.p.eps));
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[k][j] = x[k][j] * rx * post[k][j];
+    }
+    sum[0] = 0.f;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        r[k][j] = __builtin_fmaf(m[k][j], x[k][j], r[k][j]);
+        sum[0] = __builtin_fmaf(r[k][j], r[k][j], sum[0]);
+      }
+    char* rout = static_cast<char*>(a.p.residual_out) + row * a.p.residual_out_stride * (RES32 ? 4 : 2);
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      if (n[k] > 0) store8<RES32>(rout, col[k], n[k], r[k]);
+    row_sums<LANES>(sum, lds, half);
+    const float rstd = rsqrtf(__builtin_fmaf(sum[0], inv, a.p.eps));
+    char* out = static_cast<char*>(a.p.out) + row * a.p.out_stride * (IO32 ? 4 : 2);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      float o[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] = r[k][j] * rstd * w[k][j];
+      if (n[k] > 0) store8<IO32>(out, col[k], n[k], o);
+      if (a.p.out_q != nullptr) {
+        as_stored<IO32>(o);  // the form of the output as it is stored
+        store_p8(a.p.out_q + row * a.pitch, a.p.out_scale + row * (a.pitch >> 5), col[k], a.pitch, o);
+      }
+    }
+  }
+}
+
+struct BwdArgs {
+  AddNormBwdParams p;
+  float* part;  // [blocks][nout][cols]
+  int nout;
+  int pitch;
+  int* status;
+};
+
+// EXTRA: 0 = x unused, 1 = gamma, 2 = post (and gamma where given).
+template <bool RES32, bool IO32, bool PACKED, int EXTRA, int LANES, int K>
+__global__ void __launch_bounds__(LANES ? 256 : 1024) add_norm_bwd_kernel(BwdArgs a) {
+  constexpr int SD = RES32 ? kSrcF32 : kSrcBf16, SO = IO32 ? kSrcF32 : kSrcBf16;
+  constexpr int SR = PACKED ? kSrcP8 : SD, SX = PACKED ? kSrcP8 : SO;
+  __shared__ float lds[LANES ? kPartialLds : kRowSumFloats];
+  int half = 0;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;
+  const Place<LANES> at;
+  const int cols = (int)a.p.cols;
+  const float inv = 1.0f / (float)cols;
+  int col[K], n[K];
+  float w[K][8], post[K][8], m[K][8];
+  float dw[K][8] = {}, dgamma[K][8] = {}, dpost[K][8] = {};
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    col[k] = at.col(k);
+    n[k] = cols - col[k];
+    load_w(a.p.weight, col[k], n[k], w[k]);
+    if constexpr (EXTRA == 2) load_w(a.p.post_weight, col[k], n[k], post[k]);
+    if (EXTRA != 0 && a.p.gamma != nullptr) {
+      load_w(a.p.gamma, col[k], n[k], m[k]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m[k][j] *= a.p.scale;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m[k][j] = a.p.scale;
+    }
+  }
+  const int64_t step = (int64_t)gridDim.x * at.nseg;
+  int64_t row = (int64_t)blockIdx.x * at.nseg + at.seg;
+  Raw<SO> nd[K];
+  Raw<SD> ne[K];
+  Raw<SR> nr[K];
+  Raw<SX> nx[EXTRA ? K : 1];
+  auto fetch = [&](int64_t i) {
+    const char* dr = static_cast<const char*>(a.p.dout) + i * a.p.dout_stride * (IO32 ? 4 : 2);
+    const char* er = static_cast<const char*>(a.p.dresidual_out) + i * a.p.dresidual_out_stride * (RES32 ? 4 : 2);
+    const char* rr = static_cast<const char*>(a.p.r) + i * (PACKED ? a.pitch : a.p.r_stride * (RES32 ? 4 : 2));
+    const uint8_t* rs = PACKED ? a.p.r_scale + i * (a.pitch >> 5) : nullptr;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      nd[k] = load_raw<SO>(dr, nullptr, col[k], n[k]);
+      nr[k] = load_raw<SR>(rr, rs, col[k], n[k]);
+      ne[k] = load_raw<SD>(er, nullptr, col[k], a.p.dresidual_out != nullptr ? n[k] : 0);
+    }
+    if constexpr (EXTRA != 0) {
+      const char* xr = static_cast<const char*>(a.p.x) + i * (PACKED ? a.pitch : a.p.x_stride * (IO32 ? 4 : 2));
+      const uint8_t* xs = PACKED ? a.p.x_scale + i * (a.pitch >> 5) : nullptr;
+#pragma unroll
+      for (int k = 0; k < K; ++k) nx[k] = load_raw<SX>(xr, xs, col[k], n[k]);
+    }
+  };
+  if (row < a.p.rows) fetch(row);
+  for (; row < a.p.rows; row += step) {
+    float d[K][8], e[K][8], r[K][8], x[K][8];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      widen<SO>(nd[k], d[k]), widen<SR>(nr[k], r[k]), widen<SD>(ne[k], e[k]);
+      if constexpr (EXTRA != 0) widen<SX>(nx[k], x[k]);
+    }
+    if (row + step < a.p.rows) fetch(row + step);
+    float sum[EXTRA == 2 ? 3 : 2] = {};
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        sum[0] = __builtin_fmaf(r[k][j], r[k][j], sum[0]);
+        sum[1] = __builtin_fmaf(d[k][j] * w[k][j], r[k][j], sum[1]);
+        if constexpr (EXTRA == 2) sum[2] = __builtin_fmaf(x[k][j], x[k][j], sum[2]);
+      }
+    row_sums<LANES>(sum, lds, half);
+    const float rstd = rsqrtf(__builtin_fmaf(sum[0], inv, a.p.eps));
+    const float c1 = rstd * rstd * rstd * (sum[1] * inv);
+    float rx = 0.f, sum2[1] = {};
+    if constexpr (EXTRA == 2) rx = rsqrtf(__builtin_fmaf(sum[2], inv, a.p.eps));
+    char* dres = static_cast<char*>(a.p.dresidual) + row * a.p.dresidual_stride * (RES32 ? 4 : 2);
+    char* dx = static_cast<char*>(a.p.dx) + row * a.p.dx_stride * (IO32 ? 4 : 2);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float rh = r[k][j] * rstd;
+        dw[k][j] = __builtin_fmaf(d[k][j], rh, dw[k][j]);
+        e[k][j] += rstd * (d[k][j] * w[k][j]) - r[k][j] * c1;  // dr
+      }
+      if (a.p.dresidual != nullptr && n[k] > 0) store8<RES32>(dres, col[k], n[k], e[k]);
+      if constexpr (EXTRA == 0) {
+        if (a.p.dx != nullptr && n[k] > 0) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) e[k][j] *= m[k][j];
+          store8<IO32>(dx, col[k], n[k], e[k]);
+        }
+      } else if constexpr (EXTRA == 1) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          dgamma[k][j] = __builtin_fmaf(e[k][j], a.p.scale * x[k][j], dgamma[k][j]);
+          e[k][j] *= m[k][j];
+        }
+        if (a.p.dx != nullptr && n[k] > 0) store8<IO32>(dx, col[k], n[k], e[k]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float nh = x[k][j] * rx;
+          dgamma[k][j] = __builtin_fmaf(e[k][j], a.p.scale * (nh * post[k][j]), dgamma[k][j]);
+          const float dxp = m[k][j] * e[k][j];
+          dpost[k][j] = __builtin_fmaf(dxp, nh, dpost[k][j]);
+          e[k][j] = dxp * post[k][j];  // g2
+          sum2[0] = __builtin_fmaf(e[k][j], x[k][j], sum2[0]);
+        }
+      }
+    }
+    if constexpr (EXTRA == 2) {
+      row_sums<LANES>(sum2, lds, half);
+      const float c2 = rx * rx * rx * (sum2[0] * inv);
+      if (a.p.dx != nullptr) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) e[k][j] = rx * e[k][j] - x[k][j] * c2;
+          if (n[k] > 0) store8<IO32>(dx, col[k], n[k], e[k]);
+        }
+      }
+    }
+  }
+  // [dweight][dgamma where given][dpost]
+  float* part = a.part + (int64_t)blockIdx.x * a.nout * cols;
+#pragma unroll
+  for (int k = 0; k < K; ++k) store_partial<LANES>(part, col[k], n[k], dw[k], lds);
+  if constexpr (EXTRA != 0) {
+    int at_out = 1;
+    if (a.p.gamma != nullptr) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) store_partial<LANES>(part + cols, col[k], n[k], dgamma[k], lds);
+      at_out = 2;
+    }
+    if constexpr (EXTRA == 2) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) store_partial<LANES>(part + (int64_t)at_out * cols, col[k], n[k], dpost[k], lds);
+    }
+  }
+}
+
+template <bool RES32, bool IO32>
+hipError_t fwd_typed(const AddNormFwdParams& p, hipStream_t stream) {
+  const NormShape s = norm_shape(p.cols);
+  const dim3 grid((unsigned)norm_blocks(s, p.rows, 1)), block((unsigned)s.threads);
+  const FwdArgs a{p, (int)((p.cols + 31) / 32 * 32)};
+  return with_shape(s, [&](auto lanes, auto k) {
+    if (p.post_weight != nullptr)
+      hipLaunchKernelGGL((add_norm_fwd_kernel<RES32, IO32, true, lanes.value, k.value>), grid, block, 0, stream, a);
+    else
+      hipLaunchKernelGGL((add_norm_fwd_kernel<RES32, IO32, false, lanes.value, k.value>), grid, block, 0, stream, a);
+    return hipGetLastError();
+  });
+}
+
+template <bool RES32, bool IO32, bool PACKED, int EXTRA>
+hipError_t bwd_typed(const AddNormBwdParams& p, hipStream_t stream) {
+  const NormShape s = norm_shape(p.cols);
+  const int64_t blocks = norm_blocks(s, p.rows, 1);
+  BwdArgs a{p, reinterpret_cast<float*>(static_cast<char*>(p.workspace) + 256), 1, (int)((p.cols + 31) / 32 * 32),
+            static_cast<int*>(p.workspace)};
+  SumPartialsArgs sum{a.part, {p.dweight, nullptr, nullptr}, blocks, p.cols, 1};
+  if (EXTRA != 0 && p.gamma != nullptr) sum.out[sum.nout++] = p.dgamma;
+  if (EXTRA == 2) sum.out[sum.nout++] = p.dpost_weight;
+  a.nout = sum.nout;
+  const hipError_t e = with_shape(s, [&](auto lanes, auto k) {
+    hipLaunchKernelGGL((add_norm_bwd_kernel<RES32, IO32, PACKED, EXTRA, lanes.value, k.value>), dim3((unsigned)blocks),
+                       dim3((unsigned)s.threads), 0, stream, a);
+    return hipGetLastError();
+  });
+  return e != hipSuccess ? e : launch_sum_partials(sum, stream);
+}
+
+template <bool RES32, bool IO32>
+hipError_t bwd_extra(const AddNormBwdParams& p, hipStream_t stream) {
+  const bool packed = p.r_scale != nullptr;
+  if (p.post_weight != nullptr)
+    return packed ? bwd_typed<RES32, IO32, true, 2>(p, stream) : bwd_typed<RES32, IO32, false, 2>(p, stream);
+  if (p.gamma != nullptr)
+    return packed ? bwd_typed<RES32, IO32, true, 1>(p, stream) : bwd_typed<RES32, IO32, false, 1>(p, stream);
+  return packed ? bwd_typed<RES32, IO32, true, 0>(p, stream) : bwd_typed<RES32, IO32, false, 0>(p, stream);
+}
+
+}  // namespace
+
+hipError_t launch_add_norm_fwd(const AddNormFwdParams& p, hipStream_t stream) {
+  if (!p.io_bf16) return fwd_typed<true, true>(p, stream);
+  return p.res_bf16 ? fwd_typed<false, false>(p, stream) : fwd_typed<true, false>(p, stream);
+}
+
+size_t add_norm_bwd_workspace_bytes(int64_t rows, int64_t cols, int ngrads) {
+  return 256 + (size_t)norm_blocks(norm_shape(cols), rows, 1) * (size_t)ngrads * (size_t)cols * sizeof(float);
+}
+
+hipError_t launch_add_norm_bwd(const AddNormBwdParams& p, hipStream_t stream) {
+  if (!p.io_bf16) return bwd_extra<true, true>(p, stream);
+  return p.res_bf16 ? bwd_extra<false, false>(p, stream) : bwd_extra<true, false>(p, stream);
+}
+
+}  // namespace mss

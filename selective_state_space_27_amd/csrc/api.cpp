@@ -723,4 +723,376 @@ mss_status mss_ssd_chunk_bwd(const void* x, const float* delta, const float* A, 
   return hip_status(mss::launch_ssd_bwd(p, static_cast<hipStream_t>(hip_stream)));
 }
 
+// ------------------------------------------------- norms around the mixer
+namespace {
+
+// Rows of a [rows, cols] tensor in memory.
+struct RowSet {
+  const void* p;        // null: absent
+  int64_t stride, cols; // bytes
+  int64_t rows;
+};
+
+RowSet row_set(const void* p, int64_t stride, int64_t rows, int64_t cols, mss_dtype t) {
+  const int64_t es = (int64_t)elem_size(t);
+  return RowSet{p, stride * es, cols * es, rows};
+}
+RowSet dense_set(const void* p, int64_t bytes) { return RowSet{p, bytes, bytes, 1}; }
+
+Range span_of(const RowSet& s) { return range_of(s.p, (size_t)((s.rows - 1) * s.stride + s.cols)); }
+
+// Whether two row sets share a byte: exactly for rows of the same stride
+// (slices of one wider buffer interleave), by their whole spans otherwise.
+bool rows_overlap(const RowSet& a, const RowSet& b) {
+  if (a.p == nullptr || b.p == nullptr || !overlaps(span_of(a), span_of(b))) return false;
+  if (a.rows == 1 || b.rows == 1 || a.stride != b.stride) return true;
+  const int64_t d = (int64_t)(reinterpret_cast<uintptr_t>(b.p) - reinterpret_cast<uintptr_t>(a.p));
+  const int64_t m = ((d % a.stride) + a.stride) % a.stride;  // b's start within a row of a
+  return m < a.cols || a.stride - m < b.cols;
+}
+
+// Every output against every input and the outputs before it.
+bool outputs_clear(const RowSet* outs, int nouts, const RowSet* ins, int nins) {
+  for (int o = 0; o < nouts; ++o) {
+    for (int i = 0; i < nins; ++i)
+      if (rows_overlap(outs[o], ins[i])) return false;
+    for (int i = 0; i < o; ++i)
+      if (rows_overlap(outs[o], outs[i])) return false;
+  }
+  return true;
+}
+
+constexpr int64_t kMaxSpan = 1LL << 47;
+constexpr int64_t kNormCols = 16384;
+
+// Sizes: positive; a stride holds its row; spans that a 64-bit byte offset holds.
+bool rows_ok(int64_t rows, int64_t cols) { return rows > 0 && cols > 0 && cols < (1LL << 30) && rows < kMaxSpan / cols; }
+bool stride_ok(const void* p, int64_t stride, int64_t rows, int64_t cols) {
+  return p == nullptr || (stride >= cols && stride < kMaxSpan / rows);
+}
+
+bool elem_aligned(const void* p, mss_dtype t) { return (reinterpret_cast<uintptr_t>(p) & (elem_size(t) - 1)) == 0; }
+bool f32_aligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+int64_t pitch8(int64_t cols) { return (cols + 31) / 32 * 32; }
+RowSet q_set(const void* q, int64_t rows, int64_t cols) { return dense_set(q, rows * pitch8(cols)); }
+RowSet scale_set(const void* s, int64_t rows, int64_t cols) { return dense_set(s, rows * (pitch8(cols) / 32)); }
+
+// The type pairs that the norm kernels take: the wide tensor at least as wide as the other.
+mss_status norm_types(mss_dtype io, mss_dtype wide) {
+  if (!dtype_ok(io) || !dtype_ok(wide)) return MSS_ERR_DTYPE;
+  return io == MSS_FP32 && wide == MSS_BF16 ? MSS_ERR_UNSUPPORTED : MSS_OK;
+}
+
+bool eps_ok(float eps) { return eps > 0.f && eps < __builtin_inff(); }
+
+}  // namespace
+
+mss_status mss_add_norm_fwd(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
+                            const float* weight, const float* post_weight, const float* gamma, float scale, float eps,
+                            void* out, int64_t out_stride, void* residual_out, int64_t residual_out_stride,
+                            int8_t* out_q, uint8_t* out_scale, int64_t rows, int64_t cols, mss_dtype io_dtype,
+                            mss_dtype res_dtype, uint32_t flags, void* hip_stream) {
+  if (!x || !weight || !out || !residual_out || (out_q == nullptr) != (out_scale == nullptr)) return MSS_ERR_NULL;
+  if (!rows_ok(rows, cols)) return MSS_ERR_SHAPE;
+  mss_status st = norm_types(io_dtype, res_dtype);
+  if (st != MSS_OK) return st;
+  if (!stride_ok(x, x_stride, rows, cols) || !stride_ok(residual, residual_stride, rows, cols) ||
+      !stride_ok(out, out_stride, rows, cols) || !stride_ok(residual_out, residual_out_stride, rows, cols))
+    return MSS_ERR_SHAPE;
+  if (flags != 0 || cols > kNormCols || !eps_ok(eps)) return MSS_ERR_UNSUPPORTED;
+  if (!elem_aligned(x, io_dtype) || !elem_aligned(out, io_dtype) || !elem_aligned(residual, res_dtype) ||
+      !elem_aligned(residual_out, res_dtype) || !f32_aligned(weight) || !f32_aligned(post_weight) ||
+      !f32_aligned(gamma) || !aligned16(out_q))
+    return MSS_ERR_ALIGN;
+  const RowSet ins[] = {row_set(x, x_stride, rows, cols, io_dtype),
+                        row_set(residual, residual_stride, rows, cols, res_dtype), dense_set(weight, cols * 4),
+                        dense_set(post_weight, cols * 4), dense_set(gamma, cols * 4)};
+  const RowSet outs[] = {row_set(out, out_stride, rows, cols, io_dtype),
+                         row_set(residual_out, residual_out_stride, rows, cols, res_dtype), q_set(out_q, rows, cols),
+                         scale_set(out_scale, rows, cols)};
+  if (!outputs_clear(outs, 4, ins, 5)) return MSS_ERR_ALIAS;
+  mss::AddNormFwdParams p;
+  p.x = x;
+  p.residual = residual;
+  p.weight = weight;
+  p.post_weight = post_weight;
+  p.gamma = gamma;
+  p.out = out;
+  p.residual_out = residual_out;
+  p.out_q = out_q;
+  p.out_scale = out_scale;
+  p.x_stride = x_stride;
+  p.residual_stride = residual_stride;
+  p.out_stride = out_stride;
+  p.residual_out_stride = residual_out_stride;
+  p.rows = rows;
+  p.cols = cols;
+  p.scale = scale;
+  p.eps = eps;
+  p.io_bf16 = io_dtype == MSS_BF16;
+  p.res_bf16 = res_dtype == MSS_BF16;
+  return hip_status(mss::launch_add_norm_fwd(p, static_cast<hipStream_t>(hip_stream)));
+}
+
+size_t mss_add_norm_bwd_workspace_size(int64_t rows, int64_t cols, int64_t ngrads) {
+  if (!rows_ok(rows, cols) || cols > kNormCols || ngrads < 1 || ngrads > 3) return 0;
+  return mss::add_norm_bwd_workspace_bytes(rows, cols, (int)ngrads);
+}
+
+mss_status mss_add_norm_bwd(const void* dout, int64_t dout_stride, const void* dresidual_out,
+                            int64_t dresidual_out_stride, const void* r, int64_t r_stride, const uint8_t* r_scale,
+                            const void* x, int64_t x_stride, const uint8_t* x_scale, const float* weight,
+                            const float* post_weight, const float* gamma, float scale, float eps, void* dx,
+                            int64_t dx_stride, void* dresidual, int64_t dresidual_stride, float* dweight,
+                            float* dpost_weight, float* dgamma, int64_t rows, int64_t cols, mss_dtype io_dtype,
+                            mss_dtype res_dtype, uint32_t flags, void* workspace, size_t workspace_bytes,
+                            void* hip_stream) {
+  if (!dout || !r || !weight || !dweight || (post_weight == nullptr) != (dpost_weight == nullptr) ||
+      (gamma == nullptr) != (dgamma == nullptr) || ((post_weight || gamma) && !x))
+    return MSS_ERR_NULL;
+  if (!rows_ok(rows, cols)) return MSS_ERR_SHAPE;
+  mss_status st = norm_types(io_dtype, res_dtype);
+  if (st != MSS_OK) return st;
+  const bool packed = r_scale != nullptr, use_x = post_weight || gamma;
+  if (!use_x) x = nullptr, x_scale = nullptr;
+  if (!stride_ok(dout, dout_stride, rows, cols) || !stride_ok(dresidual_out, dresidual_out_stride, rows, cols) ||
+      (!packed && (!stride_ok(r, r_stride, rows, cols) || !stride_ok(x, x_stride, rows, cols))) ||
+      !stride_ok(dx, dx_stride, rows, cols) || !stride_ok(dresidual, dresidual_stride, rows, cols))
+    return MSS_ERR_SHAPE;
+  if (flags != 0 || cols > kNormCols || !eps_ok(eps) || (use_x && (x_scale != nullptr) != packed))
+    return MSS_ERR_UNSUPPORTED;
+  if (!elem_aligned(dout, io_dtype) || !elem_aligned(dresidual_out, res_dtype) || !elem_aligned(dx, io_dtype) ||
+      !elem_aligned(dresidual, res_dtype) || !f32_aligned(weight) || !f32_aligned(post_weight) || !f32_aligned(gamma) ||
+      !f32_aligned(dweight) || !f32_aligned(dpost_weight) || !f32_aligned(dgamma) ||
+      (packed ? !aligned16(r) || !aligned16(x) : !elem_aligned(r, res_dtype) || !elem_aligned(x, io_dtype)) ||
+      !aligned16(workspace))
+    return MSS_ERR_ALIGN;
+  const int ngrads = 1 + (post_weight != nullptr) + (gamma != nullptr);
+  const size_t need = mss::add_norm_bwd_workspace_bytes(rows, cols, ngrads);
+  if (!workspace || workspace_bytes < need) return MSS_ERR_WORKSPACE;
+  const RowSet ins[] = {row_set(dout, dout_stride, rows, cols, io_dtype),
+                        row_set(dresidual_out, dresidual_out_stride, rows, cols, res_dtype),
+                        packed ? q_set(r, rows, cols) : row_set(r, r_stride, rows, cols, res_dtype),
+                        packed ? q_set(x, rows, cols) : row_set(x, x_stride, rows, cols, io_dtype),
+                        scale_set(r_scale, rows, cols), scale_set(x_scale, rows, cols), dense_set(weight, cols * 4),
+                        dense_set(post_weight, cols * 4), dense_set(gamma, cols * 4),
+                        dense_set(workspace, (int64_t)need)};
+  const RowSet outs[] = {row_set(dx, dx_stride, rows, cols, io_dtype),
+                         row_set(dresidual, dresidual_stride, rows, cols, res_dtype), dense_set(dweight, cols * 4),
+                         dense_set(dpost_weight, cols * 4), dense_set(dgamma, cols * 4)};
+  if (!outputs_clear(outs, 5, ins, 10)) return MSS_ERR_ALIAS;
+  mss::AddNormBwdParams p;
+  p.dout = dout;
+  p.dresidual_out = dresidual_out;
+  p.r = r;
+  p.r_scale = r_scale;
+  p.x = x;
+  p.x_scale = x_scale;
+  p.weight = weight;
+  p.post_weight = post_weight;
+  p.gamma = gamma;
+  p.dx = dx;
+  p.dresidual = dresidual;
+  p.dweight = dweight;
+  p.dpost_weight = dpost_weight;
+  p.dgamma = dgamma;
+  p.dout_stride = dout_stride;
+  p.dresidual_out_stride = dresidual_out_stride;
+  p.r_stride = r_stride;
+  p.x_stride = x_stride;
+  p.dx_stride = dx_stride;
+  p.dresidual_stride = dresidual_stride;
+  p.rows = rows;
+  p.cols = cols;
+  p.scale = scale;
+  p.eps = eps;
+  p.io_bf16 = io_dtype == MSS_BF16;
+  p.res_bf16 = res_dtype == MSS_BF16;
+  p.workspace = workspace;
+  return hip_status(mss::launch_add_norm_bwd(p, static_cast<hipStream_t>(hip_stream)));
+}
+
+// Shape checks that both directions of the gated norm share.
+static mss_status gated_norm_shape(int64_t rows, int64_t cols, int64_t ngroups, mss_dtype y_dtype, mss_dtype io_dtype) {
+  if (!rows_ok(rows, cols) || ngroups <= 0) return MSS_ERR_SHAPE;
+  const mss_status st = norm_types(io_dtype, y_dtype);
+  if (st != MSS_OK) return st;
+  if (ngroups > 65535 || cols % ngroups != 0 || cols / ngroups > kNormCols) return MSS_ERR_UNSUPPORTED;
+  return MSS_OK;
+}
+static bool groups_pack(int64_t cols, int64_t ngroups) { return ngroups == 1 || cols / ngroups % 32 == 0; }
+
+mss_status mss_gated_norm_fwd(const void* y, int64_t y_stride, const void* z, int64_t z_stride, const float* weight,
+                              float eps, void* out, int64_t out_stride, int8_t* y_q, uint8_t* y_scale, int8_t* z_q,
+                              uint8_t* z_scale, int8_t* out_q, uint8_t* out_scale, int64_t rows, int64_t cols,
+                              int64_t ngroups, mss_dtype y_dtype, mss_dtype io_dtype, uint32_t flags,
+                              void* hip_stream) {
+  const bool keep = y_q != nullptr;
+  if (!y || !weight || !out || keep != (y_scale != nullptr) || (out_q == nullptr) != (out_scale == nullptr) ||
+      (z_q != nullptr) != (keep && z) || (z_scale != nullptr) != (keep && z))
+    return MSS_ERR_NULL;
+  mss_status st = gated_norm_shape(rows, cols, ngroups, y_dtype, io_dtype);
+  if (st != MSS_OK) return st;
+  if (!stride_ok(y, y_stride, rows, cols) || !stride_ok(z, z_stride, rows, cols) ||
+      !stride_ok(out, out_stride, rows, cols))
+    return MSS_ERR_SHAPE;
+  if ((flags & ~MSS_FLAG_NORM_FIRST) || !eps_ok(eps) || ((keep || out_q) && !groups_pack(cols, ngroups)))
+    return MSS_ERR_UNSUPPORTED;
+  if (!elem_aligned(y, y_dtype) || !elem_aligned(z, io_dtype) || !elem_aligned(out, io_dtype) || !f32_aligned(weight) ||
+      !aligned16(y_q) || !aligned16(z_q) || !aligned16(out_q))
+    return MSS_ERR_ALIGN;
+  const RowSet ins[] = {row_set(y, y_stride, rows, cols, y_dtype), row_set(z, z_stride, rows, cols, io_dtype),
+                        dense_set(weight, cols * 4)};
+  const RowSet outs[] = {row_set(out, out_stride, rows, cols, io_dtype), q_set(y_q, rows, cols),
+                         scale_set(y_scale, rows, cols), q_set(z_q, rows, cols), scale_set(z_scale, rows, cols),
+                         q_set(out_q, rows, cols), scale_set(out_scale, rows, cols)};
+  if (!outputs_clear(outs, 7, ins, 3)) return MSS_ERR_ALIAS;
+  mss::GatedNormFwdParams p;
+  p.y = y;
+  p.z = z;
+  p.weight = weight;
+  p.out = out;
+  p.y_q = y_q;
+  p.y_scale = y_scale;
+  p.z_q = z_q;
+  p.z_scale = z_scale;
+  p.out_q = out_q;
+  p.out_scale = out_scale;
+  p.y_stride = y_stride;
+  p.z_stride = z_stride;
+  p.out_stride = out_stride;
+  p.rows = rows;
+  p.cols = cols;
+  p.ngroups = ngroups;
+  p.eps = eps;
+  p.y_bf16 = y_dtype == MSS_BF16;
+  p.io_bf16 = io_dtype == MSS_BF16;
+  p.norm_first = (flags & MSS_FLAG_NORM_FIRST) != 0;
+  return hip_status(mss::launch_gated_norm_fwd(p, static_cast<hipStream_t>(hip_stream)));
+}
+
+size_t mss_gated_norm_bwd_workspace_size(int64_t rows, int64_t cols, int64_t ngroups) {
+  if (gated_norm_shape(rows, cols, ngroups, MSS_FP32, MSS_FP32) != MSS_OK) return 0;
+  return mss::gated_norm_bwd_workspace_bytes(rows, cols, ngroups);
+}
+
+mss_status mss_gated_norm_bwd(const void* dout, int64_t dout_stride, const void* y, int64_t y_stride,
+                              const uint8_t* y_scale, const void* z, int64_t z_stride, const uint8_t* z_scale,
+                              const float* weight, float eps, void* dy, int64_t dy_stride, void* dz, int64_t dz_stride,
+                              float* dweight, int64_t rows, int64_t cols, int64_t ngroups, mss_dtype y_dtype,
+                              mss_dtype io_dtype, uint32_t flags, void* workspace, size_t workspace_bytes,
+                              void* hip_stream) {
+  if (!dout || !y || !weight || !dy || !dweight || (z == nullptr) != (dz == nullptr)) return MSS_ERR_NULL;
+  mss_status st = gated_norm_shape(rows, cols, ngroups, y_dtype, io_dtype);
+  if (st != MSS_OK) return st;
+  const bool packed = y_scale != nullptr;
+  if (!stride_ok(dout, dout_stride, rows, cols) || !stride_ok(dy, dy_stride, rows, cols) ||
+      !stride_ok(dz, dz_stride, rows, cols) ||
+      (!packed && (!stride_ok(y, y_stride, rows, cols) || !stride_ok(z, z_stride, rows, cols))))
+    return MSS_ERR_SHAPE;
+  if ((flags & ~MSS_FLAG_NORM_FIRST) || !eps_ok(eps) || (z_scale != nullptr) != (packed && z) ||
+      (packed && !groups_pack(cols, ngroups)))
+    return MSS_ERR_UNSUPPORTED;
+  if (!elem_aligned(dout, io_dtype) || !elem_aligned(dy, y_dtype) || !elem_aligned(dz, io_dtype) ||
+      !f32_aligned(weight) || !f32_aligned(dweight) ||
+      (packed ? !aligned16(y) || !aligned16(z) : !elem_aligned(y, y_dtype) || !elem_aligned(z, io_dtype)) ||
+      !aligned16(workspace))
+    return MSS_ERR_ALIGN;
+  const size_t need = mss::gated_norm_bwd_workspace_bytes(rows, cols, ngroups);
+  if (!workspace || workspace_bytes < need) return MSS_ERR_WORKSPACE;
+  const RowSet ins[] = {row_set(dout, dout_stride, rows, cols, io_dtype),
+                        packed ? q_set(y, rows, cols) : row_set(y, y_stride, rows, cols, y_dtype),
+                        packed ? q_set(z, rows, cols) : row_set(z, z_stride, rows, cols, io_dtype),
+                        scale_set(y_scale, rows, cols), scale_set(z_scale, rows, cols), dense_set(weight, cols * 4),
+                        dense_set(workspace, (int64_t)need)};
+  const RowSet outs[] = {row_set(dy, dy_stride, rows, cols, y_dtype), row_set(dz, dz_stride, rows, cols, io_dtype),
+                         dense_set(dweight, cols * 4)};
+  if (!outputs_clear(outs, 3, ins, 7)) return MSS_ERR_ALIAS;
+  mss::GatedNormBwdParams p;
+  p.dout = dout;
+  p.y = y;
+  p.y_scale = y_scale;
+  p.z = z;
+  p.z_scale = z_scale;
+  p.weight = weight;
+  p.dy = dy;
+  p.dz = dz;
+  p.dweight = dweight;
+  p.dout_stride = dout_stride;
+  p.y_stride = y_stride;
+  p.z_stride = z_stride;
+  p.dy_stride = dy_stride;
+  p.dz_stride = dz_stride;
+  p.rows = rows;
+  p.cols = cols;
+  p.ngroups = ngroups;
+  p.eps = eps;
+  p.y_bf16 = y_dtype == MSS_BF16;
+  p.io_bf16 = io_dtype == MSS_BF16;
+  p.norm_first = (flags & MSS_FLAG_NORM_FIRST) != 0;
+  p.workspace = workspace;
+  return hip_status(mss::launch_gated_norm_bwd(p, static_cast<hipStream_t>(hip_stream)));
+}
+
+// ------------------------------------------------- 8-bit checkpoints
+static mss_status ckpt8_check(const void* x, int64_t x_stride, const void* q, const void* scale, int64_t rows,
+                              int64_t cols, mss_dtype dtype, bool pack) {
+  if (!x || !q || !scale) return MSS_ERR_NULL;
+  if (!rows_ok(rows, cols)) return MSS_ERR_SHAPE;
+  if (!dtype_ok(dtype)) return MSS_ERR_DTYPE;
+  // A launch holds fewer than 2^32 threads, each of four vectors of eight.
+  if (!stride_ok(x, x_stride, rows, cols) || rows >= (1LL << 36) / pitch8(cols)) return MSS_ERR_SHAPE;
+  if (!elem_aligned(x, dtype) || !aligned16(q)) return MSS_ERR_ALIGN;
+  const RowSet a[] = {row_set(x, x_stride, rows, cols, dtype)};
+  const RowSet b[] = {q_set(q, rows, cols), scale_set(scale, rows, cols)};
+  if (pack ? !outputs_clear(b, 2, a, 1) : !outputs_clear(a, 1, b, 2)) return MSS_ERR_ALIAS;
+  return MSS_OK;
+}
+
+mss_status mss_pack8(const void* x, int64_t x_stride, int8_t* q, uint8_t* scale, int64_t rows, int64_t cols,
+                     mss_dtype dtype, void* hip_stream) {
+  const mss_status st = ckpt8_check(x, x_stride, q, scale, rows, cols, dtype, true);
+  if (st != MSS_OK) return st;
+  const mss::Ckpt8Params p{x, nullptr, q, scale, x_stride, rows, cols, dtype == MSS_BF16};
+  return hip_status(mss::launch_pack8(p, static_cast<hipStream_t>(hip_stream)));
+}
+
+mss_status mss_unpack8(const int8_t* q, const uint8_t* scale, void* x, int64_t x_stride, int64_t rows, int64_t cols,
+                       mss_dtype dtype, void* hip_stream) {
+  const mss_status st = ckpt8_check(x, x_stride, q, scale, rows, cols, dtype, false);
+  if (st != MSS_OK) return st;
+  const mss::Ckpt8Params p{nullptr, x, const_cast<int8_t*>(q), const_cast<uint8_t*>(scale), x_stride, rows, cols,
+                           dtype == MSS_BF16};
+  return hip_status(mss::launch_unpack8(p, static_cast<hipStream_t>(hip_stream)));
+}
+
+static bool wgrad8_shape_ok(int64_t tokens, int64_t outs, int64_t ins) {
+  return tokens > 0 && outs > 0 && ins > 0 && tokens <= (1LL << 36) && outs <= (1LL << 20) && ins <= (1LL << 20) &&
+         outs * ins <= (1LL << 34);
+}
+
+size_t mss_wgrad8_workspace_size(int64_t tokens, int64_t outs, int64_t ins) {
+  return wgrad8_shape_ok(tokens, outs, ins) ? mss::wgrad8_workspace_bytes(tokens, outs, ins) : 0;
+}
+
+mss_status mss_wgrad8(const void* dy, int64_t dy_stride, const int8_t* q, const uint8_t* scale, void* dw,
+                      int64_t tokens, int64_t outs, int64_t ins, mss_dtype dy_dtype, mss_dtype dw_dtype,
+                      uint32_t flags, void* workspace, size_t workspace_bytes, void* hip_stream) {
+  if (!dy || !q || !scale || !dw) return MSS_ERR_NULL;
+  if (!dtype_ok(dy_dtype) || !dtype_ok(dw_dtype)) return MSS_ERR_DTYPE;
+  if (!wgrad8_shape_ok(tokens, outs, ins) || !stride_ok(dy, dy_stride, tokens, outs)) return MSS_ERR_SHAPE;
+  if (dy_dtype != MSS_BF16 || (flags & ~MSS_FLAG_ACCUMULATE)) return MSS_ERR_UNSUPPORTED;
+  if (!elem_aligned(dy, dy_dtype) || !aligned16(q) || !aligned16(dw) || !aligned16(workspace)) return MSS_ERR_ALIGN;
+  const size_t need = mss::wgrad8_workspace_bytes(tokens, outs, ins);
+  if (!workspace || workspace_bytes < need) return MSS_ERR_WORKSPACE;
+  const RowSet in[] = {row_set(dy, dy_stride, tokens, outs, dy_dtype), q_set(q, tokens, ins),
+                       scale_set(scale, tokens, ins), dense_set(workspace, (int64_t)need)};
+  const RowSet out[] = {dense_set(dw, outs * ins * (int64_t)elem_size(dw_dtype))};
+  if (!outputs_clear(out, 1, in, 4)) return MSS_ERR_ALIAS;
+  const mss::Wgrad8Params p{dy,   q,    scale, dw, dy_stride, tokens, outs, ins, dw_dtype == MSS_BF16,
+                            (flags & MSS_FLAG_ACCUMULATE) != 0, workspace};
+  return hip_status(mss::launch_wgrad8(p, static_cast<hipStream_t>(hip_stream)));
+}
+
 }  // extern "C"

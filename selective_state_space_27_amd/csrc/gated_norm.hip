@@ -1,0 +1,281 @@
+// Norm after a mixer, fused with its gate (gfx950): forward and backward.
+//
+// Per row and group of columns, with RMS(v) = v rstd(v), rstd(v) = 1 /
+// sqrt(mean(v^2) + eps) over the group, s(z) = z sigma(z), s'(z) = sigma(z)
+// (1 + z (1 - sigma(z))):
+//   gate first:  v = y s(z);  out = RMS(v) w      (no z: v = y)
+//   norm first:  out = RMS(y) w s(z)
+// Backward, g the gradient of the normed values times w:
+//   gate first:  g = dout w;  dv = rstd g - v rstd^3 mean(g v);
+//                dy = dv s(z);  dz = dv y s'(z);  dw = sum_rows dout v rstd
+//   norm first:  g = dout w s(z);  dy = rstd g - y rstd^3 mean(g y);
+//                dz = dout w y rstd s'(z);  dw = sum_rows dout s(z) y rstd
+// rstd is formed again in the backward, in the same reduction as mean(g v).
+//
+// Every element is read once and written once: both directions are bound by
+// HBM.  Rows are laid over lanes as norm_common.hpp describes; a group of
+// columns has its own workgroups (grid y).
+#include <type_traits>
+
+#include "norm_common.hpp"
+
+namespace mss {
+namespace {
+
+enum : int { kNoGate = 0, kGateFirst = 1, kNormFirst = 2 };
+
+// sigma(z); the limits come out right (exp2 overflows to inf, 1 / inf = 0).
+__device__ __forceinline__ float sigmoid(float z) { return rcp_fast(1.0f + exp2_fast(-z * kLog2e)); }
+
+struct FwdArgs {
+  GatedNormFwdParams p;
+  int pitch;  // of the 8-bit forms
+  int gcols;  // columns of a group
+};
+
+template <bool Y32, bool IO32, int MODE, int LANES, int K>
+__global__ void __launch_bounds__(LANES ? 256 : 1024) gated_norm_fwd_kernel(FwdArgs a) {
+  constexpr int SY = Y32 ? kSrcF32 : kSrcBf16, SZ = IO32 ? kSrcF32 : kSrcBf16;
+  __shared__ float lds[LANES ? 1 : kRowSumFloats];
+  int half = 0;
+  const Place<LANES> at;
+  const int c0 = (int)blockIdx.y * a.gcols;
+  const float inv = 1.0f / (float)a.gcols;
+  int col[K], n[K];
+  float w[K][8];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    col[k] = c0 + at.col(k);
+    n[k] = a.gcols - at.col(k);
+    load_w(a.p.weight, col[k], n[k], w[k]);
+  }
+  const int64_t step = (int64_t)gridDim.x * at.nseg;
+  int64_t row = (int64_t)blockIdx.x * at.nseg + at.seg;
+  Raw<SY> ny[K];
+  Raw<SZ> nz[MODE != kNoGate ? K : 1];
+  auto fetch = [&](int64_t i) {
+    const char* yr = static_cast<const char*>(a.p.y) + i * a.p.y_stride * (Y32 ? 4 : 2);
+    const char* zr = static_cast<const char*>(a.p.z) + i * a.p.z_stride * (IO32 ? 4 : 2);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      ny[k] = load_raw<SY>(yr, nullptr, col[k], n[k]);
+      if constexpr (MODE != kNoGate) nz[k] = load_raw<SZ>(zr, nullptr, col[k], n[k]);
+    }
+  };
+  if (row < a.p.rows) fetch(row);
+  for (; row < a.p.rows; row += step) {
+    float y[K][8], z[K][8];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      widen<SY>(ny[k], y[k]);
+      if constexpr (MODE != kNoGate) widen<SZ>(nz[k], z[k]);
+    }
+    if (row + step < a.p.rows) fetch(row + step);
+    const int64_t prow = row * a.pitch, srow = row * (a.pitch >> 5);
+    if (a.p.y_q != nullptr) {
+      const int pend = a.p.ngroups == 1 ? a.pitch : c0 + a.gcols;
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        store_p8(a.p.y_q + prow, a.p.y_scale + srow, col[k], pend, y[k]);
+        if constexpr (MODE != kNoGate) store_p8(a.p.z_q + prow, a.p.z_scale + srow, col[k], pend, z[k]);
+      }
+    }
+    float sum[1] = {};
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if constexpr (MODE == kGateFirst) y[k][j] *= z[k][j] * sigmoid(z[k][j]);
+        sum[0] = __builtin_fmaf(y[k][j], y[k][j], sum[0]);
+      }
+    row_sums<LANES>(sum, lds, half);
+    const float rstd = rsqrtf(__builtin_fmaf(sum[0], inv, a.p.eps));
+    char* out = static_cast<char*>(a.p.out) + row * a.p.out_stride * (IO32 ? 4 : 2);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      float o[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        o[j] = y[k][j] * rstd * w[k][j];
+        if constexpr (MODE == kNormFirst) o[j] *= z[k][j] * sigmoid(z[k][j]);
+      }
+      if (n[k] > 0) store8<IO32>(out, col[k], n[k], o);
+      if (a.p.out_q != nullptr) {
+        as_stored<IO32>(o);  // the form of the output as it is stored
+        store_p8(a.p.out_q + prow, a.p.out_scale + srow, col[k], a.p.ngroups == 1 ? a.pitch : c0 + a.gcols, o);
+      }
+    }
+  }
+}
+
+struct BwdArgs {
+  GatedNormBwdParams p;
+  float* part;  // [blocks][cols]
+  int pitch;
+  int gcols;
+  int* status;
+};
+
+template <bool Y32, bool IO32, bool PACKED, int MODE, int LANES, int K>
+__global__ void __launch_bounds__(LANES ? 256 : 1024) gated_norm_bwd_kernel(BwdArgs a) {
+  constexpr int SO = IO32 ? kSrcF32 : kSrcBf16;
+  constexpr int SY = PACKED ? kSrcP8 : Y32 ? kSrcF32 : kSrcBf16, SZ = PACKED ? kSrcP8 : SO;
+  __shared__ float lds[LANES ? kPartialLds : kRowSumFloats];
+  int half = 0;
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *a.status = 0;
+  const Place<LANES> at;
+  const int c0 = (int)blockIdx.y * a.gcols;
+  const float inv = 1.0f / (float)a.gcols;
+  int col[K], n[K];
+  float w[K][8], dw[K][8] = {};
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    col[k] = c0 + at.col(k);
+    n[k] = a.gcols - at.col(k);
+    load_w(a.p.weight, col[k], n[k], w[k]);
+  }
+  const int64_t step = (int64_t)gridDim.x * at.nseg;
+  int64_t row = (int64_t)blockIdx.x * at.nseg + at.seg;
+  Raw<SO> nd[K];
+  Raw<SY> ny[K];
+  Raw<SZ> nz[MODE != kNoGate ? K : 1];
+  auto fetch = [&](int64_t i) {
+    const char* dr = static_cast<const char*>(a.p.dout) + i * a.p.dout_stride * (IO32 ? 4 : 2);
+    const char* yr = static_cast<const char*>(a.p.y) + i * (PACKED ? a.pitch : a.p.y_stride * (Y32 ? 4 : 2));
+    const char* zr = static_cast<const char*>(a.p.z) + i * (PACKED ? a.pitch : a.p.z_stride * (IO32 ? 4 : 2));
+    const uint8_t* ys = PACKED ? a.p.y_scale + i * (a.pitch >> 5) : nullptr;
+    const uint8_t* zs = PACKED ? a.p.z_scale + i * (a.pitch >> 5) : nullptr;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      nd[k] = load_raw<SO>(dr, nullptr, col[k], n[k]);
+      ny[k] = load_raw<SY>(yr, ys, col[k], n[k]);
+      if constexpr (MODE != kNoGate) nz[k] = load_raw<SZ>(zr, zs, col[k], n[k]);
+    }
+  };
+  if (row < a.p.rows) fetch(row);
+  for (; row < a.p.rows; row += step) {
+    float d[K][8], y[K][8], z[K][8];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      widen<SO>(nd[k], d[k]), widen<SY>(ny[k], y[k]);
+      if constexpr (MODE != kNoGate) widen<SZ>(nz[k], z[k]);
+    }
+    if (row + step < a.p.rows) fetch(row + step);
+    float sum[2] = {};
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        float g = d[k][j] * w[k][j], v = y[k][j];
+        if constexpr (MODE != kNoGate) {
+          const float s = z[k][j] * sigmoid(z[k][j]);
+          if constexpr (MODE == kGateFirst) v *= s;
+          else g *= s;
+        }
+        sum[0] = __builtin_fmaf(v, v, sum[0]);
+        sum[1] = __builtin_fmaf(g, v, sum[1]);
+      }
+    row_sums<LANES>(sum, lds, half);
+    const float rstd = rsqrtf(__builtin_fmaf(sum[0], inv, a.p.eps));
+    const float c1 = rstd * rstd * rstd * (sum[1] * inv);
+    char* dyr = static_cast<char*>(a.p.dy) + row * a.p.dy_stride * (Y32 ? 4 : 2);
+    char* dzr = static_cast<char*>(a.p.dz) + row * a.p.dz_stride * (IO32 ? 4 : 2);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      float dy[8], dz[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float g = d[k][j] * w[k][j];
+        if constexpr (MODE == kNoGate) {
+          dy[j] = rstd * g - y[k][j] * c1;
+          dw[k][j] = __builtin_fmaf(d[k][j], y[k][j] * rstd, dw[k][j]);
+        } else {
+          const float sg = sigmoid(z[k][j]), s = z[k][j] * sg;
+          const float ds = __builtin_fmaf(s, 1.0f - sg, sg);  // sigma (1 + z (1 - sigma))
+          if constexpr (MODE == kGateFirst) {
+            const float v = y[k][j] * s, dv = rstd * g - v * c1;
+            dw[k][j] = __builtin_fmaf(d[k][j], v * rstd, dw[k][j]);
+            dy[j] = dv * s;
+            dz[j] = dv * y[k][j] * ds;
+          } else {
+            const float nh = y[k][j] * rstd;
+            dw[k][j] = __builtin_fmaf(d[k][j], nh * s, dw[k][j]);
+            dy[j] = rstd * (g * s) - y[k][j] * c1;
+            dz[j] = g * nh * ds;
+          }
+        }
+      }
+      if (n[k] > 0) {
+        store8<Y32>(dyr, col[k], n[k], dy);
+        if constexpr (MODE != kNoGate) store8<IO32>(dzr, col[k], n[k], dz);
+      }
+    }
+  }
+  float* part = a.part + (int64_t)blockIdx.x * a.p.cols + c0;
+#pragma unroll
+  for (int k = 0; k < K; ++k) store_partial<LANES>(part, at.col(k), n[k], dw[k], lds);
+}
+
+template <bool Y32, bool IO32, int MODE>
+hipError_t fwd_mode(const GatedNormFwdParams& p, hipStream_t stream) {
+  const int64_t gcols = p.cols / p.ngroups;
+  const NormShape s = norm_shape(gcols);
+  const dim3 grid((unsigned)norm_blocks(s, p.rows, p.ngroups), (unsigned)p.ngroups), block((unsigned)s.threads);
+  const FwdArgs a{p, (int)((p.cols + 31) / 32 * 32), (int)gcols};
+  return with_shape(s, [&](auto lanes, auto k) {
+    hipLaunchKernelGGL((gated_norm_fwd_kernel<Y32, IO32, MODE, lanes.value, k.value>), grid, block, 0, stream, a);
+    return hipGetLastError();
+  });
+}
+
+template <bool Y32, bool IO32>
+hipError_t fwd_typed(const GatedNormFwdParams& p, hipStream_t stream) {
+  if (p.z == nullptr) return fwd_mode<Y32, IO32, kNoGate>(p, stream);
+  return p.norm_first ? fwd_mode<Y32, IO32, kNormFirst>(p, stream) : fwd_mode<Y32, IO32, kGateFirst>(p, stream);
+}
+
+template <bool Y32, bool IO32, bool PACKED, int MODE>
+hipError_t bwd_mode(const GatedNormBwdParams& p, hipStream_t stream) {
+  const int64_t gcols = p.cols / p.ngroups;
+  const NormShape s = norm_shape(gcols);
+  const int64_t blocks = norm_blocks(s, p.rows, p.ngroups);
+  const BwdArgs a{p, reinterpret_cast<float*>(static_cast<char*>(p.workspace) + 256), (int)((p.cols + 31) / 32 * 32),
+                  (int)gcols, static_cast<int*>(p.workspace)};
+  const hipError_t e = with_shape(s, [&](auto lanes, auto k) {
+    hipLaunchKernelGGL((gated_norm_bwd_kernel<Y32, IO32, PACKED, MODE, lanes.value, k.value>),
+                       dim3((unsigned)blocks, (unsigned)p.ngroups), dim3((unsigned)s.threads), 0, stream, a);
+    return hipGetLastError();
+  });
+  if (e != hipSuccess) return e;
+  return launch_sum_partials(SumPartialsArgs{a.part, {p.dweight, nullptr, nullptr}, blocks, p.cols, 1}, stream);
+}
+
+template <bool Y32, bool IO32, bool PACKED>
+hipError_t bwd_gate(const GatedNormBwdParams& p, hipStream_t stream) {
+  if (p.z == nullptr) return bwd_mode<Y32, IO32, PACKED, kNoGate>(p, stream);
+  return p.norm_first ? bwd_mode<Y32, IO32, PACKED, kNormFirst>(p, stream)
+                      : bwd_mode<Y32, IO32, PACKED, kGateFirst>(p, stream);
+}
+
+template <bool Y32, bool IO32>
+hipError_t bwd_typed(const GatedNormBwdParams& p, hipStream_t stream) {
+  return p.y_scale != nullptr ? bwd_gate<Y32, IO32, true>(p, stream) : bwd_gate<Y32, IO32, false>(p, stream);
+}
+
+}  // namespace
+
+hipError_t launch_gated_norm_fwd(const GatedNormFwdParams& p, hipStream_t stream) {
+  if (!p.io_bf16) return fwd_typed<true, true>(p, stream);
+  return p.y_bf16 ? fwd_typed<false, false>(p, stream) : fwd_typed<true, false>(p, stream);
+}
+
+size_t gated_norm_bwd_workspace_bytes(int64_t rows, int64_t cols, int64_t ngroups) {
+  return 256 + (size_t)norm_blocks(norm_shape(cols / ngroups), rows, ngroups) * (size_t)cols * sizeof(float);
+}
+
+hipError_t launch_gated_norm_bwd(const GatedNormBwdParams& p, hipStream_t stream) {
+  if (!p.io_bf16) return bwd_typed<true, true>(p, stream);
+  return p.y_bf16 ? bwd_typed<false, false>(p, stream) : bwd_typed<true, false>(p, stream);
+}
+
+}  // namespace mss

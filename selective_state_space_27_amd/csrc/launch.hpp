@@ -195,4 +195,115 @@ size_t ssd_bwd_halves_workspace_bytes(int64_t batch, int64_t seqlen, int64_t nhe
                                       int64_t ngroups);
 hipError_t launch_ssd_bwd_halves(const SSDBwdParams& p, hipStream_t stream);
 
+// Norm before a block with its residual (add_norm.hip).  Strides are of rows,
+// in elements.
+struct AddNormFwdParams {
+  const void* x;
+  const void* residual;       // nullable
+  const float* weight;
+  const float* post_weight;   // nullable
+  const float* gamma;         // nullable
+  void* out;
+  void* residual_out;
+  int8_t* out_q;              // nullable, with out_scale
+  uint8_t* out_scale;
+  int64_t x_stride, residual_stride, out_stride, residual_out_stride;
+  int64_t rows, cols;
+  float scale, eps;
+  bool io_bf16, res_bf16;     // x, out; residual, residual_out
+};
+hipError_t launch_add_norm_fwd(const AddNormFwdParams& p, hipStream_t stream);
+
+struct AddNormBwdParams {
+  const void* dout;
+  const void* dresidual_out;  // nullable
+  const void* r;              // the stored residual, or its q
+  const uint8_t* r_scale;     // nullable
+  const void* x;              // null when neither post_weight nor gamma is given
+  const uint8_t* x_scale;     // given when r_scale and x are
+  const float* weight;
+  const float* post_weight;   // nullable
+  const float* gamma;         // nullable
+  void* dx;                   // nullable
+  void* dresidual;            // nullable
+  float* dweight;
+  float* dpost_weight;        // exactly when post_weight
+  float* dgamma;              // exactly when gamma
+  int64_t dout_stride, dresidual_out_stride, r_stride, x_stride, dx_stride, dresidual_stride;
+  int64_t rows, cols;
+  float scale, eps;
+  bool io_bf16, res_bf16;
+  void* workspace;
+};
+size_t add_norm_bwd_workspace_bytes(int64_t rows, int64_t cols, int ngrads);
+hipError_t launch_add_norm_bwd(const AddNormBwdParams& p, hipStream_t stream);
+
+// Norm after a mixer with its gate (gated_norm.hip).
+struct GatedNormFwdParams {
+  const void* y;
+  const void* z;              // nullable
+  const float* weight;
+  void* out;
+  int8_t* y_q;                // nullable; with y_scale, and with z_q and z_scale exactly when z
+  uint8_t* y_scale;
+  int8_t* z_q;
+  uint8_t* z_scale;
+  int8_t* out_q;              // nullable, with out_scale
+  uint8_t* out_scale;
+  int64_t y_stride, z_stride, out_stride;
+  int64_t rows, cols, ngroups;
+  float eps;
+  bool y_bf16, io_bf16;       // y; z and out
+  bool norm_first;
+};
+hipError_t launch_gated_norm_fwd(const GatedNormFwdParams& p, hipStream_t stream);
+
+struct GatedNormBwdParams {
+  const void* dout;
+  const void* y;              // or its q
+  const uint8_t* y_scale;     // nullable
+  const void* z;              // nullable; or its q
+  const uint8_t* z_scale;     // given when y_scale and z are
+  const float* weight;
+  void* dy;
+  void* dz;                   // exactly when z
+  float* dweight;
+  int64_t dout_stride, y_stride, z_stride, dy_stride, dz_stride;
+  int64_t rows, cols, ngroups;
+  float eps;
+  bool y_bf16, io_bf16;       // dy (and y); dout, dz (and z)
+  bool norm_first;
+  void* workspace;
+};
+size_t gated_norm_bwd_workspace_bytes(int64_t rows, int64_t cols, int64_t ngroups);
+hipError_t launch_gated_norm_bwd(const GatedNormBwdParams& p, hipStream_t stream);
+
+// 8-bit checkpoints (ckpt8.hip): src -> q, scale; or q, scale -> dst.
+struct Ckpt8Params {
+  const void* src;
+  void* dst;
+  int8_t* q;
+  uint8_t* scale;
+  int64_t stride;             // of src's or dst's rows
+  int64_t rows, cols;
+  bool bf16;
+};
+hipError_t launch_pack8(const Ckpt8Params& p, hipStream_t stream);
+hipError_t launch_unpack8(const Ckpt8Params& p, hipStream_t stream);
+
+// Weight gradient from an 8-bit checkpoint (wgrad8.hip).
+struct Wgrad8Params {
+  const void* dy;             // bf16 [tokens, outs]
+  const int8_t* q;            // [tokens, pitch]
+  const uint8_t* scale;       // [tokens, pitch / 32]
+  void* dw;                   // [outs, ins]
+  int64_t dy_stride;
+  int64_t tokens, outs, ins;
+  bool dw_bf16;
+  bool accumulate;
+  void* workspace;
+};
+size_t wgrad8_workspace_bytes(int64_t tokens, int64_t outs, int64_t ins);
+hipError_t launch_wgrad8(const Wgrad8Params& p, hipStream_t stream);
+
 }  // namespace mss

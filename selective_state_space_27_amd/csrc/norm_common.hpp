@@ -1,0 +1,113 @@
+// Shape of the norm kernels (add_norm.hip, gated_norm.hip): how rows are laid
+// over lanes, and the sums over rows for the weights' gradients.
+//
+// A "segment" is what one norm runs over: a row, or one group of a row's
+// columns.  Segments of up to 512 columns take 16, 32 or 64 lanes of a wave
+// (LANES; a workgroup of 256 threads holds 256 / LANES of them, the sums need
+// no barrier); longer ones take a workgroup (LANES = 0) of just enough waves
+// for eight columns per thread, or for sixteen (K = 2) past kOneVectorMax
+// columns.  Workgroups walk over rows with a stride, the next row's loads
+// issued before the present one's sums, and keep the weights (and the
+// gradients' partial sums over rows) in registers.
+#pragma once
+
+#include "launch.hpp"
+#include "rows.hpp"
+
+namespace mss {
+
+constexpr int kNormCUs = 256;
+constexpr int kOneVectorMax = 8192;   // columns of a segment with one vector per thread
+constexpr int kNormColsMax = 16384;   // columns of a segment at most (1024 threads x 2 vectors)
+
+// Segment layout of a launch.
+struct NormShape {
+  int lanes;    // 16, 32, 64, or 0 (workgroup)
+  int k;        // vectors of 8 columns per thread
+  int threads;  // of a workgroup
+  int segs;     // segments a workgroup holds at a time
+};
+
+inline NormShape norm_shape(int64_t cols) {
+  if (cols <= 128) return {16, 1, 256, 16};
+  if (cols <= 256) return {32, 1, 256, 8};
+  if (cols <= 512) return {64, 1, 256, 4};
+  const int k = cols <= kOneVectorMax ? 1 : 2;
+  const int threads = (int)((cols + 8 * k - 1) / (8 * k) + 63) / 64 * 64;
+  return {0, k, threads, 1};
+}
+
+// Workgroups per group of columns: every slot of the card (2048 threads per
+// CU) taken once, and no more than there are rows.
+inline int64_t norm_blocks(const NormShape& s, int64_t rows, int64_t groups) {
+  const int64_t slots = (int64_t)kNormCUs * (2048 / s.threads);
+  const int64_t want = slots / groups > 0 ? slots / groups : 1;
+  const int64_t most = (rows + s.segs - 1) / s.segs;
+  return want < most ? want : most;
+}
+
+// Calls f(std::integral_constant<int, LANES>, <int, K>) for the shape.
+template <typename F>
+inline hipError_t with_shape(const NormShape& s, F&& f) {
+  if (s.lanes == 16) return f(std::integral_constant<int, 16>{}, std::integral_constant<int, 1>{});
+  if (s.lanes == 32) return f(std::integral_constant<int, 32>{}, std::integral_constant<int, 1>{});
+  if (s.lanes == 64) return f(std::integral_constant<int, 64>{}, std::integral_constant<int, 1>{});
+  if (s.k == 1) return f(std::integral_constant<int, 0>{}, std::integral_constant<int, 1>{});
+  return f(std::integral_constant<int, 0>{}, std::integral_constant<int, 2>{});
+}
+
+// Where a thread is: which of the workgroup's segments, its first column, and
+// the column its k-th vector starts at.
+template <int LANES>
+struct Place {
+  int seg;   // segment of the workgroup
+  int nseg;  // segments of the workgroup
+  __device__ __forceinline__ Place() {
+    if constexpr (LANES == 0) seg = 0, nseg = 1;
+    else seg = (int)threadIdx.x / LANES, nseg = 256 / LANES;
+  }
+  __device__ __forceinline__ int col(int k) const {
+    if constexpr (LANES == 0) return (k * (int)blockDim.x + (int)threadIdx.x) * 8;
+    else return ((int)threadIdx.x % LANES) * 8;
+  }
+};
+
+// Eight weights (fp32, any alignment of 4), zeros past the end.
+__device__ __forceinline__ void load_w(const float* w, int col, int n, float (&v)[8]) {
+  widen<kSrcF32>(load_raw<kSrcF32>(w, nullptr, col, n), v);
+}
+
+// A workgroup's sums over its rows, `part[col]`: the sums of its segments (the
+// same columns, different rows) meet in LDS, in a fixed order.
+template <int LANES>
+__device__ __forceinline__ void store_partial(float* part, int col, int n, const float (&acc)[8], float* lds) {
+  if constexpr (LANES == 0) {
+    if (n > 0) store8<true>(part, col, n, acc);
+  } else {
+    __syncthreads();  // before: `lds` may still be read from the last call
+#pragma unroll
+    for (int j = 0; j < 8; ++j) lds[threadIdx.x * 8 + j] = acc[j];
+    __syncthreads();
+    constexpr int W = LANES * 8;  // columns a segment's lanes cover
+    const int ncols = col + n;    // the segment's columns (the same for every thread)
+    for (int c = threadIdx.x; c < W; c += 256) {
+      float s = 0.f;
+#pragma unroll
+      for (int g = 0; g < 256 / LANES; ++g) s += lds[g * W + c];
+      if (c < ncols) part[c] = s;
+    }
+  }
+}
+constexpr int kPartialLds = 256 * 8;
+
+// Sums of `nparts` partial rows: out[p][col] over [nparts][nout][cols].
+struct SumPartialsArgs {
+  const float* part;
+  float* out[3];
+  int64_t nparts;
+  int64_t cols;
+  int nout;
+};
+hipError_t launch_sum_partials(const SumPartialsArgs& a, hipStream_t stream);
+
+}  // namespace mss

@@ -1,0 +1,46 @@
+// Sums of the workgroups' partial rows for the weights' gradients (gfx950).
+//
+// 16 columns x 64 slices of the partial rows per workgroup of 1024 threads:
+// each thread sums its slice's rows in order, the slices' sums meet in LDS in a
+// fixed order.  The partials were just written and come out of the caches.
+#include "norm_common.hpp"
+
+namespace mss {
+namespace {
+
+constexpr int kCols = 16, kSlices = 64;
+
+__global__ void __launch_bounds__(kCols* kSlices) sum_partials_kernel(SumPartialsArgs a) {
+  __shared__ float lds[kSlices][kCols + 1];
+  const int c = threadIdx.x % kCols, s = threadIdx.x / kCols;
+  const int64_t col = (int64_t)blockIdx.x * kCols + c;
+  const int64_t pitch = (int64_t)a.nout * a.cols;
+  float v = 0.f;
+  if (col < a.cols) {
+    const float* p = a.part + (int64_t)blockIdx.y * a.cols + col;
+    int64_t i = s;
+    for (; i + 3 * kSlices < a.nparts; i += 4 * kSlices) {
+      const float v0 = p[i * pitch], v1 = p[(i + kSlices) * pitch], v2 = p[(i + 2 * kSlices) * pitch],
+                  v3 = p[(i + 3 * kSlices) * pitch];
+      v += (v0 + v1) + (v2 + v3);
+    }
+    for (; i < a.nparts; i += kSlices) v += p[i * pitch];
+  }
+  lds[s][c] = v;
+  __syncthreads();
+  for (int h = kSlices / 2; h > 0; h >>= 1) {
+    if (s < h) lds[s][c] += lds[s + h][c];
+    __syncthreads();
+  }
+  if (s == 0 && col < a.cols) a.out[blockIdx.y][col] = lds[0][c];
+}
+
+}  // namespace
+
+hipError_t launch_sum_partials(const SumPartialsArgs& a, hipStream_t stream) {
+  hipLaunchKernelGGL(sum_partials_kernel, dim3((unsigned)((a.cols + kCols - 1) / kCols), (unsigned)a.nout),
+                     dim3(kCols * kSlices), 0, stream, a);
+  return hipGetLastError();
+}
+
+}  // namespace mss
