@@ -597,7 +597,7 @@ mss_status mss_unpack8(const int8_t* q, const uint8_t* scale, void* x, int64_t x
 /*   q, scale: the form of mss_pack8 of a [tokens, ins] tensor;              */
 /*   dw [outs, ins] dw_dtype.                                                */
 /* Supported: outs and ins up to 2^20, outs * ins up to 2^34, tokens up to   */
-/* 2^36, tokens * dy_stride below 2^47 (else MSS_ERR_SHAPE); dy_dtype        */
+/* 2^35, tokens * dy_stride below 2^47 (else MSS_ERR_SHAPE); dy_dtype        */
 /* MSS_BF16 (else MSS_ERR_UNSUPPORTED: fp32 gradients would have to be       */
 /* rounded).  dw 16-byte aligned; it must not overlap an input.  `workspace` */
 /* needs mss_wgrad8_workspace_size() bytes, 16-byte aligned.                 */

@@ -1068,7 +1068,7 @@ mss_status mss_unpack8(const int8_t* q, const uint8_t* scale, void* x, int64_t x
 }
 
 static bool wgrad8_shape_ok(int64_t tokens, int64_t outs, int64_t ins) {
-  return tokens > 0 && outs > 0 && ins > 0 && tokens <= (1LL << 36) && outs <= (1LL << 20) && ins <= (1LL << 20) &&
+  return tokens > 0 && outs > 0 && ins > 0 && tokens <= (1LL << 35) && outs <= (1LL << 20) && ins <= (1LL << 20) &&
          outs * ins <= (1LL << 34);
 }
 

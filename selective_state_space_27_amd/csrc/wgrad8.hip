@@ -3,16 +3,31 @@
 // on v_mfma_f32_32x32x16_bf16 with fp32 accumulation.  X's values are exact in
 // bf16, so nothing is rounded before the products.
 //
-// Both operands lie with the summed axis t slow, so a tile of 64 steps is
+// Both operands lie with the summed axis t slow, so a tile of 32 steps is
 // staged in LDS as it lies in memory (t-major), X widened on the way, and the
 // matrix operands (eight steps of one column per lane) come out of LDS by
 // transposing reads.  A staged row is cut into chunks of 64 bytes, chunk c of
 // row t stored at c ^ (t % 4): the four rows that a transposing read touches
 // then lie in different banks.
 //
+// What bounds it: the matrix cores, at the clock that the card holds under
+// them (about 1.9 GHz of 2.4 here).  256 x 256 tiles, eight waves of 128 x 64:
+// a wave reads 6 KB of LDS for 8 products, so LDS (1536 cycles for 64 steps,
+// reads and writes) stays under the matrix cores' 2048; smaller wave tiles
+// would not.  With dY loaded straight into LDS five stages ahead, the next
+// stage's first operands read before the barrier, and the widening of X
+// between the products, 32768 x 10576 x 2560 takes 1.53 ms, 1163 TFLOP/s (a
+// bf16 matrix product of 8192^3 by the vendor's library reaches 1210, its
+// product of this very shape and layout 812).  Before that: 623 TFLOP/s with
+// one stage ahead through registers, 665 without bounds checks inside, 886
+// with the transfers into LDS, 989 with their addresses kept instead of
+// computed, 1033 and 1163 with the cut tiles' sums joined wider and cut less.
+//
 // Output tiles that do not fill the card's last round are cut along t into
 // `splits` parts each, whose fp32 sums go to the workspace and are added in
 // order by a second kernel: the result does not depend on scheduling.
+#include <type_traits>
+
 #include "launch.hpp"
 #include "rows.hpp"
 #include "ssd_common.hpp"
@@ -23,7 +38,7 @@ namespace {
 using ssd::f32x16;
 using ssd::mfma;
 
-constexpr int kBK = 64;  // steps of a stage
+constexpr int kBK = 32;  // steps of a stage
 
 struct Args {
   const uint16_t* dy;
@@ -50,6 +65,14 @@ __device__ __forceinline__ void put(const Args& a, int64_t i, float v) {
     float* p = static_cast<float*>(a.dw) + i;
     *p = a.accumulate ? *p + v : v;
   }
+}
+
+// Tile `i` of the order: bands of eight tile rows, column by column.
+__host__ __device__ __forceinline__ void tile_at(int mt, int nt, int i, int& m, int& n) {
+  const int band = i / (8 * nt), r = i - band * 8 * nt;
+  const int left = mt - band * 8, rows = left < 8 ? left : 8;
+  n = r / rows;
+  m = band * 8 + r - n * rows;
 }
 
 template <int WM, int WN, int TM, int TN>  // waves, and 32 x 32 tiles of a wave
@@ -79,45 +102,117 @@ __device__ __forceinline__ u32x4 widen_bf16(uint32_t w0, uint32_t w1, uint32_t s
   return o;
 }
 
+// The tile and the stages of a workgroup.  Workgroups go to the eight XCDs in
+// turn; each XCD takes a run of neighbouring tiles (bands of eight tile rows,
+// column by column), so that the 32 it holds at a time share their operands in
+// its L2.
+struct Item {
+  int m, n;         // tile
+  int part;         // its part among the cut ones, or -1: the whole sum
+  int first, last;  // stages
+};
+__device__ __forceinline__ int xcd_run(int b, int total) {
+  const int x = b & 7, q = total >> 3, r = total & 7;
+  return x * q + min(x, r) + (b >> 3);
+}
+__device__ __forceinline__ Item item_of(const Args& a) {
+  Item it;
+  int tile;
+  if ((int)blockIdx.x < a.whole) {
+    tile = xcd_run(blockIdx.x, a.whole);
+    it.part = -1, it.first = 0, it.last = a.stages;
+  } else {
+    const int cut = a.mt * a.nt - a.whole, i = xcd_run(blockIdx.x - a.whole, cut * a.splits);
+    const int s = i / cut;
+    tile = i - s * cut;
+    it.part = tile * a.splits + s;
+    tile += a.whole;
+    it.first = (int)((int64_t)a.stages * s / a.splits);
+    it.last = (int)((int64_t)a.stages * (s + 1) / a.splits);
+  }
+  tile_at(a.mt, a.nt, tile, it.m, it.n);
+  return it;
+}
+
+// f(i, j) for every tile, the indices constants (an accumulator stays in registers).
+template <int TM, int TN, int I = 0, typename F>
+__device__ __forceinline__ void each_tile(F&& f) {
+  if constexpr (I < TM * TN) {
+    f(std::integral_constant<int, I / TN>{}, std::integral_constant<int, I % TN>{});
+    each_tile<TM, TN, I + 1>(f);
+  }
+}
+
+// A wave's accumulators: row 8 (r / 4) + r % 4 from lm, column ln of each 32 x 32 tile.
+template <int BM, int BN, int TM, int TN>
+__device__ __forceinline__ void write_tile(const Args& a, const Item& it, const f32x16 (&acc)[TM][TN], int lm, int ln) {
+  if (it.part >= 0) {
+    float* p = a.part + ((int64_t)it.part * BM + lm) * BN + ln;
+    each_tile<TM, TN>([&](auto i, auto j) {
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        p[(32 * i.value + 8 * (r >> 2) + (r & 3)) * BN + 32 * j.value] = acc[i.value][j.value][r];
+    });
+    return;
+  }
+  each_tile<TM, TN>([&](auto i, auto j) {
+    const int m = it.m * BM + lm + 32 * i.value, n = it.n * BN + ln + 32 * j.value;
+    if (n >= a.ins) return;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      const int mr = m + 8 * (r >> 2) + (r & 3);
+      if (mr < a.outs) put(a, (int64_t)mr * a.ins + n, acc[i.value][j.value][r]);
+    }
+  });
+}
+
+// Any alignment and stride of dY's rows: through registers, one stage ahead.
 template <typename C, int WM, int WN, int TM, int TN>
 __global__ void __launch_bounds__(C::kThreads) wgrad8_kernel(Args a) {
   constexpr int BM = C::BM, BN = C::BN, WA = BM * 2, WB = BN * 2;
-  constexpr int kStage = kBK * (WA + WB);  // [64][BM] of dY, [64][BN] of X, bf16
+  constexpr int kStage = kBK * (WA + WB);  // [kBK][BM] of dY, [kBK][BN] of X, bf16
   __shared__ __align__(16) unsigned char smem[2 * kStage];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   if (blockIdx.x == 0 && tid == 0) *a.status = 0;
-  // The tile and the stages of this workgroup.
-  int tile = blockIdx.x, part = -1, first = 0, last = a.stages;
-  if (tile >= a.whole) {
-    part = tile - a.whole;
-    tile = a.whole + part / a.splits;
-    const int s = part % a.splits;
-    first = (int)((int64_t)a.stages * s / a.splits);
-    last = (int)((int64_t)a.stages * (s + 1) / a.splits);
-  }
-  const int m0 = tile / a.nt * BM, n0 = tile % a.nt * BN;
+  const Item it = item_of(a);
+  const int m0 = it.m * BM, n0 = it.n * BN, first = it.first, last = it.last;
 
   u32x4 ra[C::kAPass];
   struct QRegs {
     u32x4 q;
     uint32_t scale;
   } rb[C::kBPass];
+  const int arow = tid / (BM / 8), acol = tid % (BM / 8) * 8, brow = tid / (BN / 16), bcol = tid % (BN / 16) * 16;
+  const uint16_t* ap = a.dy + arow * a.dy_stride + m0 + acol;
+  const int8_t* bp = a.q + (int64_t)brow * a.pitch + n0 + bcol;
+  const uint8_t* sp = a.scale + (int64_t)brow * (a.pitch >> 5) + ((n0 + bcol) >> 5);
+  const bool inside = m0 + BM <= a.outs && n0 + BN <= a.pitch;
   auto fetch = [&](int st) {
+    const int64_t t0 = (int64_t)st * kBK;
+    if (inside && t0 + kBK <= a.tokens) {
+#pragma unroll
+      for (int p = 0; p < C::kAPass; ++p)
+        ra[p] = *reinterpret_cast<const u32x4_a2*>(ap + (t0 + p * C::kARows) * a.dy_stride);
+#pragma unroll
+      for (int p = 0; p < C::kBPass; ++p) {
+        rb[p].q = *reinterpret_cast<const u32x4*>(bp + (t0 + p * C::kBRows) * a.pitch);
+        rb[p].scale = (uint32_t)sp[(t0 + p * C::kBRows) * (a.pitch >> 5)] << 23;
+      }
+      return;
+    }
 #pragma unroll
     for (int p = 0; p < C::kAPass; ++p) {
-      const int64_t t = (int64_t)st * kBK + p * C::kARows + tid / (BM / 8);
-      const int c = m0 + tid % (BM / 8) * 8;
-      ra[p] = load_raw<kSrcBf16>(a.dy + t * a.dy_stride, nullptr, c, t < a.tokens ? a.outs - c : 0).a;
+      const int64_t t = t0 + p * C::kARows + arow;
+      ra[p] = load_raw<kSrcBf16>(a.dy + t * a.dy_stride, nullptr, m0 + acol, t < a.tokens ? a.outs - m0 - acol : 0).a;
     }
 #pragma unroll
     for (int p = 0; p < C::kBPass; ++p) {
-      const int64_t t = (int64_t)st * kBK + p * C::kBRows + tid / (BN / 16);
-      const int c = n0 + tid % (BN / 16) * 16;
+      const int64_t t = t0 + p * C::kBRows + brow;
       rb[p].q = u32x4{};
       rb[p].scale = 0;
-      if (t < a.tokens && c < a.pitch) {  // the pitch is whole blocks of 32
-        rb[p].q = *reinterpret_cast<const u32x4*>(a.q + t * a.pitch + c);
-        rb[p].scale = (uint32_t)a.scale[t * (a.pitch >> 5) + (c >> 5)] << 23;
+      if (t < a.tokens && n0 + bcol < a.pitch) {  // the pitch is whole blocks of 32
+        rb[p].q = *reinterpret_cast<const u32x4*>(bp + (t0 + p * C::kBRows) * a.pitch);
+        rb[p].scale = (uint32_t)sp[(t0 + p * C::kBRows) * (a.pitch >> 5)] << 23;
       }
     }
   };
@@ -175,33 +270,228 @@ __global__ void __launch_bounds__(C::kThreads) wgrad8_kernel(Args a) {
     }
     if (st + 1 < last) commit(smem + ((st + 1 - first) & 1) * kStage);
   }
-  // Accumulators: row 8 (r / 4) + 4 hf + r % 4, column lane % 32 of a 32 x 32 tile.
-  const int lc = lane & 31;
-#pragma unroll
-  for (int i = 0; i < TM; ++i)
-#pragma unroll
-    for (int j = 0; j < TN; ++j)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int m = wm + 32 * i + 8 * (r >> 2) + 4 * hf + (r & 3), n = wn + 32 * j + lc;
-        if (part >= 0) a.part[((int64_t)part * BM + m) * BN + n] = acc[i][j][r];
-        else if (m0 + m < a.outs && n0 + n < a.ins) put(a, (int64_t)(m0 + m) * a.ins + n0 + n, acc[i][j][r]);
-      }
+  write_tile<BM, BN, TM, TN>(a, it, acc, wm + 4 * hf, wn + (lane & 31));
 }
 
-// The cut tiles: their parts added in order.  grid (tile, BM / 4 rows of four), BN threads.
-template <int BM, int BN>
-__global__ void __launch_bounds__(BN) wgrad8_join_kernel(Args a) {
-  const int tile = a.whole + blockIdx.x, m0 = tile / a.nt * BM, n = tile % a.nt * BN + threadIdx.x;
+// The same product where dY's rows are 16-byte aligned, whole vectors of
+// eight, and at most 2^23 elements apart: dY goes from memory straight into LDS.
+constexpr int kDK = kBK;  // steps of a stage
+constexpr int kNA = 6;    // staged tiles of dY
+constexpr int kNX = 3;    // ... of X
+// vmcnt limit (bits 3:0 and 15:14), the other counters not waited for.
+constexpr int vmcnt(int n) { return (n & 15) | ((n >> 4) << 14) | (7 << 4) | (15 << 8); }
+
+template <int WM, int WN, int TM, int TN>
+__global__ void __launch_bounds__(WM* WN * 64) wgrad8_dma_kernel(Args a) {
+  constexpr int BM = WM * TM * 32, BN = WN * TN * 32, WA = BM * 2, WB = BN * 2;
+  constexpr int kTA = kDK * WA, kTX = kDK * WB;
+  constexpr int kPieces = kTA / 1024 / (WM * WN);  // 1 KB transfers of a wave and stage
+  static_assert(kTA % (1024 * WM * WN) == 0 && WM * WN * 64 * 16 == kDK * BN, "");
+  // One array per staged tile: the compiler then knows which transfer a read may alias.
+  __shared__ __align__(1024) unsigned char a0[kTA], a1[kTA], a2[kTA], a3[kTA], a4[kTA], a5[kTA];
+  __shared__ __align__(1024) unsigned char x0[kTX], x1[kTX], x2[kTX];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  if (blockIdx.x == 0 && tid == 0) *a.status = 0;
+  const Item it = item_of(a);
+  const int m0 = it.m * BM, n0 = it.n * BN;
+  const int64_t te = min((int64_t)it.last * kDK, a.tokens);  // end of this part's steps
+
+  // This lane's offsets: of dY (row and 16-byte slot of piece wave + p waves), q and scale.
+  uint32_t aoff[kPieces];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int m = blockIdx.y * 4 + i;
-    if (m0 + m >= a.outs || n >= a.ins) continue;
-    const float* p = a.part + ((int64_t)blockIdx.x * a.splits * BM + m) * BN + threadIdx.x;
-    float v = 0.f;
-    for (int s = 0; s < a.splits; ++s) v += p[(int64_t)s * BM * BN];
-    put(a, (int64_t)(m0 + m) * a.ins + n, v);
+  for (int p = 0; p < kPieces; ++p) {
+    const int byte = (wave + p * WM * WN) * 1024 + lane * 16, t = byte / WA, pos = byte % WA / 16;
+    aoff[p] = ((uint32_t)t * (uint32_t)a.dy_stride + ((((pos >> 2) ^ (t & 3)) << 2 | (pos & 3)) << 3)) * 2;
   }
+  const int xt = tid / (BN / 16), xc = tid % (BN / 16) * 16, spitch = a.pitch >> 5;
+  const uint32_t qoff = (uint32_t)xt * a.pitch + xc, soff = (uint32_t)xt * spitch + (xc >> 5);
+  // X's two slots of a thread swap places in every other 256 bytes: sixteen
+  // lanes, which write every second slot of 512 bytes, then meet all banks.
+  const int xflip = (xc >> 7 & 1) << 4;
+  const int xs0 = stage_slot(xt, xc / 8, WB) ^ xflip, xs1 = stage_slot(xt, xc / 8 + 1, WB) ^ xflip;
+
+  // Where the next transfer of dY starts and the steps left from there, and the
+  // same of X.  With 64 steps left, a stage's accesses end inside the tensors
+  // however narrow they are (32 rows, and columns past the last one run on for
+  // at most 32 rows more); with fewer, the descriptor ends with the part, and
+  // what lies past it reads as zeros.
+  const char* pa = reinterpret_cast<const char*>(a.dy + (int64_t)it.first * kDK * a.dy_stride + m0);
+  const int8_t* pq = a.q + (int64_t)it.first * kDK * a.pitch + n0;
+  const uint8_t* ps = a.scale + (int64_t)it.first * kDK * spitch + (n0 >> 5);
+  int64_t left_a = te - (int64_t)it.first * kDK, left_x = left_a;  // not kept while `open`
+  const int64_t step_a = a.dy_stride * (2 * kDK), step_q = (int64_t)a.pitch * kDK, step_s = (int64_t)spitch * kDK;
+  constexpr uint32_t kOpen = 0x7fffff00u;
+  auto load_a = [&](auto open, unsigned char* dst) {
+    uint32_t bytes = kOpen;
+    if constexpr (!open.value) {
+      const int n = (int)max(min(left_a, (int64_t)64), (int64_t)0);
+      if (n < 64) bytes = n == 0 ? 0u : ((uint32_t)(n - 1) * (uint32_t)a.dy_stride + (uint32_t)(a.outs - m0)) * 2u;
+      left_a -= kDK;
+    }
+    const rsrc_t r = make_rsrc(pa, bytes);
+#pragma unroll
+    for (int p = 0; p < kPieces; ++p)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          r, (__attribute__((address_space(3))) void*)(dst + (wave + p * WM * WN) * 1024), 16, (int)aoff[p], 0, 0, 0);
+    pa += step_a;
+  };
+  struct QRegs {
+    u32x4 q;
+    uint32_t e;
+  };
+  auto load_q = [&](auto open) {
+    uint32_t qbytes = kOpen, sbytes = kOpen;
+    if constexpr (!open.value) {
+      const int n = (int)max(min(left_x, (int64_t)64), (int64_t)0);
+      if (n < 64) {
+        qbytes = n == 0 ? 0u : (uint32_t)(n * a.pitch - n0);
+        sbytes = n == 0 ? 0u : (uint32_t)(n * spitch - (n0 >> 5));
+      }
+      left_x -= kDK;
+    }
+    const rsrc_t rq = make_rsrc(pq, qbytes), rs = make_rsrc(ps, sbytes);
+    QRegs v;
+    v.q = buf_load_u32x4(rq, qoff);
+    v.e = __builtin_amdgcn_raw_buffer_load_b8(rs, (int)soff, 0, 0);
+    pq += step_q, ps += step_s;
+    return v;
+  };
+  auto put_x = [&](unsigned char* dst, const QRegs& v) {
+    *reinterpret_cast<u32x4*>(dst + xs0) = widen_bf16(v.q[0], v.q[1], v.e << 23);
+    *reinterpret_cast<u32x4*>(dst + xs1) = widen_bf16(v.q[2], v.q[3], v.e << 23);
+  };
+
+  f32x16 acc[TM][TN] = {};
+  const int wm = wave / WN * (TM * 32), wn = wave % WN * (TN * 32);
+  const int i16 = lane & 15, hf = lane >> 5, gc = (lane >> 4) & 1;
+  typedef short v4s __attribute__((ext_vector_type(4)));
+  const int frow = 8 * hf + (i16 >> 2), fsub = gc * 32 + (i16 & 3) * 8;
+  int fca[TM], fcb[TN];  // offsets of the operand reads
+#pragma unroll
+  for (int i = 0; i < TM; ++i) fca[i] = frow * WA + (((wm >> 5) + i) ^ (i16 >> 2)) * 64 + fsub;
+#pragma unroll
+  for (int j = 0; j < TN; ++j)
+    fcb[j] = frow * WB + (((wn >> 5) + j) ^ (i16 >> 2)) * 64 + (fsub ^ ((((wn >> 5) + j) >> 2 & 1) << 4));
+  auto rd = [&](const unsigned char* p, int width) -> u32x4 {
+    const u32x2 lo = __builtin_bit_cast(
+        u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)(p)));
+    const u32x2 hi = __builtin_bit_cast(
+        u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)(p + 4 * width)));
+    return u32x4{lo[0], lo[1], hi[0], hi[1]};
+  };
+  constexpr int kReads = 2 * (TM + TN);  // of one set of operands
+  static_assert(kReads <= 15, "");
+  struct Ops {
+    u32x4 a[TM], b[TN];
+  };
+  auto operands = [&](const unsigned char* sa, const unsigned char* sx, int kk) {
+    Ops o;
+#pragma unroll
+    for (int i = 0; i < TM; ++i) o.a[i] = rd(sa + fca[i] + kk * 16 * WA, WA);
+#pragma unroll
+    for (int j = 0; j < TN; ++j) o.b[j] = rd(sx + fcb[j] + kk * 16 * WB, WB);
+    return o;
+  };
+  auto products = [&](const Ops& o) {
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j) acc[i][j] = mfma(o.a[i], o.b[j], acc[i][j]);
+  };
+
+  // Stage s of six (the arrays a stage uses are then constants).  On entry its
+  // first operands are in registers, its other ones and those of stage s + 1
+  // are staged once the barrier is passed, and dY of s + 2 .. s + 4 and q of s
+  // + 2, s + 3 are on their way.
+  QRegs q0, q1;
+  Ops f0;
+  auto stage = [&](auto open, unsigned char* sa, unsigned char* sx, unsigned char* sa1, unsigned char* sx1, unsigned char* sx2,
+                   unsigned char* dst, QRegs& q) {
+    // This wave's dY of stage s + 1 has landed (the loads of three stages are
+    // younger than it), its X of s + 1 is written and all it read is in
+    // registers.  The empty assembly keeps memory accesses on their side.
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt((vmcnt(3 * (kPieces + 2)) & ~(15 << 8)) | (kReads << 8));
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    load_a(open, dst);
+    const QRegs now = q;
+    q = load_q(open);
+    const Ops f1 = operands(sa, sx, 1);
+    products(f0);
+    put_x(sx2, now);
+    __builtin_amdgcn_sched_barrier(0);
+    f0 = operands(sa1, sx1, 0);
+    products(f1);
+  };
+  const std::false_type bounded;
+  load_a(bounded, a0);
+  load_a(bounded, a1);
+  {
+    const QRegs p0 = load_q(bounded), p1 = load_q(bounded);
+    load_a(bounded, a2);
+    load_a(bounded, a3);
+    load_a(bounded, a4);
+    q0 = load_q(bounded);
+    q1 = load_q(bounded);
+    put_x(x0, p0);
+    put_x(x1, p1);
+  }
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0);
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  f0 = operands(a0, x0, 0);
+  auto six = [&](auto open) {
+    stage(open, a0, x0, a1, x1, x2, a5, q0);
+    stage(open, a1, x1, a2, x2, x0, a0, q1);
+    stage(open, a2, x2, a3, x0, x1, a1, q0);
+    stage(open, a3, x0, a4, x1, x2, a2, q1);
+    stage(open, a4, x1, a5, x2, x0, a3, q0);
+    stage(open, a5, x2, a0, x0, x1, a4, q1);
+  };
+  // Six stages at a time (past the part's end with zeros): those whose
+  // transfers, up to five stages ahead, have 64 steps left, then the rest.
+  int st = it.first;
+  const int open_end = (int)((te >> 5) - 12);
+  for (; st < open_end; st += 6) six(std::true_type{});
+  left_a = te - (int64_t)(st + 5) * kDK, left_x = te - (int64_t)(st + 4) * kDK;
+  for (; st < it.last; st += 6) six(bounded);
+  write_tile<BM, BN, TM, TN>(a, it, acc, wm + 4 * hf, wn + (lane & 31));
+}
+
+// The cut tiles: their parts added in order, four neighbouring sums a thread.
+// grid (BM BN / 1024, tile), 256 threads.
+template <int BM, int BN>
+__global__ void __launch_bounds__(256) wgrad8_join_kernel(Args a) {
+  int tm, tn;
+  tile_at(a.mt, a.nt, a.whole + blockIdx.y, tm, tn);
+  const int i = (blockIdx.x * 256 + threadIdx.x) * 4, m = tm * BM + i / BN, n = tn * BN + i % BN;
+  if (m >= a.outs || n >= a.ins) return;
+  const float* p = a.part + (int64_t)blockIdx.y * a.splits * (BM * BN) + i;
+  f32x4 v = {};
+  for (int s = 0; s < a.splits; s += 8) {
+    f32x4 t[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      t[j] = s + j < a.splits
+                 ? __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p + (int64_t)(s + j) * (BM * BN)))
+                 : f32x4{};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v += t[j];
+  }
+  const int64_t o = (int64_t)m * a.ins + n;
+  if (a.ins % 4 == 0 && !a.accumulate) {
+    if (a.dw_bf16)
+      *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.dw) + o) =
+          u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+    else
+      *reinterpret_cast<f32x4*>(static_cast<float*>(a.dw) + o) = v;
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (n + j < a.ins) put(a, o + j, v[j]);
 }
 
 // How a product is laid over the card.
@@ -220,13 +510,18 @@ Plan plan_of(int64_t tokens, int64_t outs, int64_t ins) {
   p.stages = (int)((tokens + kBK - 1) / kBK);
   const int tiles = p.mt * p.nt, rest = tiles % slots;
   p.whole = tiles - rest;
-  // Parts of the tiles past the last full round: the fewest that leave the
-  // least time, ceil(rest * s / slots) / s rounds, each part at least 4 stages.
-  p.splits = 1;
+  // Parts of the tiles past the last full round: the number that takes the
+  // least time by rounds of parts (a stage takes 0.9 us, with two workgroups of
+  // 128-wide tiles on a CU 0.55 us), 3 us to start a round, and writing and
+  // reading the parts' sums at 5 TB/s; a part has 8 stages or more.  (Counting
+  // rounds alone cut the in_proj shape above in 14 where 3 is best: 1.69 ms.)
+  const double stage = p.big ? 0.9 : 0.55, join = (p.big ? 256 * 256 : 128 * 128) * 8 / 5e6;
   double best = 1e30;
-  for (int s = 1; s <= 64 && s * 4 <= (p.stages > 4 ? p.stages : 4); ++s) {
-    const double rounds = (double)((rest * s + slots - 1) / slots) / s;
-    if (rounds < best * 0.97) best = rounds, p.splits = s;
+  p.splits = 1;
+  for (int s = 1; s <= 64 && (s == 1 || s * 8 <= p.stages); ++s) {
+    const int rounds = (rest * s + slots - 1) / slots;
+    const double us = rounds * ((double)p.stages / s * stage + 3.0) + (s > 1 ? rest * s * join : 0.0);
+    if (us < best) best = us, p.splits = s;
   }
   if (p.splits == 1) p.whole = tiles;
   return p;
@@ -236,11 +531,16 @@ template <int WM, int WN, int TM, int TN>
 hipError_t launch_cfg(const Args& a, hipStream_t stream) {
   typedef Cfg<WM, WN, TM, TN> C;
   const int cut = a.mt * a.nt - a.whole;
-  hipLaunchKernelGGL((wgrad8_kernel<C, WM, WN, TM, TN>), dim3((unsigned)(a.whole + cut * a.splits)), dim3(C::kThreads), 0,
-                     stream, a);
+  const dim3 grid((unsigned)(a.whole + cut * a.splits)), block(C::kThreads);
+  if ((reinterpret_cast<uintptr_t>(a.dy) & 15) == 0 && a.dy_stride % 8 == 0 && a.outs % 8 == 0 &&
+      a.dy_stride <= (1 << 23))
+    hipLaunchKernelGGL((wgrad8_dma_kernel<WM, WN, TM, TN>), grid, block, 0, stream, a);
+  else
+    hipLaunchKernelGGL((wgrad8_kernel<C, WM, WN, TM, TN>), grid, block, 0, stream, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || cut == 0) return e;
-  hipLaunchKernelGGL((wgrad8_join_kernel<C::BM, C::BN>), dim3((unsigned)cut, C::BM / 4), dim3(C::BN), 0, stream, a);
+  hipLaunchKernelGGL((wgrad8_join_kernel<C::BM, C::BN>), dim3(C::BM * C::BN / 1024, (unsigned)cut), dim3(256),
+                     0, stream, a);
   return hipGetLastError();
 }
 

@@ -114,7 +114,8 @@ def wgrad_ref(dy, p, tokens, outs, ins):
 # One tile, its borders, several tiles, cut sums (few tiles, many tokens), both
 # tile sizes; stages that end inside the tokens.
 SHAPES = [(1, 1, 1), (1, 64, 64), (63, 40, 33), (64, 128, 128), (65, 129, 127), (200, 256, 320), (1000, 257, 100),
-          (5000, 96, 160), (130, 1000, 31), (513, 768, 1536), (2048, 80, 2560)]
+          (5000, 96, 160), (130, 1000, 31), (513, 768, 1536), (2048, 80, 2560), (31, 8, 1), (33, 16, 40), (191, 8, 8),
+          (193, 72, 96), (385, 136, 64), (2051, 200, 136)]
 
 
 @pytest.mark.parametrize("tokens,outs,ins", SHAPES)
@@ -141,7 +142,8 @@ def test_wgrad(tokens, outs, ins, dw):
     assert torch.equal(got, mss.wgrad8(dy, p, out_dtype=DT[dw]))  # repeatable
 
 
-@pytest.mark.parametrize("tokens,outs,ins", [(300, 4112, 2050), (129, 3000, 4000)])
+@pytest.mark.parametrize("tokens,outs,ins", [(300, 4112, 2050), (129, 3000, 4000), (1000, 5000, 2601),
+                                             (70, 4001, 2050), (31, 2816, 3000)])
 def test_wgrad_large_tiles(tokens, outs, ins):
     """Enough 256-wide tiles for that layout, borders inside them."""
     g = gen(tokens)
@@ -180,6 +182,17 @@ def test_wgrad_of_a_slice_does_not_read_around_it(off, extra, tokens, outs, ins)
     x = torch.randint(-100, 101, (tokens, ins), generator=g, device="cuda:0").bfloat16()
     got = mss.wgrad8(dy, mss.pack8(x))
     assert np.array_equal(host64(got), host64(dy.contiguous()).T @ host64(x))
+
+
+@pytest.mark.parametrize("off", [0, 3])
+def test_wgrad_past_32_bit_offsets(off):
+    """Rows of dY 2^20 elements apart (aligned and not): the last ones lie past 2^32 elements."""
+    tokens, outs, ins, pitch = 4100, 72, 64, 1 << 20
+    g = gen(9)
+    dy = torch.empty(tokens * pitch, dtype=torch.bfloat16, device="cuda:0").view(tokens, pitch)[:, off:off + outs]
+    dy.copy_(torch.randint(-3, 4, (tokens, outs), generator=g, device="cuda:0"))
+    p = mss.pack8(torch.randint(-100, 101, (tokens, ins), generator=g, device="cuda:0").bfloat16())
+    assert torch.equal(mss.wgrad8(dy, p), mss.wgrad8(dy.contiguous(), p))
 
 
 def test_wgrad_non_finite():
