@@ -25,8 +25,9 @@ struct FwdArgs {
   int pitch;
 };
 
-template <bool RES32, bool IO32, bool POST, int LANES, int K>
-__global__ void __launch_bounds__(LANES ? 256 : 1024) add_norm_fwd_kernel(FwdArgs a) {
+template <bool RES32, bool IO32, bool POST, int LANES, int K, bool WHOLE>
+__global__ void __launch_bounds__(LANES ? 256 : 1024)
+    __attribute__((amdgpu_waves_per_eu(K == 2 ? 4 : 6))) add_norm_fwd_kernel(FwdArgs a) {
   constexpr int SR = RES32 ? kSrcF32 : kSrcBf16, SX = IO32 ? kSrcF32 : kSrcBf16;
   __shared__ float lds[LANES ? 1 : kRowSumFloats];
   int half = 0;
@@ -39,10 +40,10 @@ __global__ void __launch_bounds__(LANES ? 256 : 1024) add_norm_fwd_kernel(FwdArg
   for (int k = 0; k < K; ++k) {
     col[k] = at.col(k);
     n[k] = cols - col[k];
-    load_w(a.p.weight, col[k], n[k], w[k]);
-    if constexpr (POST) load_w(a.p.post_weight, col[k], n[k], post[k]);
+    load_w<WHOLE>(a.p.weight, col[k], n[k], w[k]);
+    if constexpr (POST) load_w<WHOLE>(a.p.post_weight, col[k], n[k], post[k]);
     if (a.p.gamma != nullptr) {
-      load_w(a.p.gamma, col[k], n[k], m[k]);
+      load_w<WHOLE>(a.p.gamma, col[k], n[k], m[k]);
 #pragma unroll
       for (int j = 0; j < 8; ++j) m[k][j] *= a.p.scale;
     } else {
@@ -59,8 +60,8 @@ __global__ void __launch_bounds__(LANES ? 256 : 1024) add_norm_fwd_kernel(FwdArg
     const char* rr = static_cast<const char*>(a.p.residual) + i * a.p.residual_stride * (RES32 ? 4 : 2);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      nx[k] = load_raw<SX>(xr, nullptr, col[k], n[k]);
-      nr[k] = load_raw<SR>(rr, nullptr, col[k], a.p.residual != nullptr ? n[k] : 0);
+      nx[k] = load_raw<SX, WHOLE>(xr, nullptr, col[k], n[k]);
+      nr[k] = load_raw<SR, WHOLE>(rr, nullptr, col[k], a.p.residual != nullptr ? n[k] : 0);
     }
   };
   if (row < a.p.rows) fetch(row);
@@ -94,7 +95,7 @@ __global__ void __launch_bounds__(LANES ? 256 : 1024) add_norm_fwd_kernel(FwdArg
     char* rout = static_cast<char*>(a.p.residual_out) + row * a.p.residual_out_stride * (RES32 ? 4 : 2);
 #pragma unroll
     for (int k = 0; k < K; ++k)
-      if (n[k] > 0) store8<RES32>(rout, col[k], n[k], r[k]);
+      if (n[k] > 0) store8<RES32, WHOLE>(rout, col[k], n[k], r[k]);
     row_sums<LANES>(sum, lds, half);
     const float rstd = rsqrtf(__builtin_fmaf(sum[0], inv, a.p.eps));
     char* out = static_cast<char*>(a.p.out) + row * a.p.out_stride * (IO32 ? 4 : 2);
@@ -103,7 +104,7 @@ __global__ void __launch_bounds__(LANES ? 256 : 1024) add_norm_fwd_kernel(FwdArg
       float o[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) o[j] = r[k][j] * rstd * w[k][j];
-      if (n[k] > 0) store8<IO32>(out, col[k], n[k], o);
+      if (n[k] > 0) store8<IO32, WHOLE>(out, col[k], n[k], o);
       if (a.p.out_q != nullptr) {
         as_stored<IO32>(o);  // the form of the output as it is stored
         store_p8(a.p.out_q + row * a.pitch, a.p.out_scale + row * (a.pitch >> 5), col[k], a.pitch, o);
@@ -121,10 +122,15 @@ struct BwdArgs {
 };
 
 // EXTRA: 0 = x unused, 1 = gamma, 2 = post (and gamma where given).
-template <bool RES32, bool IO32, bool PACKED, int EXTRA, int LANES, int K>
-__global__ void __launch_bounds__(LANES ? 256 : 1024) add_norm_bwd_kernel(BwdArgs a) {
+template <bool RES32, bool IO32, bool PACKED, int EXTRA, int LANES, int K, bool WHOLE>
+__global__ void __launch_bounds__(LANES ? 256 : 1024)
+    __attribute__((amdgpu_waves_per_eu(LANES ? (EXTRA ? 3 : 4) : K == 2 || EXTRA ? 4 : 5))) add_norm_bwd_kernel(BwdArgs a) {
   constexpr int SD = RES32 ? kSrcF32 : kSrcBf16, SO = IO32 ? kSrcF32 : kSrcBf16;
   constexpr int SR = PACKED ? kSrcP8 : SD, SX = PACKED ? kSrcP8 : SO;
+  // The next row is fetched ahead where the registers hold it.  With two vectors
+  // per thread they do not: the row is kept as loaded and widened a second time
+  // after the sums, and with EXTRA the weights are read again for every row.
+  constexpr bool kAhead = EXTRA != 2 && K == 1, kRenew = K == 2;
   __shared__ float lds[LANES ? kPartialLds : kRowSumFloats];
   int half = 0;
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;
@@ -134,20 +140,24 @@ __global__ void __launch_bounds__(LANES ? 256 : 1024) add_norm_bwd_kernel(BwdArg
   int col[K], n[K];
   float w[K][8], post[K][8], m[K][8];
   float dw[K][8] = {}, dgamma[K][8] = {}, dpost[K][8] = {};
-#pragma unroll
-  for (int k = 0; k < K; ++k) {
-    col[k] = at.col(k);
-    n[k] = cols - col[k];
-    load_w(a.p.weight, col[k], n[k], w[k]);
-    if constexpr (EXTRA == 2) load_w(a.p.post_weight, col[k], n[k], post[k]);
+  constexpr bool kReload = K == 2 && EXTRA != 0;
+  auto weights = [&](int k) {
+    load_w<WHOLE>(a.p.weight, col[k], n[k], w[k]);
+    if constexpr (EXTRA == 2) load_w<WHOLE>(a.p.post_weight, col[k], n[k], post[k]);
     if (EXTRA != 0 && a.p.gamma != nullptr) {
-      load_w(a.p.gamma, col[k], n[k], m[k]);
+      load_w<WHOLE>(a.p.gamma, col[k], n[k], m[k]);
 #pragma unroll
       for (int j = 0; j < 8; ++j) m[k][j] *= a.p.scale;
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) m[k][j] = a.p.scale;
     }
+  };
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    col[k] = at.col(k);
+    n[k] = cols - col[k];
+    if constexpr (!kReload) weights(k);
   }
   const int64_t step = (int64_t)gridDim.x * at.nseg;
   int64_t row = (int64_t)blockIdx.x * at.nseg + at.seg;
@@ -162,35 +172,52 @@ __global__ void __launch_bounds__(LANES ? 256 : 1024) add_norm_bwd_kernel(BwdArg
     const uint8_t* rs = PACKED ? a.p.r_scale + i * (a.pitch >> 5) : nullptr;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      nd[k] = load_raw<SO>(dr, nullptr, col[k], n[k]);
-      nr[k] = load_raw<SR>(rr, rs, col[k], n[k]);
-      ne[k] = load_raw<SD>(er, nullptr, col[k], a.p.dresidual_out != nullptr ? n[k] : 0);
+      nd[k] = load_raw<SO, WHOLE>(dr, nullptr, col[k], n[k]);
+      nr[k] = load_raw<SR, WHOLE>(rr, rs, col[k], n[k]);
+      ne[k] = load_raw<SD, WHOLE>(er, nullptr, col[k], a.p.dresidual_out != nullptr ? n[k] : 0);
     }
     if constexpr (EXTRA != 0) {
       const char* xr = static_cast<const char*>(a.p.x) + i * (PACKED ? a.pitch : a.p.x_stride * (IO32 ? 4 : 2));
       const uint8_t* xs = PACKED ? a.p.x_scale + i * (a.pitch >> 5) : nullptr;
 #pragma unroll
-      for (int k = 0; k < K; ++k) nx[k] = load_raw<SX>(xr, xs, col[k], n[k]);
+      for (int k = 0; k < K; ++k) nx[k] = load_raw<SX, WHOLE>(xr, xs, col[k], n[k]);
     }
   };
-  if (row < a.p.rows) fetch(row);
+  if (kAhead && row < a.p.rows) fetch(row);
   for (; row < a.p.rows; row += step) {
-    float d[K][8], e[K][8], r[K][8], x[K][8];
+    if constexpr (!kAhead) fetch(row);
+    Raw<SO> rd[K];
+    Raw<SD> re[K];
+    Raw<SR> rr[K];
+    Raw<SX> rx_[EXTRA ? K : 1];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      widen<SO>(nd[k], d[k]), widen<SR>(nr[k], r[k]), widen<SD>(ne[k], e[k]);
-      if constexpr (EXTRA != 0) widen<SX>(nx[k], x[k]);
+      rd[k] = nd[k], re[k] = ne[k], rr[k] = nr[k];
+      if constexpr (EXTRA != 0) rx_[k] = nx[k];
     }
-    if (row + step < a.p.rows) fetch(row + step);
+    if (kAhead && row + step < a.p.rows) fetch(row + step);
+    float d[K][8], e[K][8], r[K][8], x[K][8];
+    auto widen_row = [&](int k) {
+      widen<SO>(rd[k], d[k]), widen<SR>(rr[k], r[k]);
+      if constexpr (EXTRA != 0) widen<SX>(rx_[k], x[k]);
+    };
     float sum[EXTRA == 2 ? 3 : 2] = {};
 #pragma unroll
-    for (int k = 0; k < K; ++k)
+    for (int k = 0; k < K; ++k) {
+      widen_row(k);
+      if constexpr (kReload) load_w<WHOLE>(a.p.weight, col[k], n[k], w[k]);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         sum[0] = __builtin_fmaf(r[k][j], r[k][j], sum[0]);
         sum[1] = __builtin_fmaf(d[k][j] * w[k][j], r[k][j], sum[1]);
         if constexpr (EXTRA == 2) sum[2] = __builtin_fmaf(x[k][j], x[k][j], sum[2]);
       }
+      if constexpr (kRenew) {
+        renew(rd[k]), renew(rr[k]);
+        if constexpr (EXTRA != 0) renew(rx_[k]);
+        __builtin_amdgcn_sched_barrier(0);  // one vector at a time
+      }
+    }
     row_sums<LANES>(sum, lds, half);
     const float rstd = rsqrtf(__builtin_fmaf(sum[0], inv, a.p.eps));
     const float c1 = rstd * rstd * rstd * (sum[1] * inv);
@@ -200,18 +227,24 @@ __global__ void __launch_bounds__(LANES ? 256 : 1024) add_norm_bwd_kernel(BwdArg
     char* dx = static_cast<char*>(a.p.dx) + row * a.p.dx_stride * (IO32 ? 4 : 2);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
+      if constexpr (kRenew) widen_row(k);
+      if constexpr (kReload) {
+        asm volatile("" ::: "memory");
+        weights(k);
+      }
+      widen<SD>(re[k], e[k]);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float rh = r[k][j] * rstd;
         dw[k][j] = __builtin_fmaf(d[k][j], rh, dw[k][j]);
         e[k][j] += rstd * (d[k][j] * w[k][j]) - r[k][j] * c1;  // dr
       }
-      if (a.p.dresidual != nullptr && n[k] > 0) store8<RES32>(dres, col[k], n[k], e[k]);
+      if (a.p.dresidual != nullptr && n[k] > 0) store8<RES32, WHOLE>(dres, col[k], n[k], e[k]);
       if constexpr (EXTRA == 0) {
         if (a.p.dx != nullptr && n[k] > 0) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) e[k][j] *= m[k][j];
-          store8<IO32>(dx, col[k], n[k], e[k]);
+          store8<IO32, WHOLE>(dx, col[k], n[k], e[k]);
         }
       } else if constexpr (EXTRA == 1) {
 #pragma unroll
@@ -219,7 +252,7 @@ __global__ void __launch_bounds__(LANES ? 256 : 1024) add_norm_bwd_kernel(BwdArg
           dgamma[k][j] = __builtin_fmaf(e[k][j], a.p.scale * x[k][j], dgamma[k][j]);
           e[k][j] *= m[k][j];
         }
-        if (a.p.dx != nullptr && n[k] > 0) store8<IO32>(dx, col[k], n[k], e[k]);
+        if (a.p.dx != nullptr && n[k] > 0) store8<IO32, WHOLE>(dx, col[k], n[k], e[k]);
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -231,16 +264,22 @@ __global__ void __launch_bounds__(LANES ? 256 : 1024) add_norm_bwd_kernel(BwdArg
           sum2[0] = __builtin_fmaf(e[k][j], x[k][j], sum2[0]);
         }
       }
+      if constexpr (kRenew) __builtin_amdgcn_sched_barrier(0);
     }
     if constexpr (EXTRA == 2) {
+      if constexpr (kRenew) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) renew(rx_[k]);
+      }
       row_sums<LANES>(sum2, lds, half);
       const float c2 = rx * rx * rx * (sum2[0] * inv);
       if (a.p.dx != nullptr) {
 #pragma unroll
         for (int k = 0; k < K; ++k) {
+          if constexpr (kRenew) widen<SX>(rx_[k], x[k]);
 #pragma unroll
           for (int j = 0; j < 8; ++j) e[k][j] = rx * e[k][j] - x[k][j] * c2;
-          if (n[k] > 0) store8<IO32>(dx, col[k], n[k], e[k]);
+          if (n[k] > 0) store8<IO32, WHOLE>(dx, col[k], n[k], e[k]);
         }
       }
     }
@@ -248,17 +287,17 @@ __global__ void __launch_bounds__(LANES ? 256 : 1024) add_norm_bwd_kernel(BwdArg
   // [dweight][dgamma where given][dpost]
   float* part = a.part + (int64_t)blockIdx.x * a.nout * cols;
 #pragma unroll
-  for (int k = 0; k < K; ++k) store_partial<LANES>(part, col[k], n[k], dw[k], lds);
+  for (int k = 0; k < K; ++k) store_partial<LANES, WHOLE>(part, col[k], n[k], dw[k], lds);
   if constexpr (EXTRA != 0) {
     int at_out = 1;
     if (a.p.gamma != nullptr) {
 #pragma unroll
-      for (int k = 0; k < K; ++k) store_partial<LANES>(part + cols, col[k], n[k], dgamma[k], lds);
+      for (int k = 0; k < K; ++k) store_partial<LANES, WHOLE>(part + cols, col[k], n[k], dgamma[k], lds);
       at_out = 2;
     }
     if constexpr (EXTRA == 2) {
 #pragma unroll
-      for (int k = 0; k < K; ++k) store_partial<LANES>(part + (int64_t)at_out * cols, col[k], n[k], dpost[k], lds);
+      for (int k = 0; k < K; ++k) store_partial<LANES, WHOLE>(part + (int64_t)at_out * cols, col[k], n[k], dpost[k], lds);
     }
   }
 }
@@ -266,13 +305,13 @@ __global__ void __launch_bounds__(LANES ? 256 : 1024) add_norm_bwd_kernel(BwdArg
 template <bool RES32, bool IO32>
 hipError_t fwd_typed(const AddNormFwdParams& p, hipStream_t stream) {
   const NormShape s = norm_shape(p.cols);
-  const dim3 grid((unsigned)norm_blocks(s, p.rows, 1)), block((unsigned)s.threads);
+  const dim3 grid((unsigned)norm_blocks(s, p.rows, 1, false)), block((unsigned)s.threads);
   const FwdArgs a{p, (int)((p.cols + 31) / 32 * 32)};
-  return with_shape(s, [&](auto lanes, auto k) {
+  return with_shape(s, p.cols % 8 == 0, [&](auto lanes, auto k, auto whole) {
     if (p.post_weight != nullptr)
-      hipLaunchKernelGGL((add_norm_fwd_kernel<RES32, IO32, true, lanes.value, k.value>), grid, block, 0, stream, a);
+      hipLaunchKernelGGL((add_norm_fwd_kernel<RES32, IO32, true, lanes.value, k.value, whole.value>), grid, block, 0, stream, a);
     else
-      hipLaunchKernelGGL((add_norm_fwd_kernel<RES32, IO32, false, lanes.value, k.value>), grid, block, 0, stream, a);
+      hipLaunchKernelGGL((add_norm_fwd_kernel<RES32, IO32, false, lanes.value, k.value, whole.value>), grid, block, 0, stream, a);
     return hipGetLastError();
   });
 }
@@ -280,15 +319,15 @@ hipError_t fwd_typed(const AddNormFwdParams& p, hipStream_t stream) {
 template <bool RES32, bool IO32, bool PACKED, int EXTRA>
 hipError_t bwd_typed(const AddNormBwdParams& p, hipStream_t stream) {
   const NormShape s = norm_shape(p.cols);
-  const int64_t blocks = norm_blocks(s, p.rows, 1);
+  const int64_t blocks = norm_blocks(s, p.rows, 1, true);
   BwdArgs a{p, reinterpret_cast<float*>(static_cast<char*>(p.workspace) + 256), 1, (int)((p.cols + 31) / 32 * 32),
             static_cast<int*>(p.workspace)};
   SumPartialsArgs sum{a.part, {p.dweight, nullptr, nullptr}, blocks, p.cols, 1};
   if (EXTRA != 0 && p.gamma != nullptr) sum.out[sum.nout++] = p.dgamma;
   if (EXTRA == 2) sum.out[sum.nout++] = p.dpost_weight;
   a.nout = sum.nout;
-  const hipError_t e = with_shape(s, [&](auto lanes, auto k) {
-    hipLaunchKernelGGL((add_norm_bwd_kernel<RES32, IO32, PACKED, EXTRA, lanes.value, k.value>), dim3((unsigned)blocks),
+  const hipError_t e = with_shape(s, p.cols % 8 == 0, [&](auto lanes, auto k, auto whole) {
+    hipLaunchKernelGGL((add_norm_bwd_kernel<RES32, IO32, PACKED, EXTRA, lanes.value, k.value, whole.value>), dim3((unsigned)blocks),
                        dim3((unsigned)s.threads), 0, stream, a);
     return hipGetLastError();
   });
@@ -313,7 +352,7 @@ hipError_t launch_add_norm_fwd(const AddNormFwdParams& p, hipStream_t stream) {
 }
 
 size_t add_norm_bwd_workspace_bytes(int64_t rows, int64_t cols, int ngrads) {
-  return 256 + (size_t)norm_blocks(norm_shape(cols), rows, 1) * (size_t)ngrads * (size_t)cols * sizeof(float);
+  return 256 + (size_t)norm_blocks(norm_shape(cols), rows, 1, true) * (size_t)ngrads * (size_t)cols * sizeof(float);
 }
 
 hipError_t launch_add_norm_bwd(const AddNormBwdParams& p, hipStream_t stream) {

@@ -33,8 +33,9 @@ struct FwdArgs {
   int gcols;  // columns of a group
 };
 
-template <bool Y32, bool IO32, int MODE, int LANES, int K>
-__global__ void __launch_bounds__(LANES ? 256 : 1024) gated_norm_fwd_kernel(FwdArgs a) {
+template <bool Y32, bool IO32, int MODE, int LANES, int K, bool WHOLE>
+__global__ void __launch_bounds__(LANES ? 256 : 1024)
+    __attribute__((amdgpu_waves_per_eu(K == 2 ? 4 : 6))) gated_norm_fwd_kernel(FwdArgs a) {
   constexpr int SY = Y32 ? kSrcF32 : kSrcBf16, SZ = IO32 ? kSrcF32 : kSrcBf16;
   __shared__ float lds[LANES ? 1 : kRowSumFloats];
   int half = 0;
@@ -47,7 +48,7 @@ __global__ void __launch_bounds__(LANES ? 256 : 1024) gated_norm_fwd_kernel(FwdA
   for (int k = 0; k < K; ++k) {
     col[k] = c0 + at.col(k);
     n[k] = a.gcols - at.col(k);
-    load_w(a.p.weight, col[k], n[k], w[k]);
+    load_w<WHOLE>(a.p.weight, col[k], n[k], w[k]);
   }
   const int64_t step = (int64_t)gridDim.x * at.nseg;
   int64_t row = (int64_t)blockIdx.x * at.nseg + at.seg;
@@ -58,8 +59,8 @@ __global__ void __launch_bounds__(LANES ? 256 : 1024) gated_norm_fwd_kernel(FwdA
     const char* zr = static_cast<const char*>(a.p.z) + i * a.p.z_stride * (IO32 ? 4 : 2);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      ny[k] = load_raw<SY>(yr, nullptr, col[k], n[k]);
-      if constexpr (MODE != kNoGate) nz[k] = load_raw<SZ>(zr, nullptr, col[k], n[k]);
+      ny[k] = load_raw<SY, WHOLE>(yr, nullptr, col[k], n[k]);
+      if constexpr (MODE != kNoGate) nz[k] = load_raw<SZ, WHOLE>(zr, nullptr, col[k], n[k]);
     }
   };
   if (row < a.p.rows) fetch(row);
@@ -99,7 +100,7 @@ __global__ void __launch_bounds__(LANES ? 256 : 1024) gated_norm_fwd_kernel(FwdA
         o[j] = y[k][j] * rstd * w[k][j];
         if constexpr (MODE == kNormFirst) o[j] *= z[k][j] * sigmoid(z[k][j]);
       }
-      if (n[k] > 0) store8<IO32>(out, col[k], n[k], o);
+      if (n[k] > 0) store8<IO32, WHOLE>(out, col[k], n[k], o);
       if (a.p.out_q != nullptr) {
         as_stored<IO32>(o);  // the form of the output as it is stored
         store_p8(a.p.out_q + prow, a.p.out_scale + srow, col[k], a.p.ngroups == 1 ? a.pitch : c0 + a.gcols, o);
@@ -116,10 +117,15 @@ struct BwdArgs {
   int* status;
 };
 
-template <bool Y32, bool IO32, bool PACKED, int MODE, int LANES, int K>
-__global__ void __launch_bounds__(LANES ? 256 : 1024) gated_norm_bwd_kernel(BwdArgs a) {
+template <bool Y32, bool IO32, bool PACKED, int MODE, int LANES, int K, bool WHOLE>
+__global__ void __launch_bounds__(LANES ? 256 : 1024)
+    __attribute__((amdgpu_waves_per_eu(4))) gated_norm_bwd_kernel(BwdArgs a) {
   constexpr int SO = IO32 ? kSrcF32 : kSrcBf16;
   constexpr int SY = PACKED ? kSrcP8 : Y32 ? kSrcF32 : kSrcBf16, SZ = PACKED ? kSrcP8 : SO;
+  // One vector per thread: the next row is fetched ahead.  Two: the registers do
+  // not hold that; the row is kept as loaded and widened a second time after the
+  // sums instead (8192 x 10240: 233 us; ahead, with spills, 429).
+  constexpr bool kAhead = K == 1, kRenew = K == 2;
   __shared__ float lds[LANES ? kPartialLds : kRowSumFloats];
   int half = 0;
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *a.status = 0;
@@ -132,7 +138,7 @@ __global__ void __launch_bounds__(LANES ? 256 : 1024) gated_norm_bwd_kernel(BwdA
   for (int k = 0; k < K; ++k) {
     col[k] = c0 + at.col(k);
     n[k] = a.gcols - at.col(k);
-    load_w(a.p.weight, col[k], n[k], w[k]);
+    load_w<WHOLE>(a.p.weight, col[k], n[k], w[k]);
   }
   const int64_t step = (int64_t)gridDim.x * at.nseg;
   int64_t row = (int64_t)blockIdx.x * at.nseg + at.seg;
@@ -147,23 +153,32 @@ __global__ void __launch_bounds__(LANES ? 256 : 1024) gated_norm_bwd_kernel(BwdA
     const uint8_t* zs = PACKED ? a.p.z_scale + i * (a.pitch >> 5) : nullptr;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      nd[k] = load_raw<SO>(dr, nullptr, col[k], n[k]);
-      ny[k] = load_raw<SY>(yr, ys, col[k], n[k]);
-      if constexpr (MODE != kNoGate) nz[k] = load_raw<SZ>(zr, zs, col[k], n[k]);
+      nd[k] = load_raw<SO, WHOLE>(dr, nullptr, col[k], n[k]);
+      ny[k] = load_raw<SY, WHOLE>(yr, ys, col[k], n[k]);
+      if constexpr (MODE != kNoGate) nz[k] = load_raw<SZ, WHOLE>(zr, zs, col[k], n[k]);
     }
   };
-  if (row < a.p.rows) fetch(row);
+  if (kAhead && row < a.p.rows) fetch(row);
   for (; row < a.p.rows; row += step) {
-    float d[K][8], y[K][8], z[K][8];
+    if constexpr (!kAhead) fetch(row);
+    Raw<SO> rd[K];
+    Raw<SY> ry[K];
+    Raw<SZ> rz[MODE != kNoGate ? K : 1];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      widen<SO>(nd[k], d[k]), widen<SY>(ny[k], y[k]);
-      if constexpr (MODE != kNoGate) widen<SZ>(nz[k], z[k]);
+      rd[k] = nd[k], ry[k] = ny[k];
+      if constexpr (MODE != kNoGate) rz[k] = nz[k];
     }
-    if (row + step < a.p.rows) fetch(row + step);
+    if (kAhead && row + step < a.p.rows) fetch(row + step);
+    float d[K][8], y[K][8], z[K][8];
+    auto widen_row = [&](int k) {
+      widen<SO>(rd[k], d[k]), widen<SY>(ry[k], y[k]);
+      if constexpr (MODE != kNoGate) widen<SZ>(rz[k], z[k]);
+    };
     float sum[2] = {};
 #pragma unroll
-    for (int k = 0; k < K; ++k)
+    for (int k = 0; k < K; ++k) {
+      widen_row(k);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         float g = d[k][j] * w[k][j], v = y[k][j];
@@ -175,6 +190,12 @@ __global__ void __launch_bounds__(LANES ? 256 : 1024) gated_norm_bwd_kernel(BwdA
         sum[0] = __builtin_fmaf(v, v, sum[0]);
         sum[1] = __builtin_fmaf(g, v, sum[1]);
       }
+      if constexpr (kRenew) {
+        renew(rd[k]), renew(ry[k]);
+        if constexpr (MODE != kNoGate) renew(rz[k]);
+        __builtin_amdgcn_sched_barrier(0);  // one vector at a time
+      }
+    }
     row_sums<LANES>(sum, lds, half);
     const float rstd = rsqrtf(__builtin_fmaf(sum[0], inv, a.p.eps));
     const float c1 = rstd * rstd * rstd * (sum[1] * inv);
@@ -183,6 +204,7 @@ __global__ void __launch_bounds__(LANES ? 256 : 1024) gated_norm_bwd_kernel(BwdA
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       float dy[8], dz[8];
+      if constexpr (kRenew) widen_row(k);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float g = d[k][j] * w[k][j];
@@ -206,24 +228,25 @@ __global__ void __launch_bounds__(LANES ? 256 : 1024) gated_norm_bwd_kernel(BwdA
         }
       }
       if (n[k] > 0) {
-        store8<Y32>(dyr, col[k], n[k], dy);
-        if constexpr (MODE != kNoGate) store8<IO32>(dzr, col[k], n[k], dz);
+        store8<Y32, WHOLE>(dyr, col[k], n[k], dy);
+        if constexpr (MODE != kNoGate) store8<IO32, WHOLE>(dzr, col[k], n[k], dz);
       }
+      if constexpr (kRenew) __builtin_amdgcn_sched_barrier(0);
     }
   }
   float* part = a.part + (int64_t)blockIdx.x * a.p.cols + c0;
 #pragma unroll
-  for (int k = 0; k < K; ++k) store_partial<LANES>(part, at.col(k), n[k], dw[k], lds);
+  for (int k = 0; k < K; ++k) store_partial<LANES, WHOLE>(part, at.col(k), n[k], dw[k], lds);
 }
 
 template <bool Y32, bool IO32, int MODE>
 hipError_t fwd_mode(const GatedNormFwdParams& p, hipStream_t stream) {
   const int64_t gcols = p.cols / p.ngroups;
   const NormShape s = norm_shape(gcols);
-  const dim3 grid((unsigned)norm_blocks(s, p.rows, p.ngroups), (unsigned)p.ngroups), block((unsigned)s.threads);
+  const dim3 grid((unsigned)norm_blocks(s, p.rows, p.ngroups, false), (unsigned)p.ngroups), block((unsigned)s.threads);
   const FwdArgs a{p, (int)((p.cols + 31) / 32 * 32), (int)gcols};
-  return with_shape(s, [&](auto lanes, auto k) {
-    hipLaunchKernelGGL((gated_norm_fwd_kernel<Y32, IO32, MODE, lanes.value, k.value>), grid, block, 0, stream, a);
+  return with_shape(s, gcols % 8 == 0, [&](auto lanes, auto k, auto whole) {
+    hipLaunchKernelGGL((gated_norm_fwd_kernel<Y32, IO32, MODE, lanes.value, k.value, whole.value>), grid, block, 0, stream, a);
     return hipGetLastError();
   });
 }
@@ -238,11 +261,11 @@ template <bool Y32, bool IO32, bool PACKED, int MODE>
 hipError_t bwd_mode(const GatedNormBwdParams& p, hipStream_t stream) {
   const int64_t gcols = p.cols / p.ngroups;
   const NormShape s = norm_shape(gcols);
-  const int64_t blocks = norm_blocks(s, p.rows, p.ngroups);
+  const int64_t blocks = norm_blocks(s, p.rows, p.ngroups, true);
   const BwdArgs a{p, reinterpret_cast<float*>(static_cast<char*>(p.workspace) + 256), (int)((p.cols + 31) / 32 * 32),
                   (int)gcols, static_cast<int*>(p.workspace)};
-  const hipError_t e = with_shape(s, [&](auto lanes, auto k) {
-    hipLaunchKernelGGL((gated_norm_bwd_kernel<Y32, IO32, PACKED, MODE, lanes.value, k.value>),
+  const hipError_t e = with_shape(s, gcols % 8 == 0, [&](auto lanes, auto k, auto whole) {
+    hipLaunchKernelGGL((gated_norm_bwd_kernel<Y32, IO32, PACKED, MODE, lanes.value, k.value, whole.value>),
                        dim3((unsigned)blocks, (unsigned)p.ngroups), dim3((unsigned)s.threads), 0, stream, a);
     return hipGetLastError();
   });
@@ -270,7 +293,7 @@ hipError_t launch_gated_norm_fwd(const GatedNormFwdParams& p, hipStream_t stream
 }
 
 size_t gated_norm_bwd_workspace_bytes(int64_t rows, int64_t cols, int64_t ngroups) {
-  return 256 + (size_t)norm_blocks(norm_shape(cols / ngroups), rows, ngroups) * (size_t)cols * sizeof(float);
+  return 256 + (size_t)norm_blocks(norm_shape(cols / ngroups), rows, ngroups, true) * (size_t)cols * sizeof(float);
 }
 
 hipError_t launch_gated_norm_bwd(const GatedNormBwdParams& p, hipStream_t stream) {

@@ -2,7 +2,7 @@
 // over lanes, and the sums over rows for the weights' gradients.
 //
 // A "segment" is what one norm runs over: a row, or one group of a row's
-// columns.  Segments of up to 512 columns take 16, 32 or 64 lanes of a wave
+// columns.  Segments of up to 512 columns take 32 or 64 lanes of a wave
 // (LANES; a workgroup of 256 threads holds 256 / LANES of them, the sums need
 // no barrier); longer ones take a workgroup (LANES = 0) of just enough waves
 // for eight columns per thread, or for sixteen (K = 2) past kOneVectorMax
@@ -10,6 +10,8 @@
 // issued before the present one's sums, and keep the weights (and the
 // gradients' partial sums over rows) in registers.
 #pragma once
+
+#include <type_traits>
 
 #include "launch.hpp"
 #include "rows.hpp"
@@ -22,14 +24,13 @@ constexpr int kNormColsMax = 16384;   // columns of a segment at most (1024 thre
 
 // Segment layout of a launch.
 struct NormShape {
-  int lanes;    // 16, 32, 64, or 0 (workgroup)
+  int lanes;    // 32, 64, or 0 (workgroup)
   int k;        // vectors of 8 columns per thread
   int threads;  // of a workgroup
   int segs;     // segments a workgroup holds at a time
 };
 
 inline NormShape norm_shape(int64_t cols) {
-  if (cols <= 128) return {16, 1, 256, 16};
   if (cols <= 256) return {32, 1, 256, 8};
   if (cols <= 512) return {64, 1, 256, 4};
   const int k = cols <= kOneVectorMax ? 1 : 2;
@@ -37,23 +38,32 @@ inline NormShape norm_shape(int64_t cols) {
   return {0, k, threads, 1};
 }
 
-// Workgroups per group of columns: every slot of the card (2048 threads per
-// CU) taken once, and no more than there are rows.
-inline int64_t norm_blocks(const NormShape& s, int64_t rows, int64_t groups) {
-  const int64_t slots = (int64_t)kNormCUs * (2048 / s.threads);
+// Workgroups per group of columns, no more than there are rows.  One to two rows
+// of the model's width in flight on a CU stream best: at 32768 x 5120 (640
+// threads) the gated norm takes 231 us with one workgroup per CU and 255 with
+// two, its backward 444 and 459 (498 with sixteen, which also writes and reads
+// more partial sums); at 32768 x 2560 (320 threads) add_norm takes 181 us with
+// one, 178 with two, 202 with eight.  Narrow rows need more: 768 columns (128
+// threads) 190, 90, 75 and 77 us with one, three, six and eight.
+inline int64_t norm_blocks(const NormShape& s, int64_t rows, int64_t groups, bool backward) {
+  const int per_cu = backward ? (s.threads >= 256 ? 1 : 512 / s.threads) : s.threads >= 640 ? 1 : 640 / s.threads;
+  const int64_t slots = (int64_t)kNormCUs * per_cu;
   const int64_t want = slots / groups > 0 ? slots / groups : 1;
   const int64_t most = (rows + s.segs - 1) / s.segs;
   return want < most ? want : most;
 }
 
-// Calls f(std::integral_constant<int, LANES>, <int, K>) for the shape.
+// Calls f with the shape's LANES and K and whether rows are whole vectors, as constants.
 template <typename F>
-inline hipError_t with_shape(const NormShape& s, F&& f) {
-  if (s.lanes == 16) return f(std::integral_constant<int, 16>{}, std::integral_constant<int, 1>{});
-  if (s.lanes == 32) return f(std::integral_constant<int, 32>{}, std::integral_constant<int, 1>{});
-  if (s.lanes == 64) return f(std::integral_constant<int, 64>{}, std::integral_constant<int, 1>{});
-  if (s.k == 1) return f(std::integral_constant<int, 0>{}, std::integral_constant<int, 1>{});
-  return f(std::integral_constant<int, 0>{}, std::integral_constant<int, 2>{});
+inline hipError_t with_shape(const NormShape& s, bool whole, F&& f) {
+  const std::integral_constant<int, 1> one;
+  const auto with = [&](auto w) {
+    if (s.lanes == 32) return f(std::integral_constant<int, 32>{}, one, w);
+    if (s.lanes == 64) return f(std::integral_constant<int, 64>{}, one, w);
+    if (s.k == 1) return f(std::integral_constant<int, 0>{}, one, w);
+    return f(std::integral_constant<int, 0>{}, std::integral_constant<int, 2>{}, w);
+  };
+  return whole ? with(std::true_type{}) : with(std::false_type{});
 }
 
 // Where a thread is: which of the workgroup's segments, its first column, and
@@ -73,16 +83,17 @@ struct Place {
 };
 
 // Eight weights (fp32, any alignment of 4), zeros past the end.
+template <bool WHOLE>
 __device__ __forceinline__ void load_w(const float* w, int col, int n, float (&v)[8]) {
-  widen<kSrcF32>(load_raw<kSrcF32>(w, nullptr, col, n), v);
+  widen<kSrcF32>(load_raw<kSrcF32, WHOLE>(w, nullptr, col, n), v);
 }
 
 // A workgroup's sums over its rows, `part[col]`: the sums of its segments (the
 // same columns, different rows) meet in LDS, in a fixed order.
-template <int LANES>
+template <int LANES, bool WHOLE>
 __device__ __forceinline__ void store_partial(float* part, int col, int n, const float (&acc)[8], float* lds) {
   if constexpr (LANES == 0) {
-    if (n > 0) store8<true>(part, col, n, acc);
+    if (n > 0) store8<true, WHOLE>(part, col, n, acc);
   } else {
     __syncthreads();  // before: `lds` may still be read from the last call
 #pragma unroll

@@ -29,7 +29,7 @@ typedef uint32_t u32x4_a2 __attribute__((ext_vector_type(4), aligned(2)));
 typedef uint32_t u32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
 
 // Eight columns of a row as loaded: 16 bytes of bf16, 32 of fp32, or 8 of q
-// and the scale's bits.
+// and the scale's exponent byte.
 template <int SRC>
 struct Raw {
   u32x4 a;
@@ -41,26 +41,27 @@ struct Raw<kSrcF32> {
 template <>
 struct Raw<kSrcP8> {
   u32x2 a;
-  uint32_t scale;
+  uint32_t e;
 };
 
 // Columns col .. col + 7 of a row; `n` of them exist (n <= 0: none, zeros).
 // For the 8-bit form, whose rows are padded, `row` is the row of q and `srow`
-// its scales.
-template <int SRC>
+// its scales.  WHOLE: the rows are whole vectors (n >= 8 or n <= 0), which
+// leaves the column by column path out of the code.
+template <int SRC, bool WHOLE = false>
 __device__ __forceinline__ Raw<SRC> load_raw(const void* row, const uint8_t* srow, int col, int n) {
   Raw<SRC> r{};
   if constexpr (SRC == kSrcP8) {
     if (n > 0) {
       r.a = *reinterpret_cast<const u32x2*>(static_cast<const int8_t*>(row) + col);
-      r.scale = (uint32_t)srow[col >> 5] << 23;
+      r.e = srow[col >> 5];  // shifted into place when used: nothing here waits for it
     }
   } else if constexpr (SRC == kSrcF32) {
     const float* p = static_cast<const float*>(row) + col;
-    if (n >= 8) {
+    if (WHOLE ? n > 0 : n >= 8) {
       r.a = *reinterpret_cast<const u32x4_a4*>(p);
       r.b = *reinterpret_cast<const u32x4_a4*>(p + 4);
-    } else if (n > 0) {
+    } else if (!WHOLE && n > 0) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         r.a[j] = j < n ? __float_as_uint(p[j]) : 0u;
@@ -69,9 +70,9 @@ __device__ __forceinline__ Raw<SRC> load_raw(const void* row, const uint8_t* sro
     }
   } else {
     const uint16_t* p = static_cast<const uint16_t*>(row) + col;
-    if (n >= 8) {
+    if (WHOLE ? n > 0 : n >= 8) {
       r.a = *reinterpret_cast<const u32x4_a2*>(p);
-    } else if (n > 0) {
+    } else if (!WHOLE && n > 0) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const uint32_t lo = 2 * j < n ? p[2 * j] : 0u, hi = 2 * j + 1 < n ? p[2 * j + 1] : 0u;
@@ -82,10 +83,30 @@ __device__ __forceinline__ Raw<SRC> load_raw(const void* row, const uint8_t* sro
   return r;
 }
 
+// Makes the compiler take the values as new: what was widened from them before
+// is not kept, but widened again.
+template <int SRC>
+__device__ __forceinline__ void renew(Raw<SRC>& r) {
+#pragma unroll
+  for (int j = 0; j < (SRC == kSrcP8 ? 2 : 4); ++j) {
+    uint32_t w = r.a[j];
+    asm volatile("" : "+v"(w));
+    r.a[j] = w;
+  }
+  if constexpr (SRC == kSrcF32) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t w = r.b[j];
+      asm volatile("" : "+v"(w));
+      r.b[j] = w;
+    }
+  }
+}
+
 template <int SRC>
 __device__ __forceinline__ void widen(const Raw<SRC>& r, float (&v)[8]) {
   if constexpr (SRC == kSrcP8) {
-    const float s = __uint_as_float(r.scale);
+    const float s = __uint_as_float(r.e << 23);
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = (float)((int32_t)(r.a[j >> 2] << (24 - 8 * (j & 3))) >> 24) * s;
   } else if constexpr (SRC == kSrcF32) {
@@ -97,12 +118,12 @@ __device__ __forceinline__ void widen(const Raw<SRC>& r, float (&v)[8]) {
   }
 }
 
-// The first n of eight values at column col of a row.
-template <bool F32>
+// The first n (> 0) of eight values at column col of a row.
+template <bool F32, bool WHOLE = false>
 __device__ __forceinline__ void store8(void* row, int col, int n, const float (&v)[8]) {
   if constexpr (F32) {
     float* p = static_cast<float*>(row) + col;
-    if (n >= 8) {
+    if (WHOLE || n >= 8) {
       *reinterpret_cast<u32x4_a4*>(p) = u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
                                               __float_as_uint(v[3])};
       *reinterpret_cast<u32x4_a4*>(p + 4) = u32x4{__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]),
@@ -114,7 +135,7 @@ __device__ __forceinline__ void store8(void* row, int col, int n, const float (&
     }
   } else {
     uint16_t* p = static_cast<uint16_t*>(row) + col;
-    if (n >= 8) {
+    if (WHOLE || n >= 8) {
       *reinterpret_cast<u32x4_a2*>(p) = u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
                                               pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
     } else {
@@ -197,11 +218,14 @@ __device__ __forceinline__ float lanes_sum(float v) {
   v += dpp_f32<kDppXor2>(v);
   v += dpp_f32<kDppHalfMirror>(v);
   v += dpp_f32<kDppMirror>(v);
-  if constexpr (LANES >= 32) v += __uint_as_float((uint32_t)__builtin_amdgcn_ds_swizzle((int)__float_as_uint(v), 0x401f));
+  // The swaps put each pair's values side by side: of 16 lanes, of 32.
+  if constexpr (LANES >= 32) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
   if constexpr (LANES == 64) {
-    const float a = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 0));
-    const float b = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 32));
-    v = a + b;
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
   }
   return v;
 }
@@ -221,20 +245,22 @@ __device__ __forceinline__ void row_sums(float (&v)[NV], float* lds, int& half) 
 #pragma unroll
     for (int i = 0; i < NV; ++i) v[i] = lanes_sum<LANES>(v[i]);
   } else {
+    // Lane i writes its wave's sum i; then 16 lanes take one sum's wave values each.
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, nw = blockDim.x >> 6;
     float* p = lds + half * (kRowSumMax * 16);
     half ^= 1;
+    float mine = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       v[i] = lanes_sum<64>(v[i]);
-      if (lane == 0) p[i * 16 + wave] = v[i];
+      mine = lane == i ? v[i] : mine;
     }
+    if (lane < NV) p[lane * 16 + wave] = mine;
     __syncthreads();
+    const float t = lanes_sum<16>((lane & 15) < nw && lane < NV * 16 ? p[lane] : 0.f);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int l = lane & 15;
-      v[i] = lanes_sum<16>(l < nw ? p[i * 16 + l] : 0.f);
-    }
+    for (int i = 0; i < NV; ++i)
+      v[i] = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(t), 16 * i));
   }
 }
 

@@ -89,10 +89,10 @@ __device__ __forceinline__ int stage_slot(int t, int s, int width) {
 }
 
 // Eight (q, scale) as bf16: exact, so the high halves of the fp32 products.
-__device__ __forceinline__ u32x4 widen_bf16(uint32_t w0, uint32_t w1, uint32_t scale_bits) {
+__device__ __forceinline__ u32x4 widen_bf16(uint32_t w0, uint32_t w1, uint32_t e) {
   Raw<kSrcP8> r;
   r.a = u32x2{w0, w1};
-  r.scale = scale_bits;
+  r.e = e;
   float v[8];
   widen<kSrcP8>(r, v);
   u32x4 o;
@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(C::kThreads) wgrad8_kernel(Args a) {
   u32x4 ra[C::kAPass];
   struct QRegs {
     u32x4 q;
-    uint32_t scale;
+    uint32_t e;
   } rb[C::kBPass];
   const int arow = tid / (BM / 8), acol = tid % (BM / 8) * 8, brow = tid / (BN / 16), bcol = tid % (BN / 16) * 16;
   const uint16_t* ap = a.dy + arow * a.dy_stride + m0 + acol;
@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(C::kThreads) wgrad8_kernel(Args a) {
 #pragma unroll
       for (int p = 0; p < C::kBPass; ++p) {
         rb[p].q = *reinterpret_cast<const u32x4*>(bp + (t0 + p * C::kBRows) * a.pitch);
-        rb[p].scale = (uint32_t)sp[(t0 + p * C::kBRows) * (a.pitch >> 5)] << 23;
+        rb[p].e = sp[(t0 + p * C::kBRows) * (a.pitch >> 5)];
       }
       return;
     }
@@ -209,10 +209,10 @@ __global__ void __launch_bounds__(C::kThreads) wgrad8_kernel(Args a) {
     for (int p = 0; p < C::kBPass; ++p) {
       const int64_t t = t0 + p * C::kBRows + brow;
       rb[p].q = u32x4{};
-      rb[p].scale = 0;
+      rb[p].e = 0;
       if (t < a.tokens && n0 + bcol < a.pitch) {  // the pitch is whole blocks of 32
         rb[p].q = *reinterpret_cast<const u32x4*>(bp + (t0 + p * C::kBRows) * a.pitch);
-        rb[p].scale = (uint32_t)sp[(t0 + p * C::kBRows) * (a.pitch >> 5)] << 23;
+        rb[p].e = sp[(t0 + p * C::kBRows) * (a.pitch >> 5)];
       }
     }
   };
@@ -226,8 +226,8 @@ __global__ void __launch_bounds__(C::kThreads) wgrad8_kernel(Args a) {
 #pragma unroll
     for (int p = 0; p < C::kBPass; ++p) {
       const int t = p * C::kBRows + tid / (BN / 16), s = tid % (BN / 16) * 2;
-      *reinterpret_cast<u32x4*>(sb + stage_slot(t, s, WB)) = widen_bf16(rb[p].q[0], rb[p].q[1], rb[p].scale);
-      *reinterpret_cast<u32x4*>(sb + stage_slot(t, s + 1, WB)) = widen_bf16(rb[p].q[2], rb[p].q[3], rb[p].scale);
+      *reinterpret_cast<u32x4*>(sb + stage_slot(t, s, WB)) = widen_bf16(rb[p].q[0], rb[p].q[1], rb[p].e);
+      *reinterpret_cast<u32x4*>(sb + stage_slot(t, s + 1, WB)) = widen_bf16(rb[p].q[2], rb[p].q[3], rb[p].e);
     }
   };
 
@@ -357,8 +357,8 @@ __global__ void __launch_bounds__(WM* WN * 64) wgrad8_dma_kernel(Args a) {
     return v;
   };
   auto put_x = [&](unsigned char* dst, const QRegs& v) {
-    *reinterpret_cast<u32x4*>(dst + xs0) = widen_bf16(v.q[0], v.q[1], v.e << 23);
-    *reinterpret_cast<u32x4*>(dst + xs1) = widen_bf16(v.q[2], v.q[3], v.e << 23);
+    *reinterpret_cast<u32x4*>(dst + xs0) = widen_bf16(v.q[0], v.q[1], v.e);
+    *reinterpret_cast<u32x4*>(dst + xs1) = widen_bf16(v.q[2], v.q[3], v.e);
   };
 
   f32x16 acc[TM][TN] = {};

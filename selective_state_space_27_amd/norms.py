@@ -13,11 +13,19 @@ stream).
 """
 from __future__ import annotations
 
+import contextlib
+import functools
+
 import torch
 
 import selective_state_space_27_amd as _mss
 
 _CODES = {torch.float32: 0, torch.bfloat16: 1}
+_HERE = contextlib.nullcontext()
+# The current stream's handle without a Stream object around it (1 us of a
+# call of 9); the public way where this torch lacks it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 class Packed8:
@@ -48,12 +56,11 @@ class Packed8:
 
 
 def _rows_cols(shape, name):
-    if len(shape) < 1 or any(n == 0 for n in shape):
+    cols = shape[-1] if len(shape) else 0
+    rows = shape.numel() // cols if cols else 0
+    if rows == 0:
         raise ValueError(f"{name} has shape {tuple(shape)}: at least one dimension, none of them empty")
-    rows = 1
-    for n in shape[:-1]:
-        rows *= n
-    return rows, shape[-1]
+    return rows, cols
 
 
 def _rows(t, name, shape, dtype, device):
@@ -69,16 +76,19 @@ def _rows(t, name, shape, dtype, device):
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     cols = shape[-1]
-    if cols > 1 and t.stride(-1) != 1:
+    if t.is_contiguous():
+        return t.data_ptr(), cols
+    strides = t.stride()
+    if cols > 1 and strides[-1] != 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
     rows, stride = 1, cols
-    for n, s in zip(reversed(shape[:-1]), reversed(t.stride()[:-1])):
+    for n, s in zip(reversed(shape[:-1]), reversed(strides[:-1])):
         if n == 1:
             continue
         if rows == 1:
             stride = s
         elif s != rows * stride:
-            raise ValueError(f"{name}: leading dimensions of {tuple(shape)} with strides {tuple(t.stride())} "
+            raise ValueError(f"{name}: leading dimensions of {tuple(shape)} with strides {tuple(strides)} "
                              "are not rows of one stride")
         rows *= n
     if stride < cols:
@@ -109,7 +119,9 @@ def _source(t, name, shape, dtype, device):
 def _vec(t, name, cols, device):
     if t is None:
         return None
-    _mss._check(t, name, (cols,), torch.float32, device)
+    if not (isinstance(t, torch.Tensor) and t.dtype == torch.float32 and t.shape == (cols,) and t.device == device and
+            t.is_contiguous()):
+        _mss._check(t, name, (cols,), torch.float32, device)
     return t.data_ptr()
 
 
@@ -120,51 +132,46 @@ def _code(dtype) -> int:
         raise TypeError(f"unsupported dtype {dtype} (float32 or bfloat16)") from None
 
 
-class _On:
-    """The stream and device a call runs on; allocations inside belong to them."""
-
-    __slots__ = ("stream", "_guards")
-
-    def __init__(self, stream, device):
-        self._guards = ()
-        if stream is None:
-            if device.index != torch.cuda.current_device():
-                self._guards = (torch.cuda.device(device),)
-            stream = torch.cuda.current_stream(device)
-        else:
-            if stream.device != device:
-                raise ValueError(f"stream is on {stream.device}, expected {device}")
-            self._guards = (torch.cuda.stream(stream),)
-        self.stream = stream.cuda_stream
-
-    def __enter__(self):
-        for g in self._guards:
-            g.__enter__()
-        return self
-
-    def __exit__(self, *exc):
-        for g in self._guards:
-            g.__exit__(*exc)
+def _on(stream, device):
+    """(stream handle, context) of a call: allocations inside the context belong
+    to the stream, launches to the device."""
+    if stream is None:
+        index = device.index
+        return _raw_stream(index), _HERE if index == torch.cuda.current_device() else torch.cuda.device(device)
+    if stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, expected {device}")
+    return stream.cuda_stream, torch.cuda.stream(stream)
 
 
-def _empty_packed(shape, dtype, device):
-    rows, cols = _rows_cols(shape, "shape")
-    pitch = -(-cols // 32) * 32
-    return Packed8(torch.empty((rows, pitch), dtype=torch.int8, device=device),
-                   torch.empty((rows, pitch // 32), dtype=torch.uint8, device=device), shape, dtype)
+def _empty_packed(rows, cols, shape, dtype, device):
+    blocks = (cols + 31) // 32
+    p = Packed8.__new__(Packed8)  # of the right make: nothing to check
+    p.q = torch.empty((rows, blocks * 32), dtype=torch.int8, device=device)
+    p.scale = torch.empty((rows, blocks), dtype=torch.uint8, device=device)
+    p.shape, p.dtype = shape, dtype
+    return p
 
 
 def _pq(p):
     return (None, None) if p is None else (p.q.data_ptr(), p.scale.data_ptr())
 
 
-def _result(given, name, shape, dtype, device):
-    """(tensor, pointer, stride) of an output, allocated unless given."""
+def _result(given, name, shape, dtype, device, like=None):
+    """(tensor, pointer, row stride) of an output, allocated unless given; `like`
+    an input of its shape, which makes that quicker where it fits."""
     if given is None:
-        t = torch.empty(shape, dtype=dtype, device=device)
+        if isinstance(like, torch.Tensor) and like.dtype == dtype and like.is_contiguous():
+            t = torch.empty_like(like)
+        else:
+            t = torch.empty(shape, dtype=dtype, device=device)
         return t, t.data_ptr(), shape[-1]
     p, stride = _rows(given, name, shape, dtype, device)
     return given, p, stride
+
+
+@functools.lru_cache(maxsize=256)
+def _workspace_size(query, *sizes):
+    return getattr(_mss.lib(), query)(*sizes)
 
 
 # ------------------------------------------------------- norm before a block
@@ -188,12 +195,13 @@ def add_norm_fwd(x, residual, weight, *, post_weight=None, gamma=None, scale=1.0
     rp, rs = _rows(residual, "residual", shape, rdt, dev)
     wp, pp, gp = (_vec(weight, "weight", cols, dev), _vec(post_weight, "post_weight", cols, dev),
                   _vec(gamma, "gamma", cols, dev))
-    with _On(stream, dev) as on:
-        out, op, os = _result(out, "out", shape, x.dtype, dev)
-        residual_out, qp, qs = _result(residual_out, "residual_out", shape, rdt, dev)
-        packed = _empty_packed(shape, x.dtype, dev) if pack_out else None
+    handle, here = _on(stream, dev)
+    with here:
+        out, op, os = _result(out, "out", shape, x.dtype, dev, x)
+        residual_out, qp, qs = _result(residual_out, "residual_out", shape, rdt, dev, residual)
+        packed = _empty_packed(rows, cols, shape, x.dtype, dev) if pack_out else None
         st = _mss.lib().mss_add_norm_fwd(xp, xs, rp, rs, wp, pp, gp, scale, eps, op, os, qp, qs, *_pq(packed), rows,
-                                         cols, io, res, 0, on.stream)
+                                         cols, io, res, 0, handle)
     _mss._raise(st, "mss_add_norm_fwd")
     return (out, residual_out, packed) if pack_out else (out, residual_out)
 
@@ -223,22 +231,22 @@ def add_norm_bwd(dout, residual_out, weight, *, dresidual_out=None, x=None, post
             raise ValueError("x is needed with post_weight or gamma")
         xp, xs, xsc = _source(x, "x", shape, dout.dtype, dev)
     ngrads = 1 + (pp is not None) + (gp is not None)
-    with _On(stream, dev) as on:
+    handle, here = _on(stream, dev)
+    with here:
         dxp = dxs = drp = drs = None
         if want_dx:
-            dx, dxp, dxs = _result(dx, "dx", shape, dout.dtype, dev)
+            dx, dxp, dxs = _result(dx, "dx", shape, dout.dtype, dev, dout)
         if want_dresidual:
-            dresidual, drp, drs = _result(dresidual, "dresidual", shape, rdt, dev)
-        grads = torch.empty((ngrads, cols), dtype=torch.float32, device=dev)
-        g = [grads[i] for i in range(ngrads)]
-        dw, dpost, dgamma = (g[0], g[1] if pp is not None else None, g[-1] if gp is not None else None)
-        need = _mss.lib().mss_add_norm_bwd_workspace_size(rows, cols, ngrads)
+            dresidual, drp, drs = _result(dresidual, "dresidual", shape, rdt, dev, residual_out)
+        dw = torch.empty_like(weight)
+        dpost, dgamma = (None if p is None else torch.empty_like(dw) for p in (pp, gp))
+        need = _workspace_size("mss_add_norm_bwd_workspace_size", rows, cols, ngrads)
         if need == 0:
             _mss._raise(5, "add_norm_bwd")
         ws = torch.empty(need, dtype=torch.uint8, device=dev)
         st = _mss.lib().mss_add_norm_bwd(dp, ds, ep, es, rp, rs, rsc, xp, xs or 0, xsc, wp, pp, gp, scale, eps, dxp,
                                          dxs or 0, drp, drs or 0, dw.data_ptr(), _mss._ptr(dpost), _mss._ptr(dgamma),
-                                         rows, cols, io, res, 0, ws.data_ptr(), need, on.stream)
+                                         rows, cols, io, res, 0, ws.data_ptr(), need, handle)
     _mss._raise(st, "mss_add_norm_bwd")
     return {"dx": dx if want_dx else None, "dresidual": dresidual if want_dresidual else None, "dweight": dw,
             "dpost_weight": dpost, "dgamma": dgamma}
@@ -265,13 +273,14 @@ def gated_norm_fwd(y, z, weight, *, ngroups=1, norm_first=False, eps=1e-5, out_d
     yp, ys = _rows(y, "y", shape, y.dtype, dev)
     zp, zs = _rows(z, "z", shape, odt, dev)
     wp = _vec(weight, "weight", cols, dev)
-    with _On(stream, dev) as on:
-        out, op, os = _result(out, "out", shape, odt, dev)
-        y8 = _empty_packed(shape, y.dtype, dev) if pack_inputs else None
-        z8 = _empty_packed(shape, odt, dev) if pack_inputs and z is not None else None
-        out8 = _empty_packed(shape, odt, dev) if pack_out else None
+    handle, here = _on(stream, dev)
+    with here:
+        out, op, os = _result(out, "out", shape, odt, dev, y)
+        y8 = _empty_packed(rows, cols, shape, y.dtype, dev) if pack_inputs else None
+        z8 = _empty_packed(rows, cols, shape, odt, dev) if pack_inputs and z is not None else None
+        out8 = _empty_packed(rows, cols, shape, odt, dev) if pack_out else None
         st = _mss.lib().mss_gated_norm_fwd(yp, ys, zp, zs, wp, eps, op, os, *_pq(y8), *_pq(z8), *_pq(out8), rows, cols,
-                                           ngroups, wide, io, _mss.MSS_FLAG_NORM_FIRST if norm_first else 0, on.stream)
+                                           ngroups, wide, io, _mss.MSS_FLAG_NORM_FIRST if norm_first else 0, handle)
     _mss._raise(st, "mss_gated_norm_fwd")
     if not pack_inputs and not pack_out:
         return out
@@ -291,19 +300,20 @@ def gated_norm_bwd(dout, y, z, weight, *, ngroups=1, norm_first=False, eps=1e-5,
     yp, ys, ysc = _source(y, "y", shape, y.dtype, dev)
     zp, zs, zsc = _source(z, "z", shape, dout.dtype, dev)
     wp = _vec(weight, "weight", cols, dev)
-    with _On(stream, dev) as on:
-        dy, dyp, dys = _result(dy, "dy", shape, y.dtype, dev)
+    handle, here = _on(stream, dev)
+    with here:
+        dy, dyp, dys = _result(dy, "dy", shape, y.dtype, dev, y)
         dzp = dzs = None
         if z is not None:
-            dz, dzp, dzs = _result(dz, "dz", shape, dout.dtype, dev)
-        dw = torch.empty(cols, dtype=torch.float32, device=dev)
-        need = _mss.lib().mss_gated_norm_bwd_workspace_size(rows, cols, ngroups)
+            dz, dzp, dzs = _result(dz, "dz", shape, dout.dtype, dev, dout)
+        dw = torch.empty_like(weight)
+        need = _workspace_size("mss_gated_norm_bwd_workspace_size", rows, cols, ngroups)
         if need == 0:
             _mss._raise(5, "gated_norm_bwd")
         ws = torch.empty(need, dtype=torch.uint8, device=dev)
         st = _mss.lib().mss_gated_norm_bwd(dp, ds, yp, ys, ysc, zp, zs, zsc, wp, eps, dyp, dys, dzp, dzs or 0,
                                            dw.data_ptr(), rows, cols, ngroups, wide, io,
-                                           _mss.MSS_FLAG_NORM_FIRST if norm_first else 0, ws.data_ptr(), need, on.stream)
+                                           _mss.MSS_FLAG_NORM_FIRST if norm_first else 0, ws.data_ptr(), need, handle)
     _mss._raise(st, "mss_gated_norm_bwd")
     return {"dy": dy, "dz": dz if z is not None else None, "dweight": dw}
 
@@ -317,9 +327,10 @@ def pack8(x, *, stream=None) -> Packed8:
     rows, cols = _rows_cols(x.shape, "x")
     code = _code(x.dtype)
     xp, xs = _rows(x, "x", x.shape, x.dtype, dev)
-    with _On(stream, dev) as on:
-        p = _empty_packed(x.shape, x.dtype, dev)
-        st = _mss.lib().mss_pack8(xp, xs, *_pq(p), rows, cols, code, on.stream)
+    handle, here = _on(stream, dev)
+    with here:
+        p = _empty_packed(rows, cols, x.shape, x.dtype, dev)
+        st = _mss.lib().mss_pack8(xp, xs, *_pq(p), rows, cols, code, handle)
     _mss._raise(st, "mss_pack8")
     return p
 
@@ -332,9 +343,10 @@ def unpack8(p, dtype=None, *, out=None, stream=None):
     dtype = dtype if dtype is not None else p.dtype
     code = _code(dtype)
     rows, cols = _rows_cols(p.shape, "p")
-    with _On(stream, dev) as on:
+    handle, here = _on(stream, dev)
+    with here:
         out, op, os = _result(out, "out", p.shape, dtype, dev)
-        st = _mss.lib().mss_unpack8(*_pq(p), op, os, rows, cols, code, on.stream)
+        st = _mss.lib().mss_unpack8(*_pq(p), op, os, rows, cols, code, handle)
     _mss._raise(st, "mss_unpack8")
     return out
 
@@ -357,15 +369,16 @@ def wgrad8(dy, x8, *, out=None, out_dtype=torch.float32, accumulate=False, strea
         raise ValueError("accumulate needs out")
     dtype = out.dtype if out is not None else out_dtype
     dcode = _code(dtype)
-    with _On(stream, dev) as on:
+    handle, here = _on(stream, dev)
+    with here:
         if out is None:
             out = torch.empty((outs, ins), dtype=dtype, device=dev)
         _mss._check(out, "out", (outs, ins), dtype, dev)
-        need = _mss.lib().mss_wgrad8_workspace_size(tokens, outs, ins)
+        need = _workspace_size("mss_wgrad8_workspace_size", tokens, outs, ins)
         if need == 0:
             _mss._raise(2, "wgrad8")
         ws = torch.empty(need, dtype=torch.uint8, device=dev)
         st = _mss.lib().mss_wgrad8(dp, ds, q, s, out.data_ptr(), tokens, outs, ins, code, dcode,
-                                   _mss.MSS_FLAG_ACCUMULATE if accumulate else 0, ws.data_ptr(), need, on.stream)
+                                   _mss.MSS_FLAG_ACCUMULATE if accumulate else 0, ws.data_ptr(), need, handle)
     _mss._raise(st, "mss_wgrad8")
     return out
