@@ -597,7 +597,8 @@ mss_status mss_unpack8(const int8_t* q, const uint8_t* scale, void* x, int64_t x
 /*   q, scale: the form of mss_pack8 of a [tokens, ins] tensor;              */
 /*   dw [outs, ins] dw_dtype.                                                */
 /* Supported: outs and ins up to 2^20, outs * ins up to 2^34, tokens up to   */
-/* 2^35, tokens * dy_stride below 2^47 (else MSS_ERR_SHAPE); dy_dtype        */
+/* 2^35, tokens * (outs + 7) below 2^36, tokens * dy_stride below 2^47 (else */
+/* MSS_ERR_SHAPE); dy_dtype                                                  */
 /* MSS_BF16 (else MSS_ERR_UNSUPPORTED: fp32 gradients would have to be       */
 /* rounded).  dw 16-byte aligned; it must not overlap an input.  `workspace` */
 /* needs mss_wgrad8_workspace_size() bytes, 16-byte aligned.                 */
@@ -607,8 +608,12 @@ mss_status mss_wgrad8(const void* dy, int64_t dy_stride, const int8_t* q, const 
                       mss_dtype dw_dtype, uint32_t flags, void* workspace, size_t workspace_bytes,
                       void* hip_stream);
 
-/* Bytes of device workspace mss_wgrad8 needs (0 when unsupported). */
-size_t mss_wgrad8_workspace_size(int64_t tokens, int64_t outs, int64_t ins);
+/* Bytes of device workspace mss_wgrad8 needs (0 when unsupported).  Of dy only
+ * the address's alignment counts: rows that are not 16-byte aligned whole
+ * vectors of eight (or lie over 2^23 elements apart) are first copied to the
+ * workspace, which is then larger by tokens * outs bf16. */
+size_t mss_wgrad8_workspace_size(const void* dy, int64_t dy_stride, int64_t tokens, int64_t outs,
+                                 int64_t ins);
 
 /* ------------------------------------------------------------------------ */
 /* Status of a call that used `workspace`.                                   */

@@ -145,7 +145,7 @@ def lib() -> ctypes.CDLL:
     L.mss_unpack8.restype = ci
     L.mss_wgrad8.argtypes = [vp, i64, vp, vp, vp, i64, i64, i64, ci, ci, u32, vp, sz, vp]
     L.mss_wgrad8.restype = ci
-    L.mss_wgrad8_workspace_size.argtypes = [i64, i64, i64]
+    L.mss_wgrad8_workspace_size.argtypes = [vp, i64, i64, i64, i64]
     L.mss_wgrad8_workspace_size.restype = sz
     L.mss_workspace_status.argtypes = [vp, vp]
     L.mss_workspace_status.restype = ctypes.c_int

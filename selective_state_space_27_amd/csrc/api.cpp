@@ -1067,13 +1067,14 @@ mss_status mss_unpack8(const int8_t* q, const uint8_t* scale, void* x, int64_t x
   return hip_status(mss::launch_unpack8(p, static_cast<hipStream_t>(hip_stream)));
 }
 
+// (A launch of the copy that aligns dy holds fewer than 2^32 threads, each of four vectors of eight.)
 static bool wgrad8_shape_ok(int64_t tokens, int64_t outs, int64_t ins) {
   return tokens > 0 && outs > 0 && ins > 0 && tokens <= (1LL << 35) && outs <= (1LL << 20) && ins <= (1LL << 20) &&
-         outs * ins <= (1LL << 34);
+         outs * ins <= (1LL << 34) && tokens < (1LL << 36) / (outs + 7);
 }
 
-size_t mss_wgrad8_workspace_size(int64_t tokens, int64_t outs, int64_t ins) {
-  return wgrad8_shape_ok(tokens, outs, ins) ? mss::wgrad8_workspace_bytes(tokens, outs, ins) : 0;
+size_t mss_wgrad8_workspace_size(const void* dy, int64_t dy_stride, int64_t tokens, int64_t outs, int64_t ins) {
+  return wgrad8_shape_ok(tokens, outs, ins) ? mss::wgrad8_workspace_bytes(dy, dy_stride, tokens, outs, ins) : 0;
 }
 
 mss_status mss_wgrad8(const void* dy, int64_t dy_stride, const int8_t* q, const uint8_t* scale, void* dw,
@@ -1084,7 +1085,7 @@ mss_status mss_wgrad8(const void* dy, int64_t dy_stride, const int8_t* q, const 
   if (!wgrad8_shape_ok(tokens, outs, ins) || !stride_ok(dy, dy_stride, tokens, outs)) return MSS_ERR_SHAPE;
   if (dy_dtype != MSS_BF16 || (flags & ~MSS_FLAG_ACCUMULATE)) return MSS_ERR_UNSUPPORTED;
   if (!elem_aligned(dy, dy_dtype) || !aligned16(q) || !aligned16(dw) || !aligned16(workspace)) return MSS_ERR_ALIGN;
-  const size_t need = mss::wgrad8_workspace_bytes(tokens, outs, ins);
+  const size_t need = mss::wgrad8_workspace_bytes(dy, dy_stride, tokens, outs, ins);
   if (!workspace || workspace_bytes < need) return MSS_ERR_WORKSPACE;
   const RowSet in[] = {row_set(dy, dy_stride, tokens, outs, dy_dtype), q_set(q, tokens, ins),
                        scale_set(scale, tokens, ins), dense_set(workspace, (int64_t)need)};

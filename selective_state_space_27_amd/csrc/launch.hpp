@@ -303,7 +303,7 @@ struct Wgrad8Params {
   bool accumulate;
   void* workspace;
 };
-size_t wgrad8_workspace_bytes(int64_t tokens, int64_t outs, int64_t ins);
+size_t wgrad8_workspace_bytes(const void* dy, int64_t dy_stride, int64_t tokens, int64_t outs, int64_t ins);
 hipError_t launch_wgrad8(const Wgrad8Params& p, hipStream_t stream);
 
 }  // namespace mss

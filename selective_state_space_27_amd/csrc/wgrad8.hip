@@ -38,17 +38,18 @@ namespace {
 using ssd::f32x16;
 using ssd::mfma;
 
-constexpr int kBK = 32;  // steps of a stage
+constexpr int kDK = 32;  // steps of a stage
 
 struct Args {
   const uint16_t* dy;
   const int8_t* q;
   const uint8_t* scale;
   void* dw;
-  float* part;  // [cut][splits][BM][BN]
+  float* part;  // [cut][splits][BM][BN], 16-byte aligned
   int64_t dy_stride;
   int64_t tokens;
   int outs, ins, pitch;
+  int acols;      // outs in whole vectors of eight: what a row of dy holds
   int mt, nt;     // tiles
   int whole;      // tiles taken whole, before the cut ones
   int splits;
@@ -74,14 +75,6 @@ __host__ __device__ __forceinline__ void tile_at(int mt, int nt, int i, int& m, 
   n = r / rows;
   m = band * 8 + r - n * rows;
 }
-
-template <int WM, int WN, int TM, int TN>  // waves, and 32 x 32 tiles of a wave
-struct Cfg {
-  static constexpr int kThreads = WM * WN * 64, BM = WM * TM * 32, BN = WN * TN * 32;
-  static constexpr int kARows = kThreads * 8 / BM;  // rows of dY a pass of 16-byte loads covers
-  static constexpr int kBRows = kThreads * 16 / BN; // rows of q
-  static constexpr int kAPass = kBK / kARows, kBPass = kBK / kBRows;
-};
 
 // Byte offset of 16-byte slot `s` of staged row t of `width` bytes.
 __device__ __forceinline__ int stage_slot(int t, int s, int width) {
@@ -166,123 +159,38 @@ __device__ __forceinline__ void write_tile(const Args& a, const Item& it, const 
   });
 }
 
-// Any alignment and stride of dY's rows: through registers, one stage ahead.
-template <typename C, int WM, int WN, int TM, int TN>
-__global__ void __launch_bounds__(C::kThreads) wgrad8_kernel(Args a) {
-  constexpr int BM = C::BM, BN = C::BN, WA = BM * 2, WB = BN * 2;
-  constexpr int kStage = kBK * (WA + WB);  // [kBK][BM] of dY, [kBK][BN] of X, bf16
-  __shared__ __align__(16) unsigned char smem[2 * kStage];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  if (blockIdx.x == 0 && tid == 0) *a.status = 0;
-  const Item it = item_of(a);
-  const int m0 = it.m * BM, n0 = it.n * BN, first = it.first, last = it.last;
-
-  u32x4 ra[C::kAPass];
-  struct QRegs {
-    u32x4 q;
-    uint32_t e;
-  } rb[C::kBPass];
-  const int arow = tid / (BM / 8), acol = tid % (BM / 8) * 8, brow = tid / (BN / 16), bcol = tid % (BN / 16) * 16;
-  const uint16_t* ap = a.dy + arow * a.dy_stride + m0 + acol;
-  const int8_t* bp = a.q + (int64_t)brow * a.pitch + n0 + bcol;
-  const uint8_t* sp = a.scale + (int64_t)brow * (a.pitch >> 5) + ((n0 + bcol) >> 5);
-  const bool inside = m0 + BM <= a.outs && n0 + BN <= a.pitch;
-  auto fetch = [&](int st) {
-    const int64_t t0 = (int64_t)st * kBK;
-    if (inside && t0 + kBK <= a.tokens) {
+// dY's rows copied to aligned ones of whole vectors of eight (zeros past the
+// last column), for rows that cannot go into LDS as they lie: 16-byte transfers
+// need 16-byte aligned rows, and a last vector that ends with the row must not
+// be read past it.  Reading and writing dY once costs less than the product
+// through registers did: 32768 x 10575 x 2560 2.61 ms that way.
+__global__ void __launch_bounds__(256) wgrad8_align_kernel(const uint16_t* src, int64_t stride, uint16_t* dst,
+                                                           int64_t tokens, int outs, uint32_t vecs) {
+  constexpr int kVecs = 4;
+  const int64_t first = (int64_t)blockIdx.x * (256 * kVecs), row0 = first / vecs;
+  const uint32_t rem0 = (uint32_t)(first - row0 * vecs);
+  u32x4 v[kVecs];
+  int64_t row[kVecs];
+  int col[kVecs];
 #pragma unroll
-      for (int p = 0; p < C::kAPass; ++p)
-        ra[p] = *reinterpret_cast<const u32x4_a2*>(ap + (t0 + p * C::kARows) * a.dy_stride);
-#pragma unroll
-      for (int p = 0; p < C::kBPass; ++p) {
-        rb[p].q = *reinterpret_cast<const u32x4*>(bp + (t0 + p * C::kBRows) * a.pitch);
-        rb[p].e = sp[(t0 + p * C::kBRows) * (a.pitch >> 5)];
-      }
-      return;
-    }
-#pragma unroll
-    for (int p = 0; p < C::kAPass; ++p) {
-      const int64_t t = t0 + p * C::kARows + arow;
-      ra[p] = load_raw<kSrcBf16>(a.dy + t * a.dy_stride, nullptr, m0 + acol, t < a.tokens ? a.outs - m0 - acol : 0).a;
-    }
-#pragma unroll
-    for (int p = 0; p < C::kBPass; ++p) {
-      const int64_t t = t0 + p * C::kBRows + brow;
-      rb[p].q = u32x4{};
-      rb[p].e = 0;
-      if (t < a.tokens && n0 + bcol < a.pitch) {  // the pitch is whole blocks of 32
-        rb[p].q = *reinterpret_cast<const u32x4*>(bp + (t0 + p * C::kBRows) * a.pitch);
-        rb[p].e = sp[(t0 + p * C::kBRows) * (a.pitch >> 5)];
-      }
-    }
-  };
-  auto commit = [&](unsigned char* st) {
-#pragma unroll
-    for (int p = 0; p < C::kAPass; ++p) {
-      const int t = p * C::kARows + tid / (BM / 8);
-      *reinterpret_cast<u32x4*>(st + stage_slot(t, tid % (BM / 8), WA)) = ra[p];
-    }
-    unsigned char* sb = st + kBK * WA;
-#pragma unroll
-    for (int p = 0; p < C::kBPass; ++p) {
-      const int t = p * C::kBRows + tid / (BN / 16), s = tid % (BN / 16) * 2;
-      *reinterpret_cast<u32x4*>(sb + stage_slot(t, s, WB)) = widen_bf16(rb[p].q[0], rb[p].q[1], rb[p].e);
-      *reinterpret_cast<u32x4*>(sb + stage_slot(t, s + 1, WB)) = widen_bf16(rb[p].q[2], rb[p].q[3], rb[p].e);
-    }
-  };
-
-  f32x16 acc[TM][TN] = {};
-  const int wm = wave / WN * (TM * 32), wn = wave % WN * (TN * 32);
-  const int i16 = lane & 15, hf = lane >> 5, gc = (lane >> 4) & 1;
-  // Steps kk*16 + 8 hf .. + 8 of column base + lane % 32 (base a multiple of
-  // 32): two transposing reads of four rows.  Lane i of a 16-lane group
-  // addresses row i / 4 of the four, columns 4 (i % 4) .. + 4 of the group's 16.
-  typedef short v4s __attribute__((ext_vector_type(4)));
-  auto frag = [&](const unsigned char* st, int kk, int base, int width) -> u32x4 {
-    const int t = kk * 16 + 8 * hf + (i16 >> 2);
-    const unsigned char* p = st + t * width + ((base >> 5) ^ (i16 >> 2)) * 64 + gc * 32 + (i16 & 3) * 8;
-    const u32x2 lo = __builtin_bit_cast(
-        u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)(p)));
-    const u32x2 hi = __builtin_bit_cast(
-        u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)(p + 4 * width)));
-    return u32x4{lo[0], lo[1], hi[0], hi[1]};
-  };
-
-  if (first < last) {
-    fetch(first);
-    commit(smem);
+  for (int i = 0; i < kVecs; ++i) {
+    const uint32_t t = rem0 + i * 256 + threadIdx.x, r = t / vecs;
+    row[i] = row0 + r;
+    col[i] = (int)(t - r * vecs) * 8;
+    v[i] = load_raw<kSrcBf16>(src + row[i] * stride, nullptr, col[i], row[i] < tokens ? outs - col[i] : 0).a;
   }
-  for (int st = first; st < last; ++st) {
-    unsigned char* cur = smem + ((st - first) & 1) * kStage;
-    __syncthreads();  // this stage is written, and the other one read
-    if (st + 1 < last) fetch(st + 1);
 #pragma unroll
-    for (int kk = 0; kk < kBK / 16; ++kk) {
-      u32x4 fa[TM], fb[TN];
-#pragma unroll
-      for (int i = 0; i < TM; ++i) fa[i] = frag(cur, kk, wm + 32 * i, WA);
-#pragma unroll
-      for (int j = 0; j < TN; ++j) fb[j] = frag(cur + kBK * WA, kk, wn + 32 * j, WB);
-#pragma unroll
-      for (int i = 0; i < TM; ++i)
-#pragma unroll
-        for (int j = 0; j < TN; ++j) acc[i][j] = mfma(fa[i], fb[j], acc[i][j]);
-    }
-    if (st + 1 < last) commit(smem + ((st + 1 - first) & 1) * kStage);
-  }
-  write_tile<BM, BN, TM, TN>(a, it, acc, wm + 4 * hf, wn + (lane & 31));
+  for (int i = 0; i < kVecs; ++i)
+    if (row[i] < tokens) *reinterpret_cast<u32x4*>(dst + row[i] * ((int64_t)vecs * 8) + col[i]) = v[i];
 }
 
-// The same product where dY's rows are 16-byte aligned, whole vectors of
-// eight, and at most 2^23 elements apart: dY goes from memory straight into LDS.
-constexpr int kDK = kBK;  // steps of a stage
-constexpr int kNA = 6;    // staged tiles of dY
-constexpr int kNX = 3;    // ... of X
+// Six staged tiles of dY and three of X.  dY's rows are 16-byte aligned, whole
+// vectors of eight and at most 2^23 elements apart.
 // vmcnt limit (bits 3:0 and 15:14), the other counters not waited for.
 constexpr int vmcnt(int n) { return (n & 15) | ((n >> 4) << 14) | (7 << 4) | (15 << 8); }
 
 template <int WM, int WN, int TM, int TN>
-__global__ void __launch_bounds__(WM* WN * 64) wgrad8_dma_kernel(Args a) {
+__global__ void __launch_bounds__(WM* WN * 64) wgrad8_kernel(Args a) {
   constexpr int BM = WM * TM * 32, BN = WN * TN * 32, WA = BM * 2, WB = BN * 2;
   constexpr int kTA = kDK * WA, kTX = kDK * WB;
   constexpr int kPieces = kTA / 1024 / (WM * WN);  // 1 KB transfers of a wave and stage
@@ -325,7 +233,7 @@ __global__ void __launch_bounds__(WM* WN * 64) wgrad8_dma_kernel(Args a) {
     uint32_t bytes = kOpen;
     if constexpr (!open.value) {
       const int n = (int)max(min(left_a, (int64_t)64), (int64_t)0);
-      if (n < 64) bytes = n == 0 ? 0u : ((uint32_t)(n - 1) * (uint32_t)a.dy_stride + (uint32_t)(a.outs - m0)) * 2u;
+      if (n < 64) bytes = n == 0 ? 0u : ((uint32_t)(n - 1) * (uint32_t)a.dy_stride + (uint32_t)(a.acols - m0)) * 2u;
       left_a -= kDK;
     }
     const rsrc_t r = make_rsrc(pa, bytes);
@@ -507,7 +415,7 @@ Plan plan_of(int64_t tokens, int64_t outs, int64_t ins) {
   const int bt = p.big ? 256 : 128, slots = p.big ? 256 : 512;
   p.mt = (int)((outs + bt - 1) / bt);
   p.nt = (int)((ins + bt - 1) / bt);
-  p.stages = (int)((tokens + kBK - 1) / kBK);
+  p.stages = (int)((tokens + kDK - 1) / kDK);
   const int tiles = p.mt * p.nt, rest = tiles % slots;
   p.whole = tiles - rest;
   // Parts of the tiles past the last full round: the number that takes the
@@ -527,42 +435,58 @@ Plan plan_of(int64_t tokens, int64_t outs, int64_t ins) {
   return p;
 }
 
+// Whether dY's rows can go into LDS as they lie.
+bool direct(const void* dy, int64_t dy_stride, int64_t outs) {
+  return (reinterpret_cast<uintptr_t>(dy) & 15) == 0 && dy_stride % 8 == 0 && outs % 8 == 0 && dy_stride <= (1 << 23);
+}
+
+size_t parts_bytes(const Plan& p) {
+  const size_t tile = p.big ? 256 * 256 : 128 * 128;
+  return (size_t)(p.mt * p.nt - p.whole) * (size_t)p.splits * tile * sizeof(float);
+}
+
 template <int WM, int WN, int TM, int TN>
 hipError_t launch_cfg(const Args& a, hipStream_t stream) {
-  typedef Cfg<WM, WN, TM, TN> C;
+  constexpr int BM = WM * TM * 32, BN = WN * TN * 32;
   const int cut = a.mt * a.nt - a.whole;
-  const dim3 grid((unsigned)(a.whole + cut * a.splits)), block(C::kThreads);
-  if ((reinterpret_cast<uintptr_t>(a.dy) & 15) == 0 && a.dy_stride % 8 == 0 && a.outs % 8 == 0 &&
-      a.dy_stride <= (1 << 23))
-    hipLaunchKernelGGL((wgrad8_dma_kernel<WM, WN, TM, TN>), grid, block, 0, stream, a);
-  else
-    hipLaunchKernelGGL((wgrad8_kernel<C, WM, WN, TM, TN>), grid, block, 0, stream, a);
+  hipLaunchKernelGGL((wgrad8_kernel<WM, WN, TM, TN>), dim3((unsigned)(a.whole + cut * a.splits)), dim3(WM * WN * 64), 0,
+                     stream, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || cut == 0) return e;
-  hipLaunchKernelGGL((wgrad8_join_kernel<C::BM, C::BN>), dim3(C::BM * C::BN / 1024, (unsigned)cut), dim3(256),
-                     0, stream, a);
+  hipLaunchKernelGGL((wgrad8_join_kernel<BM, BN>), dim3(BM * BN / 1024, (unsigned)cut), dim3(256), 0, stream, a);
   return hipGetLastError();
 }
 
 }  // namespace
 
-size_t wgrad8_workspace_bytes(int64_t tokens, int64_t outs, int64_t ins) {
-  const Plan p = plan_of(tokens, outs, ins);
-  const size_t tile = p.big ? 256 * 256 : 128 * 128;
-  return 256 + (size_t)(p.mt * p.nt - p.whole) * (size_t)p.splits * tile * sizeof(float);
+size_t wgrad8_workspace_bytes(const void* dy, int64_t dy_stride, int64_t tokens, int64_t outs, int64_t ins) {
+  const size_t copy = direct(dy, dy_stride, outs) ? 0 : (size_t)tokens * (size_t)((outs + 7) / 8 * 16);
+  return 256 + parts_bytes(plan_of(tokens, outs, ins)) + copy;
 }
 
 hipError_t launch_wgrad8(const Wgrad8Params& p, hipStream_t stream) {
   const Plan pl = plan_of(p.tokens, p.outs, p.ins);
+  char* ws = static_cast<char*>(p.workspace);
   Args a;
   a.dy = static_cast<const uint16_t*>(p.dy);
+  a.dy_stride = p.dy_stride;
+  if (!direct(p.dy, p.dy_stride, p.outs)) {
+    uint16_t* copy = reinterpret_cast<uint16_t*>(ws + 256 + parts_bytes(pl));
+    const uint32_t vecs = (uint32_t)((p.outs + 7) / 8);
+    hipLaunchKernelGGL(wgrad8_align_kernel, dim3((unsigned)((p.tokens * vecs + 1023) / 1024)), dim3(256), 0, stream, a.dy,
+                       p.dy_stride, copy, p.tokens, (int)p.outs, vecs);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    a.dy = copy;
+    a.dy_stride = (int64_t)vecs * 8;
+  }
   a.q = p.q;
   a.scale = p.scale;
   a.dw = p.dw;
-  a.part = reinterpret_cast<float*>(static_cast<char*>(p.workspace) + 256);
-  a.dy_stride = p.dy_stride;
+  a.part = reinterpret_cast<float*>(ws + 256);
   a.tokens = p.tokens;
   a.outs = (int)p.outs;
+  a.acols = (int)((p.outs + 7) / 8 * 8);
   a.ins = (int)p.ins;
   a.pitch = (int)((p.ins + 31) / 32 * 32);
   a.mt = pl.mt, a.nt = pl.nt, a.whole = pl.whole, a.splits = pl.splits, a.stages = pl.stages;

@@ -374,7 +374,7 @@ def wgrad8(dy, x8, *, out=None, out_dtype=torch.float32, accumulate=False, strea
         if out is None:
             out = torch.empty((outs, ins), dtype=dtype, device=dev)
         _mss._check(out, "out", (outs, ins), dtype, dev)
-        need = _workspace_size("mss_wgrad8_workspace_size", tokens, outs, ins)
+        need = _mss.lib().mss_wgrad8_workspace_size(dp, ds, tokens, outs, ins)
         if need == 0:
             _mss._raise(2, "wgrad8")
         ws = torch.empty(need, dtype=torch.uint8, device=dev)

@@ -193,7 +193,7 @@ def test_pack8_outputs_apart():
 
 def wgrad(**kw):
     d = dict(dy=P(0), ds=48, q=P(1), s=P(2), dw=P(3), tokens=100, outs=48, ins=40, dydt=BF16, dwdt=FP32, flags=0,
-             ws=P(4), wsb=mss.lib().mss_wgrad8_workspace_size(100, 48, 40), stream=None)
+             ws=P(4), wsb=mss.lib().mss_wgrad8_workspace_size(P(0), 48, 100, 48, 40), stream=None)
     return call("mss_wgrad8", d, list(d), **kw)
 
 
@@ -216,7 +216,13 @@ def test_wgrad8_refusals():
     assert wgrad(wsb=0) == WS
     assert wgrad(dw=P(0)) == ALIAS
     assert wgrad(dw=P(4)) == ALIAS
-    assert mss.lib().mss_wgrad8_workspace_size(0, 1, 1) == 0
+    assert wgrad(tokens=1 << 31, ds=48) == SHAPE            # more than 2^32 threads of the copy
+    size = mss.lib().mss_wgrad8_workspace_size
+    assert size(P(0), 1, 0, 1, 1) == 0
+    # rows that cannot be read as they lie need room for their copy
+    apart = [size(P(0, 2), 48, 100, 48, 40), size(P(0), 52, 100, 48, 40), size(P(0), 1 << 24, 100, 48, 40)]
+    assert all(n == size(P(0), 48, 100, 48, 40) + 100 * 48 * 2 for n in apart)
+    assert wgrad(dy=P(0, 2)) == WS                          # sized for aligned rows
 
 
 def test_binding_refuses_cpu_tensors_and_empty_shapes():
