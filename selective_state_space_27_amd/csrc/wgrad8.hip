@@ -404,35 +404,46 @@ __global__ void __launch_bounds__(256) wgrad8_join_kernel(Args a) {
 
 // How a product is laid over the card.
 struct Plan {
-  bool big;  // 256 x 256 tiles (one workgroup per CU), else 128 x 128 (two)
+  bool big;  // 256 x 256 tiles (one workgroup on a CU), else 128 x 128 (two)
   int mt, nt, whole, splits, stages;
+  double us;  // estimate
 };
 
-Plan plan_of(int64_t tokens, int64_t outs, int64_t ins) {
+// Tiles of one size.  The tiles past the last full round are cut along t into
+// the number of parts that takes the least time: a CU takes 0.88 us for a stage
+// of a 256-wide tile and 0.28 us for one of a 128-wide (whether it holds one or
+// two of them), a round 3 us to start, the join 3 us and the parts' sums, written
+// and read, 5 TB/s; a part has 8 stages or more.  (Counting rounds alone cut the
+// in_proj shape above in 14 where 3 is best: 1.69 ms.)
+Plan plan_with(bool big, int64_t tokens, int64_t outs, int64_t ins) {
   Plan p;
-  const int64_t t256 = ((outs + 255) / 256) * ((ins + 255) / 256);
-  p.big = t256 >= 128;
-  const int bt = p.big ? 256 : 128, slots = p.big ? 256 : 512;
+  p.big = big;
+  const int bt = big ? 256 : 128, slots = big ? 256 : 512;
+  const double stage = big ? 0.88 : 0.28, join = (double)(bt * bt) * 8 / 5e6;
   p.mt = (int)((outs + bt - 1) / bt);
   p.nt = (int)((ins + bt - 1) / bt);
   p.stages = (int)((tokens + kDK - 1) / kDK);
   const int tiles = p.mt * p.nt, rest = tiles % slots;
   p.whole = tiles - rest;
-  // Parts of the tiles past the last full round: the number that takes the
-  // least time by rounds of parts (a stage takes 0.9 us, with two workgroups of
-  // 128-wide tiles on a CU 0.55 us), 3 us to start a round, and writing and
-  // reading the parts' sums at 5 TB/s; a part has 8 stages or more.  (Counting
-  // rounds alone cut the in_proj shape above in 14 where 3 is best: 1.69 ms.)
-  const double stage = p.big ? 0.9 : 0.55, join = (p.big ? 256 * 256 : 128 * 128) * 8 / 5e6;
-  double best = 1e30;
-  p.splits = 1;
-  for (int s = 1; s <= 64 && (s == 1 || s * 8 <= p.stages); ++s) {
-    const int rounds = (rest * s + slots - 1) / slots;
-    const double us = rounds * ((double)p.stages / s * stage + 3.0) + (s > 1 ? rest * s * join : 0.0);
-    if (us < best) best = us, p.splits = s;
+  const double before = p.whole / 256 * (p.stages * stage);
+  p.us = 1e30;
+  for (int s = 1; s <= 128 && (s == 1 || s * 8 <= p.stages); ++s) {
+    const int parts = rest * s;
+    const double us = before + 3.0 + (double)((parts + 255) / 256) * ((double)p.stages / s * stage) +
+                      (s > 1 ? 3.0 + parts * join : 0.0);
+    if (us < p.us) p.us = us, p.splits = s;
   }
   if (p.splits == 1) p.whole = tiles;
   return p;
+}
+
+// The layout with the smaller estimate: 256-wide tiles where there are enough of
+// them or long enough sums (32768 x 2560 x 768: 131 us, 128-wide 158), 128-wide
+// ones for little work (4096 x 2048 x 2048: 51 us, 256-wide 56; 8191 x 768 x
+// 1536: 36 and 42).
+Plan plan_of(int64_t tokens, int64_t outs, int64_t ins) {
+  const Plan a = plan_with(true, tokens, outs, ins), b = plan_with(false, tokens, outs, ins);
+  return a.us <= b.us ? a : b;
 }
 
 // Whether dY's rows can go into LDS as they lie.

@@ -143,9 +143,10 @@ def test_wgrad(tokens, outs, ins, dw):
 
 
 @pytest.mark.parametrize("tokens,outs,ins", [(300, 4112, 2050), (129, 3000, 4000), (1000, 5000, 2601),
-                                             (70, 4001, 2050), (31, 2816, 3000)])
+                                             (70, 4001, 2050), (31, 2816, 3000), (1500, 4000, 3900),
+                                             (1470, 4007, 3833), (32768, 1296, 1020), (32007, 1290, 1020)])
 def test_wgrad_large_tiles(tokens, outs, ins):
-    """Enough 256-wide tiles for that layout, borders inside them."""
+    """Sizes for 256-wide tiles, whole and cut along the tokens, borders inside them."""
     g = gen(tokens)
     dy = torch.randint(-3, 4, (tokens, outs), generator=g, device="cuda:0").bfloat16()
     x = torch.randint(-100, 101, (tokens, ins), generator=g, device="cuda:0").bfloat16()
