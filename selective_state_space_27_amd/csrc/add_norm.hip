@@ -5,9 +5,10 @@
 //   x' = post ? RMS(x) post : x;  r = residual + m x';  out = RMS(r) w.
 // Backward at the stored r, with g = dout w:
 //   dr = rstd g - r rstd^3 mean(g r) + dresidual_out      (dresidual)
-//   dw = sum_rows dout r rstd;  dgamma = scale sum_rows dr x'
-//   dx = m dr, or with post, n = RMS(x), g2 = m dr post:
-//   dpost = sum_rows m dr n;  dx = rstd_x g2 - x rstd_x^3 mean(g2 x).
+//   dw = sum_rows dout r rstd
+//   dx = m dr, or with post, n = RMS(x), g2 = m post dr:
+//   dx = rstd_x g2 - x rstd_x^3 mean(g2 x);  with S = sum_rows dr n (n = x
+//   without post):  dgamma = scale post S,  dpost = m S.  One sum serves both.
 // rstd is formed again from r in the backward: sum(r^2) and sum(g r) are one
 // reduction, so it costs nothing and needs no tensor of its own.
 //
@@ -127,10 +128,12 @@ __global__ void __launch_bounds__(LANES ? 256 : 1024)
     __attribute__((amdgpu_waves_per_eu(LANES ? (EXTRA ? 3 : 4) : K == 2 || EXTRA ? 4 : 5))) add_norm_bwd_kernel(BwdArgs a) {
   constexpr int SD = RES32 ? kSrcF32 : kSrcBf16, SO = IO32 ? kSrcF32 : kSrcBf16;
   constexpr int SR = PACKED ? kSrcP8 : SD, SX = PACKED ? kSrcP8 : SO;
-  // The next row is fetched ahead where the registers hold it.  With two vectors
-  // per thread they do not: the row is kept as loaded and widened a second time
-  // after the sums, and with EXTRA the weights are read again for every row.
-  constexpr bool kAhead = EXTRA != 2 && K == 1, kRenew = K == 2;
+  // One vector per thread: the next row is fetched ahead (16384 x 2560 bf16 with
+  // post: 96 us, 128 without).  Two: the registers do not hold that; the row is
+  // kept as loaded and widened a second time after the sums, and with EXTRA the
+  // weights are read again for every row (4096 x 10240, bf16 with an fp32
+  // residual: 132 us; gamma 169; post 301, where some registers still spill).
+  constexpr bool kAhead = K == 1, kRenew = K == 2;
   __shared__ float lds[LANES ? kPartialLds : kRowSumFloats];
   int half = 0;
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;
@@ -138,19 +141,24 @@ __global__ void __launch_bounds__(LANES ? 256 : 1024)
   const int cols = (int)a.p.cols;
   const float inv = 1.0f / (float)cols;
   int col[K], n[K];
-  float w[K][8], post[K][8], m[K][8];
-  float dw[K][8] = {}, dgamma[K][8] = {}, dpost[K][8] = {};
+  float w[K][8], m[K][8];  // m: scale gamma post
+  float dw[K][8] = {}, s[K][8] = {};
   constexpr bool kReload = K == 2 && EXTRA != 0;
   auto weights = [&](int k) {
     load_w<WHOLE>(a.p.weight, col[k], n[k], w[k]);
-    if constexpr (EXTRA == 2) load_w<WHOLE>(a.p.post_weight, col[k], n[k], post[k]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m[k][j] = a.p.scale;
     if (EXTRA != 0 && a.p.gamma != nullptr) {
-      load_w<WHOLE>(a.p.gamma, col[k], n[k], m[k]);
+      float g[8];
+      load_w<WHOLE>(a.p.gamma, col[k], n[k], g);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) m[k][j] *= a.p.scale;
-    } else {
+      for (int j = 0; j < 8; ++j) m[k][j] *= g[j];
+    }
+    if constexpr (EXTRA == 2) {
+      float g[8];
+      load_w<WHOLE>(a.p.post_weight, col[k], n[k], g);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) m[k][j] = a.p.scale;
+      for (int j = 0; j < 8; ++j) m[k][j] *= g[j];
     }
   };
 #pragma unroll
@@ -246,23 +254,14 @@ __global__ void __launch_bounds__(LANES ? 256 : 1024)
           for (int j = 0; j < 8; ++j) e[k][j] *= m[k][j];
           store8<IO32, WHOLE>(dx, col[k], n[k], e[k]);
         }
-      } else if constexpr (EXTRA == 1) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          dgamma[k][j] = __builtin_fmaf(e[k][j], a.p.scale * x[k][j], dgamma[k][j]);
-          e[k][j] *= m[k][j];
-        }
-        if (a.p.dx != nullptr && n[k] > 0) store8<IO32, WHOLE>(dx, col[k], n[k], e[k]);
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float nh = x[k][j] * rx;
-          dgamma[k][j] = __builtin_fmaf(e[k][j], a.p.scale * (nh * post[k][j]), dgamma[k][j]);
-          const float dxp = m[k][j] * e[k][j];
-          dpost[k][j] = __builtin_fmaf(dxp, nh, dpost[k][j]);
-          e[k][j] = dxp * post[k][j];  // g2
-          sum2[0] = __builtin_fmaf(e[k][j], x[k][j], sum2[0]);
+          s[k][j] = __builtin_fmaf(e[k][j], EXTRA == 2 ? x[k][j] * rx : x[k][j], s[k][j]);
+          e[k][j] *= m[k][j];  // dx, or g2
+          if constexpr (EXTRA == 2) sum2[0] = __builtin_fmaf(e[k][j], x[k][j], sum2[0]);
         }
+        if (EXTRA == 1 && a.p.dx != nullptr && n[k] > 0) store8<IO32, WHOLE>(dx, col[k], n[k], e[k]);
       }
       if constexpr (kRenew) __builtin_amdgcn_sched_barrier(0);
     }
@@ -284,21 +283,12 @@ __global__ void __launch_bounds__(LANES ? 256 : 1024)
       }
     }
   }
-  // [dweight][dgamma where given][dpost]
-  float* part = a.part + (int64_t)blockIdx.x * a.nout * cols;
+  float* part = a.part + (int64_t)blockIdx.x * a.nout * cols;  // [dw][S]
 #pragma unroll
   for (int k = 0; k < K; ++k) store_partial<LANES, WHOLE>(part, col[k], n[k], dw[k], lds);
   if constexpr (EXTRA != 0) {
-    int at_out = 1;
-    if (a.p.gamma != nullptr) {
 #pragma unroll
-      for (int k = 0; k < K; ++k) store_partial<LANES, WHOLE>(part + cols, col[k], n[k], dgamma[k], lds);
-      at_out = 2;
-    }
-    if constexpr (EXTRA == 2) {
-#pragma unroll
-      for (int k = 0; k < K; ++k) store_partial<LANES, WHOLE>(part + (int64_t)at_out * cols, col[k], n[k], dpost[k], lds);
-    }
+    for (int k = 0; k < K; ++k) store_partial<LANES, WHOLE>(part + cols, col[k], n[k], s[k], lds);
   }
 }
 
@@ -309,9 +299,11 @@ hipError_t fwd_typed(const AddNormFwdParams& p, hipStream_t stream) {
   const FwdArgs a{p, (int)((p.cols + 31) / 32 * 32)};
   return with_shape(s, p.cols % 8 == 0, [&](auto lanes, auto k, auto whole) {
     if (p.post_weight != nullptr)
-      hipLaunchKernelGGL((add_norm_fwd_kernel<RES32, IO32, true, lanes.value, k.value, whole.value>), grid, block, 0, stream, a);
+      hipLaunchKernelGGL((add_norm_fwd_kernel<RES32, IO32, true, lanes.value, k.value, whole.value>), grid, block, 0,
+                         stream, a);
     else
-      hipLaunchKernelGGL((add_norm_fwd_kernel<RES32, IO32, false, lanes.value, k.value, whole.value>), grid, block, 0, stream, a);
+      hipLaunchKernelGGL((add_norm_fwd_kernel<RES32, IO32, false, lanes.value, k.value, whole.value>), grid, block, 0,
+                         stream, a);
     return hipGetLastError();
   });
 }
@@ -322,13 +314,12 @@ hipError_t bwd_typed(const AddNormBwdParams& p, hipStream_t stream) {
   const int64_t blocks = norm_blocks(s, p.rows, 1, true);
   BwdArgs a{p, reinterpret_cast<float*>(static_cast<char*>(p.workspace) + 256), 1, (int)((p.cols + 31) / 32 * 32),
             static_cast<int*>(p.workspace)};
-  SumPartialsArgs sum{a.part, {p.dweight, nullptr, nullptr}, blocks, p.cols, 1};
-  if (EXTRA != 0 && p.gamma != nullptr) sum.out[sum.nout++] = p.dgamma;
-  if (EXTRA == 2) sum.out[sum.nout++] = p.dpost_weight;
-  a.nout = sum.nout;
+  a.nout = EXTRA != 0 ? 2 : 1;
+  const SumPartialsArgs sum{a.part,  p.dweight, p.dgamma, p.dpost_weight, p.post_weight,
+                            p.gamma, p.scale,   blocks,   p.cols,         a.nout};
   const hipError_t e = with_shape(s, p.cols % 8 == 0, [&](auto lanes, auto k, auto whole) {
-    hipLaunchKernelGGL((add_norm_bwd_kernel<RES32, IO32, PACKED, EXTRA, lanes.value, k.value, whole.value>), dim3((unsigned)blocks),
-                       dim3((unsigned)s.threads), 0, stream, a);
+    hipLaunchKernelGGL((add_norm_bwd_kernel<RES32, IO32, PACKED, EXTRA, lanes.value, k.value, whole.value>),
+                       dim3((unsigned)blocks), dim3((unsigned)s.threads), 0, stream, a);
     return hipGetLastError();
   });
   return e != hipSuccess ? e : launch_sum_partials(sum, stream);
@@ -352,7 +343,8 @@ hipError_t launch_add_norm_fwd(const AddNormFwdParams& p, hipStream_t stream) {
 }
 
 size_t add_norm_bwd_workspace_bytes(int64_t rows, int64_t cols, int ngrads) {
-  return 256 + (size_t)norm_blocks(norm_shape(cols), rows, 1, true) * (size_t)ngrads * (size_t)cols * sizeof(float);
+  const size_t sums = ngrads > 1 ? 2 : 1;  // dgamma and dpost_weight are one sum
+  return 256 + (size_t)norm_blocks(norm_shape(cols), rows, 1, true) * sums * (size_t)cols * sizeof(float);
 }
 
 hipError_t launch_add_norm_bwd(const AddNormBwdParams& p, hipStream_t stream) {

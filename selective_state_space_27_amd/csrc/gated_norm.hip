@@ -270,7 +270,8 @@ hipError_t bwd_mode(const GatedNormBwdParams& p, hipStream_t stream) {
     return hipGetLastError();
   });
   if (e != hipSuccess) return e;
-  return launch_sum_partials(SumPartialsArgs{a.part, {p.dweight, nullptr, nullptr}, blocks, p.cols, 1}, stream);
+  return launch_sum_partials(
+      SumPartialsArgs{a.part, p.dweight, nullptr, nullptr, nullptr, nullptr, 1.f, blocks, p.cols, 1}, stream);
 }
 
 template <bool Y32, bool IO32, bool PACKED>

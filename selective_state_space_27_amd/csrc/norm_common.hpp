@@ -111,10 +111,17 @@ __device__ __forceinline__ void store_partial(float* part, int col, int n, const
 }
 constexpr int kPartialLds = 256 * 8;
 
-// Sums of `nparts` partial rows: out[p][col] over [nparts][nout][cols].
+// Sums of `nparts` partial rows [nparts][nout][cols]: the first is dweight; the
+// second, S, gives dgamma = scale post S and dpost = scale gamma S (each where
+// its pointer is given; post and gamma null: 1).
 struct SumPartialsArgs {
   const float* part;
-  float* out[3];
+  float* dweight;
+  float* dgamma;
+  float* dpost;
+  const float* post;
+  const float* gamma;
+  float scale;
   int64_t nparts;
   int64_t cols;
   int nout;

@@ -32,7 +32,14 @@ __global__ void __launch_bounds__(kCols* kSlices) sum_partials_kernel(SumPartial
     if (s < h) lds[s][c] += lds[s + h][c];
     __syncthreads();
   }
-  if (s == 0 && col < a.cols) a.out[blockIdx.y][col] = lds[0][c];
+  if (s != 0 || col >= a.cols) return;
+  v = lds[0][c];
+  if (blockIdx.y == 0) {
+    a.dweight[col] = v;
+    return;
+  }
+  if (a.dgamma != nullptr) a.dgamma[col] = v * (a.post != nullptr ? a.scale * a.post[col] : a.scale);
+  if (a.dpost != nullptr) a.dpost[col] = v * (a.gamma != nullptr ? a.scale * a.gamma[col] : a.scale);
 }
 
 }  // namespace
