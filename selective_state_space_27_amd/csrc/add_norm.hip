@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(LANES ? 256 : 1024)
     }
     row_sums<LANES>(sum, lds, half);
     const float rstd = rsqrtf(__builtin_fmaf(sum[0], inv, a.p.eps));
-    const float c1 = rstd * rstd * rstd * (sum[1] * inv);
+    const float c1 = sum[1] * inv * rstd * rstd * rstd;
     float rx = 0.f, sum2[1] = {};
     if constexpr (EXTRA == 2) rx = rsqrtf(__builtin_fmaf(sum[2], inv, a.p.eps));
     char* dres = static_cast<char*>(a.p.dresidual) + row * a.p.dresidual_stride * (RES32 ? 4 : 2);
@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(LANES ? 256 : 1024)
         for (int k = 0; k < K; ++k) renew(rx_[k]);
       }
       row_sums<LANES>(sum2, lds, half);
-      const float c2 = rx * rx * rx * (sum2[0] * inv);
+      const float c2 = sum2[0] * inv * rx * rx * rx;
       if (a.p.dx != nullptr) {
 #pragma unroll
         for (int k = 0; k < K; ++k) {

@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(LANES ? 256 : 1024)
     }
     row_sums<LANES>(sum, lds, half);
     const float rstd = rsqrtf(__builtin_fmaf(sum[0], inv, a.p.eps));
-    const float c1 = rstd * rstd * rstd * (sum[1] * inv);
+    const float c1 = sum[1] * inv * rstd * rstd * rstd;
     char* dyr = static_cast<char*>(a.p.dy) + row * a.p.dy_stride * (Y32 ? 4 : 2);
     char* dzr = static_cast<char*>(a.p.dz) + row * a.p.dz_stride * (IO32 ? 4 : 2);
 #pragma unroll

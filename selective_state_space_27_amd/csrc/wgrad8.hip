@@ -11,17 +11,19 @@
 // then lie in different banks.
 //
 // What bounds it: the matrix cores, at the clock that the card holds under
-// them (about 1.9 GHz of 2.4 here).  256 x 256 tiles, eight waves of 128 x 64:
-// a wave reads 6 KB of LDS for 8 products, so LDS (1536 cycles for 64 steps,
-// reads and writes) stays under the matrix cores' 2048; smaller wave tiles
-// would not.  With dY loaded straight into LDS five stages ahead, the next
-// stage's first operands read before the barrier, and the widening of X
-// between the products, 32768 x 10576 x 2560 takes 1.53 ms, 1163 TFLOP/s (a
-// bf16 matrix product of 8192^3 by the vendor's library reaches 1210, its
-// product of this very shape and layout 812).  Before that: 623 TFLOP/s with
-// one stage ahead through registers, 665 without bounds checks inside, 886
-// with the transfers into LDS, 989 with their addresses kept instead of
-// computed, 1033 and 1163 with the cut tiles' sums joined wider and cut less.
+// them (about 1.9 GHz of 2.4 here; busy 61% of the cycles).  256 x 256 tiles,
+// eight waves of 128 x 64: a wave reads 6 KB of LDS for 8 products, so LDS
+// (1536 cycles for 64 steps, reads and writes) stays under the matrix cores'
+// 2048; smaller wave tiles would not.  With dY loaded straight into LDS five
+// stages ahead, the next stage's first operands read before the barrier, and
+// LDS reads and the widening of X issued between the products, 32768 x 10576 x
+// 2560 takes 1.48 ms, 1203 TFLOP/s (a bf16 matrix product of 8192^3 by the
+// vendor's library reaches 1210, its product of this very shape and layout
+// 812).  On the way: 623 TFLOP/s with one stage ahead through registers, 665
+// without bounds checks inside, 886 with the transfers into LDS, 989 with
+// their addresses kept instead of computed, 1033 and 1163 with the cut tiles'
+// sums joined wider and cut less, 1203 with no LDS bank conflicts and the order
+// of issue given.
 //
 // Output tiles that do not fill the card's last round are cut along t into
 // `splits` parts each, whose fp32 sums go to the workspace and are added in
@@ -186,6 +188,8 @@ __global__ void __launch_bounds__(256) wgrad8_align_kernel(const uint16_t* src, 
 
 // Six staged tiles of dY and three of X.  dY's rows are 16-byte aligned, whole
 // vectors of eight and at most 2^23 elements apart.
+// Instruction classes of __builtin_amdgcn_sched_group_barrier.
+constexpr int kSchedValu = 0x002, kSchedMfma = 0x008, kSchedLdsRead = 0x100;
 // vmcnt limit (bits 3:0 and 15:14), the other counters not waited for.
 constexpr int vmcnt(int n) { return (n & 15) | ((n >> 4) << 14) | (7 << 4) | (15 << 8); }
 
@@ -213,9 +217,10 @@ __global__ void __launch_bounds__(WM* WN * 64) wgrad8_kernel(Args a) {
   }
   const int xt = tid / (BN / 16), xc = tid % (BN / 16) * 16, spitch = a.pitch >> 5;
   const uint32_t qoff = (uint32_t)xt * a.pitch + xc, soff = (uint32_t)xt * spitch + (xc >> 5);
-  // X's two slots of a thread swap places in every other 256 bytes: sixteen
-  // lanes, which write every second slot of 512 bytes, then meet all banks.
-  const int xflip = (xc >> 7 & 1) << 4;
+  // X's two slots of a thread swap places in every other 128 bytes: eight lanes,
+  // which write every second slot of 256 bytes, then meet all banks (20% of the
+  // LDS cycles were conflicts without).
+  const int xflip = (xc >> 6 & 1) << 4;
   const int xs0 = stage_slot(xt, xc / 8, WB) ^ xflip, xs1 = stage_slot(xt, xc / 8 + 1, WB) ^ xflip;
 
   // Where the next transfer of dY starts and the steps left from there, and the
@@ -279,7 +284,7 @@ __global__ void __launch_bounds__(WM* WN * 64) wgrad8_kernel(Args a) {
   for (int i = 0; i < TM; ++i) fca[i] = frow * WA + (((wm >> 5) + i) ^ (i16 >> 2)) * 64 + fsub;
 #pragma unroll
   for (int j = 0; j < TN; ++j)
-    fcb[j] = frow * WB + (((wn >> 5) + j) ^ (i16 >> 2)) * 64 + (fsub ^ ((((wn >> 5) + j) >> 2 & 1) << 4));
+    fcb[j] = frow * WB + (((wn >> 5) + j) ^ (i16 >> 2)) * 64 + (fsub ^ ((((wn >> 5) + j) >> 1 & 1) << 4));
   auto rd = [&](const unsigned char* p, int width) -> u32x4 {
     const u32x2 lo = __builtin_bit_cast(
         u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)(p)));
@@ -328,9 +333,27 @@ __global__ void __launch_bounds__(WM* WN * 64) wgrad8_kernel(Args a) {
     const Ops f1 = operands(sa, sx, 1);
     products(f0);
     put_x(sx2, now);
+    // Order of issue: the LDS reads between the first four products, most of the
+    // widening between the other four.
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      __builtin_amdgcn_sched_group_barrier(kSchedMfma, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(kSchedLdsRead, 3, 0);
+      __builtin_amdgcn_sched_group_barrier(kSchedValu, 4, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      __builtin_amdgcn_sched_group_barrier(kSchedMfma, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(kSchedValu, 8, 0);
+    }
     __builtin_amdgcn_sched_barrier(0);
     f0 = operands(sa1, sx1, 0);
     products(f1);
+#pragma unroll
+    for (int i = 0; i < 6; ++i) {
+      __builtin_amdgcn_sched_group_barrier(kSchedMfma, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(kSchedLdsRead, 2, 0);
+    }
   };
   const std::false_type bounded;
   load_a(bounded, a0);
