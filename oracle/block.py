@@ -128,6 +128,9 @@ def gated_norm_bwd(dout, y, z, weight, ngroups=1, norm_first=False, eps=1e-5):
 
 
 # ---------------------------------------------------------- 8-bit checkpoints
+TOP = 127.5 - 2.0 ** -17  # a block's maximum is below this many steps
+
+
 def pack8(x):
     """(q int8 [rows, pitch], exponent bytes uint8 [rows, pitch / 32])."""
     x = _f(x)
@@ -140,7 +143,7 @@ def pack8(x):
     top = np.where(finite, np.abs(np.where(np.isfinite(v), v, 0.0)).max(axis=2), 0.0)
     e = np.full(top.shape, 1, dtype=np.int64)
     for k in range(2, 249):  # the smallest power of two that holds the block
-        e = np.where(top >= 127.5 * 2.0 ** (k - 1 - 127), k, e)
+        e = np.where(top >= TOP * 2.0 ** (k - 1 - 127), k, e)
     q = np.clip(np.rint(np.where(finite[:, :, None], v, 0.0) / 2.0 ** (e - 127.0)[:, :, None]), -127, 127)
     return q.astype(np.int8).reshape(rows, pitch), np.where(finite, e, 255).astype(np.uint8)
 

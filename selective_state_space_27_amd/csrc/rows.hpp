@@ -4,7 +4,9 @@
 // form's rounding.
 //
 // The 8-bit form of a [rows, cols] tensor: per row and block of 32 columns a
-// scale s = 2^(e - 127), the smallest power of two with max|x| / s < 127.5, and
+// scale s = 2^(e - 127), the smallest power of two with max|x| / s < 127.5 - 2^-17
+// (127.5's lower neighbour in fp32: the threshold of max|x| * (1 / 127.5) in fp32,
+// so that a plain fp32 evaluation of the form finds the same scales), and
 // q = rint(x / s) in int8 (two's complement).  Rows of q are padded with zeros
 // to a multiple of 32 columns (the pitch), scales are the bytes e, one per 32
 // columns.  |x - q s| <= s / 2.  1 <= e <= 248: a block of zeros or of values
@@ -175,8 +177,8 @@ __device__ __forceinline__ u32x2 quantise8(const float (&v)[8], uint32_t& e) {
   for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
   m = max(m, dpp_u32<kDppXor1>(m));
   m = max(m, dpp_u32<kDppXor2>(m));
-  // max / 2^(exponent) is in [1, 2): at 127.5/64 and above the next power is taken.
-  const int up = (m & 0x7fffffu) >= 0x7f0000u ? 1 : 0;
+  // max / 2^(exponent) is in [1, 2): from 127.5/64 less one unit the next power is taken.
+  const int up = (m & 0x7fffffu) >= 0x7effffu ? 1 : 0;
   const int b = min(max((int)(m >> 23) - 6 + up, 1), 248);
   const bool finite = m < 0x7f800000u;
   e = finite ? (uint32_t)b : 255u;

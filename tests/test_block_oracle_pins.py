@@ -101,7 +101,7 @@ def test_pack8_definition():
     assert q.shape == (5, 96) and e.shape == (5, 3) and np.all(q[:, 70:] == 0)
     s = 2.0 ** (e.astype(float) - 127)
     top = np.abs(np.pad(x, ((0, 0), (0, 26)))).reshape(5, 3, 32).max(2)
-    assert np.all(top / s < 127.5) and np.all(top / (s / 2) >= 127.5)  # the smallest power of two
+    assert np.all(top / s < ob.TOP) and np.all(top / (s / 2) >= ob.TOP)  # the smallest power of two
     back = ob.unpack8(q, e, 70)
     assert np.all(np.abs(back - x) <= np.repeat(s / 2, 32, axis=1)[:, :70])
     # packing what it stands for changes nothing
@@ -113,10 +113,11 @@ def test_pack8_edges():
     row = np.zeros((1, 32))
     q, e = ob.pack8(row)
     assert e[0, 0] == 1 and not q.any()
-    row[0, 3] = 127.5  # rounds to the next power
-    q, e = ob.pack8(row)
-    assert e[0, 0] == 128 and q[0, 3] == 64
-    row[0, 3] = np.nextafter(127.5, 0)
+    for top in (127.5, 127.5 - 2.0 ** -17):  # the next power
+        row[0, 3] = top
+        q, e = ob.pack8(row)
+        assert e[0, 0] == 128 and q[0, 3] == 64
+    row[0, 3] = 127.5 - 2.0 ** -16
     q, e = ob.pack8(row)
     assert e[0, 0] == 127 and q[0, 3] == 127
     row[0, 4] = 2.5  # ties to even

@@ -74,6 +74,8 @@ def test_edges(io):
             torch.full((64,), tiny), torch.full((64,), -tiny / 8), torch.full((64,), 127.5), torch.full((64,), 127.0),
             torch.arange(64) - 31.5, torch.cat([torch.full((32,), 1e-30), torch.full((32,), 1e30)]),
             torch.tensor([-0.0] * 64), torch.full((64,), 1.9921875 * 2.0 ** 20)]
+    # around the threshold of a scale, at small, middle and large exponents
+    rows += [torch.full((64,), (127.5 - k * 2.0 ** -17) * 2.0 ** p) for k in (-1, 0, 1, 2, 3) for p in (-100, 0, 100)]
     x = torch.stack([r.float() for r in rows]).to(dt).to("cuda:0")
     p = mss.pack8(x)
     same_form(p, host64(x))
