@@ -29,9 +29,9 @@ struct FwdArgs {
   int pitch;
 };
 
-template <bool RES32, bool IO32, bool POST, int LANES, int K, bool WHOLE>
-__global__ void __launch_bounds__(LANES ? 256 : 1024)
-    __attribute__((amdgpu_waves_per_eu(K == 2 ? 4 : 6))) add_norm_fwd_kernel(FwdArgs a) {
+template <bool RES32, bool IO32, bool POST, int LANES, int K, int T, bool WHOLE>
+__global__ void __launch_bounds__(T)
+    __attribute__((amdgpu_waves_per_eu(T == 768 ? 3 : K == 2 ? 4 : 6))) add_norm_fwd_kernel(FwdArgs a) {
   constexpr int SR = RES32 ? kSrcF32 : kSrcBf16, SX = IO32 ? kSrcF32 : kSrcBf16;
   __shared__ float lds[LANES ? 1 : kRowSumFloats];
   int half = 0;
@@ -126,16 +126,17 @@ struct BwdArgs {
 };
 
 // EXTRA: 0 = x unused, 1 = gamma, 2 = post (and gamma where given).
-template <bool RES32, bool IO32, bool PACKED, int EXTRA, int LANES, int K, bool WHOLE>
-__global__ void __launch_bounds__(LANES ? 256 : 1024)
-    __attribute__((amdgpu_waves_per_eu(LANES ? (EXTRA ? 3 : 4) : K == 2 || EXTRA ? 4 : 5))) add_norm_bwd_kernel(BwdArgs a) {
+template <bool RES32, bool IO32, bool PACKED, int EXTRA, int LANES, int K, int T, bool WHOLE>
+__global__ void __launch_bounds__(T)
+    __attribute__((amdgpu_waves_per_eu(LANES ? (EXTRA ? 3 : 4) : T == 768 ? 3 : K == 2 || EXTRA ? 4 : 5)))
+    add_norm_bwd_kernel(BwdArgs a) {
   constexpr int SD = RES32 ? kSrcF32 : kSrcBf16, SO = IO32 ? kSrcF32 : kSrcBf16;
   constexpr int SR = PACKED ? kSrcP8 : SD, SX = PACKED ? kSrcP8 : SO;
   // One vector per thread: the next row is fetched ahead (16384 x 2560 bf16 with
   // post: 96 us, 128 without).  Two: the registers do not hold that; the row is
-  // kept as loaded and widened a second time after the sums, and with EXTRA the
-  // weights are read again for every row (4096 x 10240, bf16 with an fp32
-  // residual: 132 us; gamma 169; post 301, where some registers still spill).
+  // kept as loaded and widened a second time after the sums, and where they are
+  // short of it still the weights are read again for every row (4096 x 10240, bf16
+  // with an fp32 residual: 132 us; gamma 155; post 165, 170 with them kept).
   constexpr bool kAhead = K == 1, kRenew = K == 2;
   __shared__ float lds[LANES ? kPartialLds : kRowSumFloats];
   int half = 0;
@@ -146,7 +147,7 @@ __global__ void __launch_bounds__(LANES ? 256 : 1024)
   int col[K], n[K];
   float w[K][8], m[K][8];  // m: scale gamma post
   float dw[K][8] = {}, s[K][8] = {};
-  constexpr bool kReload = K == 2 && EXTRA != 0;
+  constexpr bool kReload = K == 2 && (EXTRA == 2 || (EXTRA == 1 && T == 1024));
   auto weights = [&](int k) {
     load_w<WHOLE>(a.p.weight, col[k], n[k], w[k]);
 #pragma unroll
@@ -300,12 +301,12 @@ hipError_t fwd_typed(const AddNormFwdParams& p, hipStream_t stream) {
   const NormShape s = norm_shape(p.cols);
   const dim3 grid((unsigned)norm_blocks(s, p.rows, 1, false)), block((unsigned)s.threads);
   const FwdArgs a{p, (int)((p.cols + 31) / 32 * 32)};
-  return with_shape(s, p.cols % 8 == 0, [&](auto lanes, auto k, auto whole) {
+  return with_shape(s, p.cols % 8 == 0, [&](auto lanes, auto k, auto t, auto whole) {
     if (p.post_weight != nullptr)
-      hipLaunchKernelGGL((add_norm_fwd_kernel<RES32, IO32, true, lanes.value, k.value, whole.value>), grid, block, 0,
+      hipLaunchKernelGGL((add_norm_fwd_kernel<RES32, IO32, true, lanes.value, k.value, t.value, whole.value>), grid, block, 0,
                          stream, a);
     else
-      hipLaunchKernelGGL((add_norm_fwd_kernel<RES32, IO32, false, lanes.value, k.value, whole.value>), grid, block, 0,
+      hipLaunchKernelGGL((add_norm_fwd_kernel<RES32, IO32, false, lanes.value, k.value, t.value, whole.value>), grid, block, 0,
                          stream, a);
     return hipGetLastError();
   });
@@ -320,8 +321,8 @@ hipError_t bwd_typed(const AddNormBwdParams& p, hipStream_t stream) {
   a.nout = EXTRA != 0 ? 2 : 1;
   const SumPartialsArgs sum{a.part,  p.dweight, p.dgamma, p.dpost_weight, p.post_weight,
                             p.gamma, p.scale,   blocks,   p.cols,         a.nout};
-  const hipError_t e = with_shape(s, p.cols % 8 == 0, [&](auto lanes, auto k, auto whole) {
-    hipLaunchKernelGGL((add_norm_bwd_kernel<RES32, IO32, PACKED, EXTRA, lanes.value, k.value, whole.value>),
+  const hipError_t e = with_shape(s, p.cols % 8 == 0, [&](auto lanes, auto k, auto t, auto whole) {
+    hipLaunchKernelGGL((add_norm_bwd_kernel<RES32, IO32, PACKED, EXTRA, lanes.value, k.value, t.value, whole.value>),
                        dim3((unsigned)blocks), dim3((unsigned)s.threads), 0, stream, a);
     return hipGetLastError();
   });

@@ -35,9 +35,9 @@ struct FwdArgs {
   int gcols;  // columns of a group
 };
 
-template <bool Y32, bool IO32, int MODE, int LANES, int K, bool WHOLE>
-__global__ void __launch_bounds__(LANES ? 256 : 1024)
-    __attribute__((amdgpu_waves_per_eu(K == 2 ? 4 : 6))) gated_norm_fwd_kernel(FwdArgs a) {
+template <bool Y32, bool IO32, int MODE, int LANES, int K, int T, bool WHOLE>
+__global__ void __launch_bounds__(T)
+    __attribute__((amdgpu_waves_per_eu(T == 768 ? 3 : K == 2 ? 4 : 6))) gated_norm_fwd_kernel(FwdArgs a) {
   constexpr int SY = Y32 ? kSrcF32 : kSrcBf16, SZ = IO32 ? kSrcF32 : kSrcBf16;
   __shared__ float lds[LANES ? 1 : kRowSumFloats];
   int half = 0;
@@ -119,15 +119,17 @@ struct BwdArgs {
   int* status;
 };
 
-template <bool Y32, bool IO32, bool PACKED, int MODE, int LANES, int K, bool WHOLE>
-__global__ void __launch_bounds__(LANES ? 256 : 1024)
-    __attribute__((amdgpu_waves_per_eu(4))) gated_norm_bwd_kernel(BwdArgs a) {
+template <bool Y32, bool IO32, bool PACKED, int MODE, int LANES, int K, int T, bool WHOLE>
+__global__ void __launch_bounds__(T)
+    __attribute__((amdgpu_waves_per_eu(T == 768 ? 3 : 4))) gated_norm_bwd_kernel(BwdArgs a) {
   constexpr int SO = IO32 ? kSrcF32 : kSrcBf16;
   constexpr int SY = PACKED ? kSrcP8 : Y32 ? kSrcF32 : kSrcBf16, SZ = PACKED ? kSrcP8 : SO;
-  // One vector per thread: the next row is fetched ahead.  Two: the registers do
-  // not hold that; the row is kept as loaded and widened a second time after the
-  // sums instead (8192 x 10240: 233 us; ahead, with spills, 429).
-  constexpr bool kAhead = K == 1, kRenew = K == 2;
+  // The next row is fetched ahead where the registers hold it: not with two
+  // vectors per thread in workgroups of up to 1024.  With two, the row is kept as
+  // loaded and widened a second time after the sums (8192 x 10240 from the 8-bit
+  // forms: 167 us; in workgroups of up to 1024 333 without and 479 with the next
+  // row ahead, for registers that spill).
+  constexpr bool kAhead = K == 1 || T == 768, kRenew = K == 2;
   __shared__ float lds[LANES ? kPartialLds : kRowSumFloats];
   int half = 0;
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *a.status = 0;
@@ -247,8 +249,8 @@ hipError_t fwd_mode(const GatedNormFwdParams& p, hipStream_t stream) {
   const NormShape s = norm_shape(gcols);
   const dim3 grid((unsigned)norm_blocks(s, p.rows, p.ngroups, false), (unsigned)p.ngroups), block((unsigned)s.threads);
   const FwdArgs a{p, (int)((p.cols + 31) / 32 * 32), (int)gcols};
-  return with_shape(s, gcols % 8 == 0, [&](auto lanes, auto k, auto whole) {
-    hipLaunchKernelGGL((gated_norm_fwd_kernel<Y32, IO32, MODE, lanes.value, k.value, whole.value>), grid, block, 0, stream, a);
+  return with_shape(s, gcols % 8 == 0, [&](auto lanes, auto k, auto t, auto whole) {
+    hipLaunchKernelGGL((gated_norm_fwd_kernel<Y32, IO32, MODE, lanes.value, k.value, t.value, whole.value>), grid, block, 0, stream, a);
     return hipGetLastError();
   });
 }
@@ -266,8 +268,8 @@ hipError_t bwd_mode(const GatedNormBwdParams& p, hipStream_t stream) {
   const int64_t blocks = norm_blocks(s, p.rows, p.ngroups, true);
   const BwdArgs a{p, reinterpret_cast<float*>(static_cast<char*>(p.workspace) + 256), (int)((p.cols + 31) / 32 * 32),
                   (int)gcols, static_cast<int*>(p.workspace)};
-  const hipError_t e = with_shape(s, gcols % 8 == 0, [&](auto lanes, auto k, auto whole) {
-    hipLaunchKernelGGL((gated_norm_bwd_kernel<Y32, IO32, PACKED, MODE, lanes.value, k.value, whole.value>),
+  const hipError_t e = with_shape(s, gcols % 8 == 0, [&](auto lanes, auto k, auto t, auto whole) {
+    hipLaunchKernelGGL((gated_norm_bwd_kernel<Y32, IO32, PACKED, MODE, lanes.value, k.value, t.value, whole.value>),
                        dim3((unsigned)blocks, (unsigned)p.ngroups), dim3((unsigned)s.threads), 0, stream, a);
     return hipGetLastError();
   });

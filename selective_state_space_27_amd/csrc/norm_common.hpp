@@ -53,15 +53,22 @@ inline int64_t norm_blocks(const NormShape& s, int64_t rows, int64_t groups, boo
   return want < most ? want : most;
 }
 
-// Calls f with the shape's LANES and K and whether rows are whole vectors, as constants.
+// Calls f with the shape's LANES and K, the most threads of its workgroups and
+// whether rows are whole vectors, as constants.  768 threads at most leave 168
+// registers for two vectors each (columns up to 12288), 1024 leave 128.
 template <typename F>
 inline hipError_t with_shape(const NormShape& s, bool whole, F&& f) {
+  typedef std::integral_constant<int, 0> group;
   const std::integral_constant<int, 1> one;
+  const std::integral_constant<int, 2> two;
+  const std::integral_constant<int, 256> t256;
+  const std::integral_constant<int, 768> t768;
+  const std::integral_constant<int, 1024> t1024;
   const auto with = [&](auto w) {
-    if (s.lanes == 32) return f(std::integral_constant<int, 32>{}, one, w);
-    if (s.lanes == 64) return f(std::integral_constant<int, 64>{}, one, w);
-    if (s.k == 1) return f(std::integral_constant<int, 0>{}, one, w);
-    return f(std::integral_constant<int, 0>{}, std::integral_constant<int, 2>{}, w);
+    if (s.lanes == 32) return f(std::integral_constant<int, 32>{}, one, t256, w);
+    if (s.lanes == 64) return f(std::integral_constant<int, 64>{}, one, t256, w);
+    if (s.k == 1) return f(group{}, one, t1024, w);
+    return s.threads <= 768 ? f(group{}, two, t768, w) : f(group{}, two, t1024, w);
   };
   return whole ? with(std::true_type{}) : with(std::false_type{});
 }

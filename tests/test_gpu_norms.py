@@ -82,7 +82,7 @@ def test_add_norm_fwd_sizes(cols):
 
 @pytest.mark.parametrize("io,wide", PAIRS)
 @pytest.mark.parametrize("post,gamma", [(False, False), (False, True), (True, False), (True, True)])
-@pytest.mark.parametrize("rows,cols,pad", [(1, 2560, 0), (3, 100, 3), (70, 768, 5), (9, 9000, 1)])
+@pytest.mark.parametrize("rows,cols,pad", [(1, 2560, 0), (3, 100, 3), (70, 768, 5), (9, 9000, 1), (4, 15001, 0)])
 def test_add_norm_fwd_options(io, wide, post, gamma, rows, cols, pad):
     g = gen(rows)
     x, res, w = act(g, rows, cols, DT[io], pad=pad), act(g, rows, cols, DT[wide], 3.0, pad=pad), weight(g, cols)
@@ -137,7 +137,8 @@ def test_add_norm_bwd_sizes(cols):
 @pytest.mark.parametrize("io,wide", PAIRS)
 @pytest.mark.parametrize("post,gamma", [(False, False), (False, True), (True, False), (True, True)])
 @pytest.mark.parametrize("rows,cols,pad,packed", [(1, 1001, 0, False), (33, 100, 3, True), (600, 200, 0, False),
-                                                  (70, 768, 5, False), (6, 12000, 0, True), (1500, 513, 1, False)])
+                                                  (70, 768, 5, False), (6, 12000, 0, True), (1500, 513, 1, False),
+                                                  (3, 16000, 0, False), (300, 12999, 1, True)])
 def test_add_norm_bwd_options(io, wide, post, gamma, rows, cols, pad, packed):
     add_bwd_case(gen(rows), rows, cols, io, wide, post, gamma, packed, pad, dres=rows != 70)
 
@@ -235,7 +236,8 @@ def test_gated_norm_sizes(cols):
 @pytest.mark.parametrize("gate,first", MODES)
 @pytest.mark.parametrize("rows,cols,ngroups,packed,pad", [
     (1, 5120, 1, False, 0), (1, 5120, 8, True, 0), (40, 96, 3, True, 0), (33, 1536, 8, False, 3), (5, 100, 1, True, 1),
-    (300, 60, 5, False, 0), (4, 10000, 1, True, 0), (3, 20480, 2, True, 0), (2, 65, 65, False, 0)])
+    (300, 60, 5, False, 0), (4, 10000, 1, True, 0), (3, 20480, 2, True, 0), (2, 65, 65, False, 0),
+    (5, 16384, 1, True, 0), (300, 14001, 1, False, 1)])
 def test_gated_norm_options(io, wide, gate, first, rows, cols, ngroups, packed, pad):
     gated_case(gen(rows), rows, cols, io, wide, gate == "gate", first, ngroups, packed, pad)
 
