@@ -19,8 +19,7 @@
 namespace mss {
 
 constexpr int kNormCUs = 256;
-constexpr int kOneVectorMax = 8192;   // columns of a segment with one vector per thread
-constexpr int kNormColsMax = 16384;   // columns of a segment at most (1024 threads x 2 vectors)
+constexpr int kOneVectorMax = 8192;  // columns of a segment with one vector per thread
 
 // Segment layout of a launch.
 struct NormShape {

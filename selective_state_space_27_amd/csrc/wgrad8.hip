@@ -25,7 +25,7 @@
 // sums joined wider and cut less, 1203 with no LDS bank conflicts and the order
 // of issue given.
 //
-// Output tiles that do not fill the card's last round are cut along t into
+// Output tiles past the last full set of the card's CUs are cut along t into
 // `splits` parts each, whose fp32 sums go to the workspace and are added in
 // order by a second kernel: the result does not depend on scheduling.
 #include <type_traits>
@@ -186,13 +186,14 @@ __global__ void __launch_bounds__(256) wgrad8_align_kernel(const uint16_t* src, 
     if (row[i] < tokens) *reinterpret_cast<u32x4*>(dst + row[i] * ((int64_t)vecs * 8) + col[i]) = v[i];
 }
 
-// Six staged tiles of dY and three of X.  dY's rows are 16-byte aligned, whole
-// vectors of eight and at most 2^23 elements apart.
 // Instruction classes of __builtin_amdgcn_sched_group_barrier.
 constexpr int kSchedValu = 0x002, kSchedMfma = 0x008, kSchedLdsRead = 0x100;
 // vmcnt limit (bits 3:0 and 15:14), the other counters not waited for.
 constexpr int vmcnt(int n) { return (n & 15) | ((n >> 4) << 14) | (7 << 4) | (15 << 8); }
 
+// The products of a tile, WM x WN waves of TM x TN tiles of 32 x 32.  Six tiles of
+// dY and three of X are staged; dY's rows are 16-byte aligned, whole vectors of
+// eight and at most 2^23 elements apart.
 template <int WM, int WN, int TM, int TN>
 __global__ void __launch_bounds__(WM* WN * 64) wgrad8_kernel(Args a) {
   constexpr int BM = WM * TM * 32, BN = WN * TN * 32, WA = BM * 2, WB = BN * 2;
@@ -432,11 +433,11 @@ struct Plan {
   double us;  // estimate
 };
 
-// Tiles of one size.  The tiles past the last full round are cut along t into
-// the number of parts that takes the least time: a CU takes 0.88 us for a stage
-// of a 256-wide tile and 0.28 us for one of a 128-wide (whether it holds one or
-// two of them), a round 3 us to start, the join 3 us and the parts' sums, written
-// and read, 5 TB/s; a part has 8 stages or more.  (Counting rounds alone cut the
+// Tiles of one size.  The tiles past the last full set are cut along t into the
+// number of parts that takes the least time: a CU takes 0.88 us for a stage of a
+// 256-wide tile and 0.28 us for one of a 128-wide (whether it holds one or two of
+// them), 3 us to start, the join 3 us and the parts' sums, written and read, 5
+// TB/s; a part has 8 stages or more.  (Counting the CUs' turns alone cut the
 // in_proj shape above in 14 where 3 is best: 1.69 ms.)
 Plan plan_with(bool big, int64_t tokens, int64_t outs, int64_t ins) {
   Plan p;
@@ -461,7 +462,7 @@ Plan plan_with(bool big, int64_t tokens, int64_t outs, int64_t ins) {
 }
 
 // The layout with the smaller estimate: 256-wide tiles where there are enough of
-// them or long enough sums (32768 x 2560 x 768: 131 us, 128-wide 158), 128-wide
+// them or long enough sums (32768 x 2560 x 768: 123 us, 128-wide 158), 128-wide
 // ones for little work (4096 x 2048 x 2048: 51 us, 256-wide 56; 8191 x 768 x
 // 1536: 36 and 42).
 Plan plan_of(int64_t tokens, int64_t outs, int64_t ins) {
