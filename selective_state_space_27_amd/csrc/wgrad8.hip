@@ -17,13 +17,13 @@
 // 2048; smaller wave tiles would not.  With dY loaded straight into LDS five
 // stages ahead, the next stage's first operands read before the barrier, and
 // LDS reads and the widening of X issued between the products, 32768 x 10576 x
-// 2560 takes 1.48 ms, 1203 TFLOP/s (a bf16 matrix product of 8192^3 by the
+// 2560 takes 1.43 ms, 1244 TFLOP/s (a bf16 matrix product of 8192^3 by the
 // vendor's library reaches 1210, its product of this very shape and layout
 // 812).  On the way: 623 TFLOP/s with one stage ahead through registers, 665
 // without bounds checks inside, 886 with the transfers into LDS, 989 with
 // their addresses kept instead of computed, 1033 and 1163 with the cut tiles'
 // sums joined wider and cut less, 1203 with no LDS bank conflicts and the order
-// of issue given.
+// of issue given, 1244 with the first loads in order and no branches at the end.
 //
 // Output tiles past the last full set of the card's CUs are cut along t into
 // `splits` parts each, whose fp32 sums go to the workspace and are added in
@@ -138,6 +138,40 @@ __device__ __forceinline__ void each_tile(F&& f) {
   }
 }
 
+// A wave's accumulators to dW, added to it with ACC: elements past dW's edges go to
+// an offset past the descriptor's end, where loads give 0 and stores are dropped,
+// so no element branches (with a branch for each, a 128 x 128 tile took 5.6 us).
+template <bool BF16, bool ACC, int BM, int BN, int TM, int TN>
+__device__ __forceinline__ void store_tile(const Args& a, const Item& it, const f32x16 (&acc)[TM][TN], int lm, int ln) {
+  constexpr uint32_t kBytes = BF16 ? 2 : 4;
+  const rsrc_t dst = make_rsrc(static_cast<char*>(a.dw) + (int64_t)it.m * BM * a.ins * kBytes, 0x7fffff00u);
+  each_tile<TM, TN>([&](auto i, auto j) {
+    const int m = lm + 32 * i.value, n = it.n * BN + ln + 32 * j.value;
+    const int rows = n < a.ins ? a.outs - it.m * BM : 0;
+    uint32_t off[16];
+    float v[16];
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      const int mr = m + 8 * (r >> 2) + (r & 3);
+      off[r] = mr < rows ? ((uint32_t)mr * (uint32_t)a.ins + (uint32_t)n) * kBytes : kOffNone;
+      v[r] = acc[i.value][j.value][r];
+    }
+    if constexpr (ACC) {
+      float old[16];
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        old[r] = BF16 ? bf16_to_f32(buf_load_u16(dst, off[r])) : __uint_as_float(buf_load_u32(dst, off[r]));
+#pragma unroll
+      for (int r = 0; r < 16; ++r) v[r] += old[r];
+    }
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      if constexpr (BF16) buf_store_u16(dst, off[r], f32_to_bf16(v[r]));
+      else buf_store_u32(dst, off[r], __float_as_uint(v[r]));
+    }
+  });
+}
+
 // A wave's accumulators: row 8 (r / 4) + r % 4 from lm, column ln of each 32 x 32 tile.
 template <int BM, int BN, int TM, int TN>
 __device__ __forceinline__ void write_tile(const Args& a, const Item& it, const f32x16 (&acc)[TM][TN], int lm, int ln) {
@@ -150,15 +184,13 @@ __device__ __forceinline__ void write_tile(const Args& a, const Item& it, const 
     });
     return;
   }
-  each_tile<TM, TN>([&](auto i, auto j) {
-    const int m = it.m * BM + lm + 32 * i.value, n = it.n * BN + ln + 32 * j.value;
-    if (n >= a.ins) return;
-#pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      const int mr = m + 8 * (r >> 2) + (r & 3);
-      if (mr < a.outs) put(a, (int64_t)mr * a.ins + n, acc[i.value][j.value][r]);
-    }
-  });
+  if (a.dw_bf16) {
+    if (a.accumulate) store_tile<true, true, BM, BN>(a, it, acc, lm, ln);
+    else store_tile<true, false, BM, BN>(a, it, acc, lm, ln);
+  } else {
+    if (a.accumulate) store_tile<false, true, BM, BN>(a, it, acc, lm, ln);
+    else store_tile<false, false, BM, BN>(a, it, acc, lm, ln);
+  }
 }
 
 // dY's rows copied to aligned ones of whole vectors of eight (zeros past the
@@ -298,6 +330,12 @@ __global__ void __launch_bounds__(WM* WN * 64) wgrad8_kernel(Args a) {
   struct Ops {
     u32x4 a[TM], b[TN];
   };
+  // X before dY in a stage's loads: widening X then leaves three stages of dY in
+  // flight instead of two (loads come back in order), which the short stages of
+  // four waves need (8191 x 768 x 1536: 34 us, 36 the other way); with eight
+  // waves the order of issue that it fixes costs more (32768 x 10576 x 2560: 1.48
+  // ms, 1.43 the other way).
+  constexpr bool kXFirst = WM * WN == 4;
   auto operands = [&](const unsigned char* sa, const unsigned char* sx, int kk) {
     Ops o;
 #pragma unroll
@@ -321,16 +359,23 @@ __global__ void __launch_bounds__(WM* WN * 64) wgrad8_kernel(Args a) {
   Ops f0;
   auto stage = [&](auto open, unsigned char* sa, unsigned char* sx, unsigned char* sa1, unsigned char* sx1, unsigned char* sx2,
                    unsigned char* dst, QRegs& q) {
-    // This wave's dY of stage s + 1 has landed (the loads of three stages are
-    // younger than it), its X of s + 1 is written and all it read is in
-    // registers.  The empty assembly keeps memory accesses on their side.
+    // This wave's dY of stage s + 1 has landed (at least the loads of three stages
+    // were issued after it), its X of s + 1 is written and all it read but the
+    // operands just asked for (kReads, of tiles that stay) is in registers.  The
+    // empty assembly keeps memory accesses on their side.
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_waitcnt((vmcnt(3 * (kPieces + 2)) & ~(15 << 8)) | (kReads << 8));
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    load_a(open, dst);
     const QRegs now = q;
-    q = load_q(open);
+    if constexpr (kXFirst) {
+      q = load_q(open);
+      asm volatile("" ::: "memory");
+      load_a(open, dst);
+    } else {
+      load_a(open, dst);
+      q = load_q(open);
+    }
     const Ops f1 = operands(sa, sx, 1);
     products(f0);
     put_x(sx2, now);
@@ -357,20 +402,31 @@ __global__ void __launch_bounds__(WM* WN * 64) wgrad8_kernel(Args a) {
     }
   };
   const std::false_type bounded;
+  // In this order: what a stage waits for counts the loads issued after it, and
+  // the first stages' are these.  The empty assembly keeps it.
+  const auto in_order = [] { asm volatile("" ::: "memory"); };
   load_a(bounded, a0);
   load_a(bounded, a1);
   {
     const QRegs p0 = load_q(bounded), p1 = load_q(bounded);
+    in_order();
     load_a(bounded, a2);
+    in_order();
     load_a(bounded, a3);
-    load_a(bounded, a4);
+    in_order();
     q0 = load_q(bounded);
+    in_order();
+    load_a(bounded, a4);
+    in_order();
     q1 = load_q(bounded);
+    in_order();
     put_x(x0, p0);
     put_x(x1, p1);
   }
+  // dY of the first two stages has landed (three transfers and two loads of X were
+  // issued after it), their X is written.
   asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(0);
+  __builtin_amdgcn_s_waitcnt(vmcnt(3 * kPieces + 4) & ~(15 << 8));
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
   f0 = operands(a0, x0, 0);
@@ -463,8 +519,8 @@ Plan plan_with(bool big, int64_t tokens, int64_t outs, int64_t ins) {
 
 // The layout with the smaller estimate: 256-wide tiles where there are enough of
 // them or long enough sums (32768 x 2560 x 768: 123 us, 128-wide 158), 128-wide
-// ones for little work (4096 x 2048 x 2048: 51 us, 256-wide 56; 8191 x 768 x
-// 1536: 36 and 42).
+// ones for little work (4096 x 2048 x 2048: 45 us, 256-wide 54; 8191 x 768 x
+// 1536: 35 and 37).
 Plan plan_of(int64_t tokens, int64_t outs, int64_t ins) {
   const Plan a = plan_with(true, tokens, outs, ins), b = plan_with(false, tokens, outs, ins);
   return a.us <= b.us ? a : b;
