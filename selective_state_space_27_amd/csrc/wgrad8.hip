@@ -10,20 +10,22 @@
 // row t stored at c ^ (t % 4): the four rows that a transposing read touches
 // then lie in different banks.
 //
-// What bounds it: the matrix cores, at the clock that the card holds under
-// them (about 1.9 GHz of 2.4 here; busy 61% of the cycles).  256 x 256 tiles,
-// eight waves of 128 x 64: a wave reads 6 KB of LDS for 8 products, so LDS
+// What bounds it: the power that the matrix cores may draw.  With random operands
+// the clock falls to about 1.7 GHz of 2.4 (matrix cores busy 66% of the cycles);
+// the same call with dY zero takes 1.12 ms, with both zero 1.03 ms.  256 x 256
+// tiles, eight waves of 128 x 64: a wave reads 6 KB of LDS for 8 products, so LDS
 // (1536 cycles for 64 steps, reads and writes) stays under the matrix cores'
 // 2048; smaller wave tiles would not.  With dY loaded straight into LDS five
 // stages ahead, the next stage's first operands read before the barrier, and
 // LDS reads and the widening of X issued between the products, 32768 x 10576 x
-// 2560 takes 1.43 ms, 1244 TFLOP/s (a bf16 matrix product of 8192^3 by the
-// vendor's library reaches 1210, its product of this very shape and layout
-// 812).  On the way: 623 TFLOP/s with one stage ahead through registers, 665
-// without bounds checks inside, 886 with the transfers into LDS, 989 with
-// their addresses kept instead of computed, 1033 and 1163 with the cut tiles'
-// sums joined wider and cut less, 1203 with no LDS bank conflicts and the order
-// of issue given, 1244 with the first loads in order and no branches at the end.
+// 2560 takes 1.43 ms, 1240 TFLOP/s (a bf16 matrix product of 8192^3 by the
+// vendor's library, many in a row, reaches 1390, 1790 on zeros; its product of
+// this very shape and layout 812).  On the way: 623 TFLOP/s with one stage ahead
+// through registers, 665 without bounds checks inside, 886 with the transfers
+// into LDS, 989 with their addresses kept instead of computed, 1033 and 1163 with
+// the cut tiles' sums joined wider and cut less, 1203 with no LDS bank conflicts
+// and the order of issue given, 1240 with the first loads in order and no
+// branches at the end.
 //
 // Output tiles past the last full set of the card's CUs are cut along t into
 // `splits` parts each, whose fp32 sums go to the workspace and are added in
