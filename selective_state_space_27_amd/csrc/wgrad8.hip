@@ -14,8 +14,8 @@
 // the clock falls to about 1.7 GHz of 2.4 (matrix cores busy 66% of the cycles);
 // the same call with dY zero takes 1.12 ms, with both zero 1.03 ms.  256 x 256
 // tiles, eight waves of 128 x 64: a wave reads 6 KB of LDS for 8 products, so LDS
-// (1536 cycles for 64 steps, reads and writes) stays under the matrix cores'
-// 2048; smaller wave tiles would not.  With dY loaded straight into LDS five
+// (1050 cycles for 64 steps by its counter, reads and writes) stays well under the
+// matrix cores' 2048.  With dY loaded straight into LDS five
 // stages ahead, the next stage's first operands read before the barrier, and
 // LDS reads and the widening of X issued between the products, 32768 x 10576 x
 // 2560 takes 1.43 ms, 1240 TFLOP/s (a bf16 matrix product of 8192^3 by the
