@@ -131,6 +131,7 @@ struct SumPartialsArgs {
   int64_t nparts;
   int64_t cols;
   int nout;
+  int64_t first = 0;  // column of a launch's first workgroup, set by launch_sum_partials
 };
 hipError_t launch_sum_partials(const SumPartialsArgs& a, hipStream_t stream);
 

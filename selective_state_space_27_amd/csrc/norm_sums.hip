@@ -11,11 +11,14 @@ namespace mss {
 namespace {
 
 constexpr int kCols = 16, kSlices = 64;
+// Columns of a launch: it has 64 threads a column and, along one axis of the
+// grid, fewer than 2^32 in all.
+constexpr int64_t kLaunchCols = 1LL << 25;
 
 __global__ void __launch_bounds__(kCols* kSlices) sum_partials_kernel(SumPartialsArgs a) {
   __shared__ float lds[kSlices][kCols + 1];
   const int c = threadIdx.x % kCols, s = threadIdx.x / kCols;
-  const int64_t col = (int64_t)blockIdx.x * kCols + c;
+  const int64_t col = a.first + (int64_t)blockIdx.x * kCols + c;
   const int64_t pitch = (int64_t)a.nout * a.cols;
   float v = 0.f;
   if (col < a.cols) {
@@ -46,10 +49,16 @@ __global__ void __launch_bounds__(kCols* kSlices) sum_partials_kernel(SumPartial
 
 }  // namespace
 
-hipError_t launch_sum_partials(const SumPartialsArgs& a, hipStream_t stream) {
-  hipLaunchKernelGGL(sum_partials_kernel, dim3((unsigned)((a.cols + kCols - 1) / kCols), (unsigned)a.nout),
-                     dim3(kCols * kSlices), 0, stream, a);
-  return hipGetLastError();
+hipError_t launch_sum_partials(const SumPartialsArgs& args, hipStream_t stream) {
+  SumPartialsArgs a = args;
+  for (a.first = 0; a.first < a.cols; a.first += kLaunchCols) {
+    const int64_t cols = a.cols - a.first < kLaunchCols ? a.cols - a.first : kLaunchCols;
+    hipLaunchKernelGGL(sum_partials_kernel, dim3((unsigned)((cols + kCols - 1) / kCols), (unsigned)a.nout),
+                       dim3(kCols * kSlices), 0, stream, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace mss
