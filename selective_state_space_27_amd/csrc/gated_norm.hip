@@ -26,8 +26,25 @@ namespace {
 
 enum : int { kNoGate = 0, kGateFirst = 1, kNormFirst = 2 };
 
-// sigma(z); the limits come out right (exp2 overflows to inf, 1 / inf = 0).
-__device__ __forceinline__ float sigmoid(float z) { return rcp_fast(1.0f + exp2_fast(-z * kLog2e)); }
+// sigma(z) = 1 / (1 + 2^t), t = -z log2(e); the limits come out right (exp2
+// overflows to inf, 1 / inf = 0).  t rounded to fp32 puts sigma of a nearly closed
+// gate off by up to 64 units of 2^-24 (z near -60).  For fp32 gates what t leaves
+// out, lo, is put back: 2^(t + lo) = 2^t (1 + lo ln 2), lo below 2^-16.  A gate from
+// bf16 or the 8-bit form is itself known to |z| 2^-9 of sigma, 2^15 times as much,
+// and spares the instructions (they cost 768 columns from bf16 7% and more).
+// Past +-192 sigma is 0 or 1 in fp32 already; the limit keeps infinities out of lo.
+// It also drops a NaN, which comes back where z is multiplied in.
+template <int SRC>
+__device__ __forceinline__ float sigmoid(float z) {
+  if constexpr (SRC == kSrcF32) {
+    constexpr float kLog2eRest = (float)(1.4426950408889634 - (double)kLog2e), kLn2 = 0.69314718f;
+    const float c = __builtin_amdgcn_fmed3f(z, -192.f, 192.f), t = -c * kLog2e;
+    const float lo = __builtin_fmaf(-c, kLog2eRest, __builtin_fmaf(-c, kLog2e, -t));
+    return rcp_fast(1.0f + exp2_fast(t) * __builtin_fmaf(lo, kLn2, 1.0f));
+  } else {
+    return rcp_fast(1.0f + exp2_fast(-z * kLog2e));
+  }
+}
 
 struct FwdArgs {
   GatedNormFwdParams p;
@@ -88,7 +105,7 @@ __global__ void __launch_bounds__(T)
     for (int k = 0; k < K; ++k)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        if constexpr (MODE == kGateFirst) y[k][j] *= z[k][j] * sigmoid(z[k][j]);
+        if constexpr (MODE == kGateFirst) y[k][j] *= z[k][j] * sigmoid<SZ>(z[k][j]);
         sum[0] = __builtin_fmaf(y[k][j], y[k][j], sum[0]);
       }
     row_sums<LANES>(sum, lds, half);
@@ -100,7 +117,7 @@ __global__ void __launch_bounds__(T)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         o[j] = y[k][j] * rstd * w[k][j];
-        if constexpr (MODE == kNormFirst) o[j] *= z[k][j] * sigmoid(z[k][j]);
+        if constexpr (MODE == kNormFirst) o[j] *= z[k][j] * sigmoid<SZ>(z[k][j]);
       }
       if (n[k] > 0) store8<IO32, WHOLE>(out, col[k], n[k], o);
       if (a.p.out_q != nullptr) {
@@ -125,11 +142,13 @@ __global__ void __launch_bounds__(T)
   constexpr int SO = IO32 ? kSrcF32 : kSrcBf16;
   constexpr int SY = PACKED ? kSrcP8 : Y32 ? kSrcF32 : kSrcBf16, SZ = PACKED ? kSrcP8 : SO;
   // The next row is fetched ahead where the registers hold it: not with two
-  // vectors per thread in workgroups of up to 1024.  With two, the row is kept as
-  // loaded and widened a second time after the sums (8192 x 10240 from the 8-bit
-  // forms: 167 us; in workgroups of up to 1024 333 without and 479 with the next
-  // row ahead, for registers that spill).
-  constexpr bool kAhead = K == 1 || T == 768, kRenew = K == 2;
+  // vectors per thread in workgroups of up to 1024, nor in fp32 with a gate where
+  // rows are not whole vectors (4096 x 10001: 165 us, ahead 177 to 188).  With two,
+  // the row is kept as loaded and widened a second time after the sums (8192 x 10240
+  // from the 8-bit forms: 167 us; in workgroups of up to 1024 333 without and 479
+  // with the next row ahead, for registers that spill).
+  constexpr bool kHeld = T == 768 && (WHOLE || PACKED || !IO32 || MODE == kNoGate);
+  constexpr bool kAhead = K == 1 || kHeld, kRenew = K == 2;
   __shared__ float lds[LANES ? kPartialLds : kRowSumFloats];
   int half = 0;
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *a.status = 0;
@@ -187,7 +206,7 @@ __global__ void __launch_bounds__(T)
       for (int j = 0; j < 8; ++j) {
         float g = d[k][j] * w[k][j], v = y[k][j];
         if constexpr (MODE != kNoGate) {
-          const float s = z[k][j] * sigmoid(z[k][j]);
+          const float s = z[k][j] * sigmoid<SZ>(z[k][j]);
           if constexpr (MODE == kGateFirst) v *= s;
           else g *= s;
         }
@@ -216,7 +235,7 @@ __global__ void __launch_bounds__(T)
           dy[j] = rstd * g - y[k][j] * c1;
           dw[k][j] = __builtin_fmaf(d[k][j], y[k][j] * rstd, dw[k][j]);
         } else {
-          const float sg = sigmoid(z[k][j]), s = z[k][j] * sg;
+          const float sg = sigmoid<SZ>(z[k][j]), s = z[k][j] * sg;
           const float ds = __builtin_fmaf(s, 1.0f - sg, sg);  // sigma (1 + z (1 - sigma))
           if constexpr (MODE == kGateFirst) {
             const float v = y[k][j] * s, dv = rstd * g - v * c1;
