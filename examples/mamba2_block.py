@@ -2,10 +2,11 @@
 mixer, gated norm, output projection ("Mamba-1/2/3 visual guide", section 2
 block diagram and section 3; the short convolution is left out).
 
-Training keeps every activation that the backward pass reads in 8 bits: the
+Training keeps the wide activations that the backward pass reads in 8 bits: the
 projections' inputs (their weight gradients come straight from that form), the
-mixer's input and output and the gate.  Generation runs one token at a time on
-the recurrent state.
+residual, the mixer's input and output and the gate; B and C (bfloat16) and the
+step sizes (float32), a few percent of the rest, stay as they are.  Generation
+runs one token at a time on the recurrent state.
 
     python examples/mamba2_block.py      # one training step and a few tokens
 """
@@ -37,32 +38,40 @@ class _Block(torch.autograd.Function):
         delta, a = F.softplus(dt), -torch.exp(a_log)
         y = mss.ssd_chunk_fwd(xs.contiguous(), delta, a, bs.contiguous(), cs.contiguous(), d)
         g, y8, z8, g8 = mss.gated_norm_fwd(y.view(b, length, inner), z, gate_norm, pack_inputs=True, pack_out=True)
-        kept = {"u": u8, "r": mss.pack8(r), "x": mss.pack8(xs.view(b, length, inner)), "y": y8, "z": z8, "g": g8,
-                "B": bs.contiguous(), "C": cs.contiguous(), "dt": dt}
-        ctx.kept, ctx.sizes = kept, (heads, groups, dstate)
-        ctx.save_for_backward(norm, w_in, a, d, gate_norm, w_out)
+        packed = (u8, mss.pack8(r), mss.pack8(xs.view(b, length, inner)), y8, z8, g8)
+        # Through autograd, which frees them after the backward pass.
+        ctx.save_for_backward(norm, w_in, a, d, gate_norm, w_out, bs.contiguous(), cs.contiguous(), dt,
+                              *(t for p8 in packed for t in (p8.q, p8.scale)))
+        ctx.forms, ctx.sizes = [(p8.shape, p8.dtype) for p8 in packed], (heads, groups, dstate)
         return g @ w_out.t(), r
 
     @staticmethod
+    def kept(ctx):
+        """What the backward pass reads: parameters, tensors, checkpoints."""
+        saved = ctx.saved_tensors
+        packed = [mss.Packed8(q, scale, *form) for q, scale, form in zip(saved[9::2], saved[10::2], ctx.forms)]
+        return saved[:6], saved[6:9], packed
+
+    @staticmethod
     def backward(ctx, dout, dr):
-        k, (heads, groups, dstate) = ctx.kept, ctx.sizes
-        norm, w_in, a, d, gate_norm, w_out = ctx.saved_tensors
+        heads, groups, dstate = ctx.sizes
+        (norm, w_in, a, d, gate_norm, w_out), (bs, cs, dt), (u8, r8, x8, y8, z8, g8) = _Block.kept(ctx)
         b, length, _ = dout.shape
         inner = w_out.shape[1]
         dout = dout.contiguous()
-        dw_out = mss.wgrad8(dout, k["g"])
+        dw_out = mss.wgrad8(dout, g8)
         dp = torch.empty(b, length, w_in.shape[0], dtype=dout.dtype, device=dout.device)
         dz, dxs, dbs, dcs, ddt = dp.split([inner, inner, groups * dstate, groups * dstate, heads], dim=-1)
-        gate = mss.gated_norm_bwd(dout @ w_out, k["y"], k["z"], gate_norm, dz=dz)
-        s = mss.ssd_chunk_bwd(mss.unpack8(k["x"]).view(b, length, heads, -1), F.softplus(k["dt"]), a, k["B"], k["C"], d,
+        gate = mss.gated_norm_bwd(dout @ w_out, y8, z8, gate_norm, dz=dz)
+        s = mss.ssd_chunk_bwd(mss.unpack8(x8).view(b, length, heads, -1), F.softplus(dt), a, bs, cs, d,
                               dy=gate["dy"].view(b, length, heads, -1), want_dh0=False)
         dxs.copy_(s["dx"].view(b, length, inner))
         dbs.copy_(s["dB"].flatten(2))
         dcs.copy_(s["dC"].flatten(2))
-        graw = s["ddelta"] * torch.sigmoid(k["dt"])
+        graw = s["ddelta"] * torch.sigmoid(dt)
         ddt.copy_(graw)
-        dw_in = mss.wgrad8(dp, k["u"])
-        n = mss.add_norm_bwd(dp @ w_in, k["r"], norm, dresidual_out=None if dr is None else dr.contiguous())
+        dw_in = mss.wgrad8(dp, u8)
+        n = mss.add_norm_bwd(dp @ w_in, r8, norm, dresidual_out=None if dr is None else dr.contiguous())
         return (n["dx"], n["dresidual"], n["dweight"], dw_in.to(w_in.dtype), graw.sum((0, 1)), s["dA"] * a, s["dD"],
                 gate["dweight"], dw_out.to(w_out.dtype), None, None, None)
 
@@ -112,9 +121,11 @@ def main():
     x = torch.randn(b, length, width, device="cuda", dtype=torch.bfloat16, requires_grad=True)
     residual = torch.randn(b, length, width, device="cuda", requires_grad=True)
     out, r = block(x, residual)
-    kept = out.grad_fn.kept.values()
-    held = sum(t.nbytes() if isinstance(t, mss.Packed8) else t.numel() * t.element_size() for t in kept)
-    full = sum(t.shape.numel() * (t.dtype.itemsize if isinstance(t, mss.Packed8) else t.element_size()) for t in kept)
+    _, tensors, packed = _Block.kept(out.grad_fn)
+    rest = sum(t.numel() * t.element_size() for t in tensors)
+    held = rest + sum(p.nbytes() for p in packed)
+    full = rest + sum(p.shape.numel() * p.dtype.itemsize for p in packed)
+    del tensors, packed  # the graph's again, to be freed with it
     (out.float().square().mean() + r.square().mean()).backward()
     print(f"training step: activations held {held / 2**20:.0f} MiB (unpacked {full / 2**20:.0f}), "
           f"|dW_in| {block.w_in.grad.float().norm():.4g}, |dW_out| {block.w_out.grad.float().norm():.4g}")
