@@ -54,6 +54,8 @@ class _Block(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, dout, dr):
+        if torch.is_grad_enabled():  # create_graph: what follows would drop its terms without a word
+            raise RuntimeError("the block has first derivatives only (create_graph=True asks for second ones)")
         heads, groups, dstate = ctx.sizes
         (norm, w_in, a, d, gate_norm, w_out), (bs, cs, dt), (u8, r8, x8, y8, z8, g8) = _Block.kept(ctx)
         b, length, _ = dout.shape

@@ -39,3 +39,10 @@ def test_checkpoints_are_freed_by_the_backward_pass(setup):
     torch.cuda.synchronize()
     kept = torch.cuda.memory_allocated() - before
     assert kept == sum(t.numel() * t.element_size() for t in held)  # whole multiples of the allocator's 512 bytes
+
+
+def test_second_derivatives_are_refused(setup):
+    _, block, x, residual = setup
+    out, _ = block(x, residual)
+    with pytest.raises(RuntimeError):
+        torch.autograd.grad(out.float().sum(), x, create_graph=True)
