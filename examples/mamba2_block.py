@@ -26,10 +26,11 @@ class _Block(torch.autograd.Function):
     """(x, residual) -> (block output, residual with x added)."""
 
     @staticmethod
-    def forward(ctx, x, residual, norm, w_in, dt_bias, a_log, d, gate_norm, w_out, heads, groups, dstate):
+    def forward(ctx, x, residual, norm, w_in, dt_bias, a_log, d, gate_norm, w_out, heads, groups, dstate, grad):
         b, length, _ = x.shape
         inner = w_out.shape[1]
-        u, r, u8 = mss.add_norm_fwd(x, residual, norm, residual_dtype=torch.float32, pack_out=True)
+        keep = grad and any(ctx.needs_input_grad)  # a backward pass may follow
+        u, r, *u8 = mss.add_norm_fwd(x, residual, norm, residual_dtype=torch.float32, pack_out=keep)
         p = u @ w_in.t()
         z, xs, bs, cs, dt = p.split([inner, inner, groups * dstate, groups * dstate, heads], dim=-1)
         xs = xs.reshape(b, length, heads, inner // heads)
@@ -37,8 +38,11 @@ class _Block(torch.autograd.Function):
         dt = dt.float() + dt_bias
         delta, a = F.softplus(dt), -torch.exp(a_log)
         y = mss.ssd_chunk_fwd(xs.contiguous(), delta, a, bs.contiguous(), cs.contiguous(), d)
-        g, y8, z8, g8 = mss.gated_norm_fwd(y.view(b, length, inner), z, gate_norm, pack_inputs=True, pack_out=True)
-        packed = (u8, mss.pack8(r), mss.pack8(xs.view(b, length, inner)), y8, z8, g8)
+        y = y.view(b, length, inner)
+        if not keep:
+            return mss.gated_norm_fwd(y, z, gate_norm) @ w_out.t(), r
+        g, *gate8 = mss.gated_norm_fwd(y, z, gate_norm, pack_inputs=True, pack_out=True)
+        packed = (*u8, mss.pack8(r), mss.pack8(xs.view(b, length, inner)), *gate8)
         # Through autograd, which frees them after the backward pass.
         ctx.save_for_backward(norm, w_in, a, d, gate_norm, w_out, bs.contiguous(), cs.contiguous(), dt,
                               *(t for p8 in packed for t in (p8.q, p8.scale)))
@@ -75,7 +79,7 @@ class _Block(torch.autograd.Function):
         dw_in = mss.wgrad8(dp, u8)
         n = mss.add_norm_bwd(dp @ w_in, r8, norm, dresidual_out=None if dr is None else dr.contiguous())
         return (n["dx"], n["dresidual"], n["dweight"], dw_in.to(w_in.dtype), graw.sum((0, 1)), s["dA"] * a, s["dD"],
-                gate["dweight"], dw_out.to(w_out.dtype), None, None, None)
+                gate["dweight"], dw_out.to(w_out.dtype), None, None, None, None)
 
 
 class Mamba2Block(torch.nn.Module):
@@ -96,7 +100,7 @@ class Mamba2Block(torch.nn.Module):
         if residual is None:
             residual = torch.zeros_like(x, dtype=torch.float32)
         return _Block.apply(x, residual, self.norm, self.w_in, self.dt_bias, self.a_log, self.d, self.gate_norm,
-                            self.w_out, *self.sizes)
+                            self.w_out, *self.sizes, torch.is_grad_enabled())
 
     def state(self, batch):
         heads, _, dstate = self.sizes

@@ -46,3 +46,18 @@ def test_second_derivatives_are_refused(setup):
     out, _ = block(x, residual)
     with pytest.raises(RuntimeError):
         torch.autograd.grad(out.float().sum(), x, create_graph=True)
+
+
+def test_without_gradients_nothing_is_packed(setup, monkeypatch):
+    m, block, x, residual = setup
+    out, res = block(x, residual)
+
+    def refuse(*_):
+        raise AssertionError("a checkpoint was made")
+
+    monkeypatch.setattr(m.mss.norms, "_empty_packed", refuse)
+    with torch.no_grad():
+        got = block(x, residual)
+    assert torch.equal(got[0], out) and torch.equal(got[1], res)
+    with pytest.raises(AssertionError):
+        block(x, residual)
