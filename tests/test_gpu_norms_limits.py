@@ -4,10 +4,13 @@ Tolerance as in test_gpu_norms.py (128 units of 2^-24 of the size of a value's
 terms, 192 for sums over rows, half a bf16 step), the reference in fp64 by torch
 on the GPU, for its size.
 """
+import numpy as np
 import pytest
 import torch
 
 import selective_state_space_27_amd as mss
+from gpu_util import host64
+from oracle import block as ob
 
 pytestmark = pytest.mark.gpu
 
@@ -39,3 +42,34 @@ def test_gradient_of_more_columns_than_a_launch_holds():
     tol = U * EPS24 * size
     tol = tol + torch.exp2(torch.floor(torch.log2((ref.abs() + tol).clamp_min(2.0 ** -126))) - 8)
     assert ((got["dy"].double().view(rows, groups, width) - ref).abs() - tol).max() <= 0
+
+
+@pytest.mark.parametrize("cols", [200, 2560, 9000])
+def test_small_rows_with_a_smaller_eps(cols):
+    """rstd^3 is past fp32 (1e45) where the gradient is not: the mean that it
+    multiplies is small, and taken first."""
+    g = torch.Generator(device="cuda:0")
+    g.manual_seed(cols)
+    rows, eps, tiny = 5, 1e-36, 1e-15
+
+    def draw(scale=1.0):
+        return torch.randn(rows, cols, generator=g, device="cuda:0") * scale
+
+    r, x, do = draw(tiny), draw(tiny), draw()
+    w, post = (1.0 + 0.2 * torch.randn(cols, generator=g, device="cuda:0") for _ in range(2))
+
+    def close(got, ref):
+        value, size = ref
+        assert torch.isfinite(got).all()
+        assert (np.abs(host64(got) - value) <= U * EPS24 * size).all()
+
+    got = mss.add_norm_bwd(do, r, w, eps=eps)
+    ref = ob.add_norm_bwd(host64(do), host64(r), host64(w), eps=eps)
+    close(got["dresidual"], ref["dresidual"])
+    big = draw()
+    got = mss.add_norm_bwd(do, big, w, x=x, post_weight=post, eps=eps)
+    ref = ob.add_norm_bwd(host64(do), host64(big), host64(w), None, host64(x), host64(post), eps=eps)
+    close(got["dx"], ref["dx"])
+    for z in (None, draw()):
+        got = mss.gated_norm_bwd(do, r, z, w, eps=eps)
+        close(got["dy"], ob.gated_norm_bwd(host64(do), host64(r), None if z is None else host64(z), host64(w), eps=eps)["dy"])
