@@ -128,7 +128,9 @@ def gated_norm_bwd(dout, y, z, weight, ngroups=1, norm_first=False, eps=1e-5):
 
 
 # ---------------------------------------------------------- 8-bit checkpoints
-TOP = 127.5 - 2.0 ** -17  # a block's maximum is below this many steps
+# A block's maximum is below this many steps: the form's definition, 127.5's lower neighbour in fp32 (mss_pack8 in
+# include/mambascan.h).
+TOP = 127.5 - 2.0 ** -17
 
 
 def pack8(x):

@@ -4,11 +4,13 @@
 // form's rounding.
 //
 // The 8-bit form of a [rows, cols] tensor: per row and block of 32 columns a
-// scale s = 2^(e - 127), the smallest power of two with max|x| / s < 127.5 - 2^-17
-// (127.5's lower neighbour in fp32: the threshold of max|x| * (1 / 127.5) in fp32,
-// so that a plain fp32 evaluation of the form finds the same scales), and
-// q = rint(x / s) in int8 (two's complement).  Rows of q are padded with zeros
-// to a multiple of 32 columns (the pitch), scales are the bytes e, one per 32
+// scale s = 2^(e - 127), the smallest power of two with max|x| / s < 127.5 - 2^-17,
+// and q = rint(x / s) in int8 (two's complement).  The bound is 127.5's lower
+// neighbour in fp32, where max|x| * (1 / 127.5) reaches 1: an fp32 evaluation by the
+// reciprocal, as a division by a constant commonly is on a GPU, finds the same
+// scales.  (A correctly rounded division takes the smaller one at that one mantissa;
+// no bf16 value lies there.)  Rows of q are padded with zeros to a
+// multiple of 32 columns (the pitch), scales are the bytes e, one per 32
 // columns.  |x - q s| <= s / 2.  1 <= e <= 248: a block of zeros or of values
 // below 2^-120 has e = 1, and the top of the range (where q s would overflow)
 // saturates at 127 * 2^121.  A block with an infinity or NaN in it has e = 255
