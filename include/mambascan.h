@@ -565,11 +565,12 @@ size_t mss_gated_norm_bwd_workspace_size(int64_t rows, int64_t cols, int64_t ngr
 /* power of two with max|x| / s < 127.5 - 2^-17 (127.5's lower neighbour in  */
 /* fp32, where max|x| times fp32's 1/127.5 reaches 1; a rounded division by  */
 /* 127.5 reaches it one unit later. For bf16 values: < 127.5); q = x / s     */
-/* rounded to nearest, ties to even. The value it stands for, q s, is within */
-/* s / 2 of x and exact in bf16 and fp32. 1 <= e <= 248 (blocks of zeros or  */
-/* of values below 2^-120 have e = 1; values that would reach 2^128 saturate */
-/* at 127 * 2^121). A block that holds an infinity or NaN has e = 255 and q  */
-/* = 0, and reads back as NaN.                                               */
+/* rounded to nearest, ties to even, and kept to -127 .. 127. The value it   */
+/* stands for, q s, is exact in bf16 and fp32 and within s / 2 of x; only    */
+/* magnitudes above 127.5 * 2^121, which saturate at 127 * 2^121, are off by */
+/* up to s. 1 <= e <= 248 (blocks of zeros or of values below 2^-120 have e  */
+/* = 1). A block that holds an infinity or NaN has e = 255 and q = 0, and    */
+/* reads back as NaN.                                                        */
 /*   q     [rows, pitch] int8, pitch = cols rounded up to a multiple of 32   */
 /*         (the columns past cols hold 0), 16-byte aligned;                  */
 /*   scale [rows, pitch / 32] bytes e.                                       */

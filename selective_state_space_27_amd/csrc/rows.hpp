@@ -11,9 +11,9 @@
 // scales.  (A correctly rounded division takes the smaller one at that one mantissa;
 // no bf16 value lies there.)  Rows of q are padded with zeros to a
 // multiple of 32 columns (the pitch), scales are the bytes e, one per 32
-// columns.  |x - q s| <= s / 2.  1 <= e <= 248: a block of zeros or of values
-// below 2^-120 has e = 1, and the top of the range (where q s would overflow)
-// saturates at 127 * 2^121.  A block with an infinity or NaN in it has e = 255
+// columns.  1 <= e <= 248: a block of zeros or of values below 2^-120 has e = 1,
+// and the top of the range (where q s would overflow) saturates at 127 * 2^121.
+// |x - q s| <= s / 2, but for what saturates: below s.  A block with an infinity or NaN in it has e = 255
 // and q = 0: its values read back as 0 * inf = NaN.  A power of two costs at
 // most one bit against a free scale, and buys that q s is exact in bf16 (seven
 // bits of magnitude), so the form feeds bf16 matrix products without a

@@ -322,7 +322,8 @@ def gated_norm_bwd(dout, y, z, weight, *, ngroups=1, norm_first=False, eps=1e-5,
 def pack8(x, *, stream=None) -> Packed8:
     """The 8-bit form of x ([..., cols], float32 or bfloat16): 8.25 bits an
     element, within half a step of a block of 32 columns' power-of-two scale
-    (at most max|x| / 127 of the block)."""
+    (max|x| / 127 of the block at most; fp32 magnitudes above 127.5 * 2^121
+    saturate, off by up to a step)."""
     dev = _mss._device_of(x)
     rows, cols = _rows_cols(x.shape, "x")
     code = _code(x.dtype)

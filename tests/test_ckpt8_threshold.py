@@ -47,3 +47,17 @@ def test_a_division_differs_at_the_bound_alone():
 def test_bf16_values_do_not_see_the_difference():
     # eight significant bits: 127 and 127.5 are neighbours
     assert list(exponents([127.0, 127.5])) == [127, 128]
+
+
+def test_the_error_and_where_it_saturates():
+    r = np.random.default_rng(1)
+    top = float(np.finfo(np.float32).max)
+    x = np.concatenate([r.standard_normal((50, 32)) * np.exp(r.uniform(-60, 60, (50, 1))),
+                        r.uniform(-1.0, 1.0, (50, 32)) * 127.5 * 2.0 ** 121, r.uniform(-1.0, 1.0, (50, 32)) * top,
+                        np.full((1, 32), top)])
+    x = x.astype(np.float32).astype(np.float64)
+    q, e = ob.pack8(x)
+    s = 2.0 ** (e.astype(float) - 127.0)
+    off, tail = np.abs(ob.unpack8(q, e, 32) - x), np.abs(x) > 127.5 * 2.0 ** 121
+    assert (off[~tail] <= np.broadcast_to(s / 2, x.shape)[~tail]).all()
+    assert tail.any() and (off <= s).all() and (off > s / 2)[tail].all()
