@@ -453,7 +453,8 @@ size_t mss_ssd_bwd_workspace_size(int64_t batch, int64_t seqlen, int64_t nheads,
 /* Layouts: x, out [rows, cols] io_dtype; residual, residual_out [rows,      */
 /*   cols] res_dtype, each with its own row stride (elements, at least cols) */
 /*   and any alignment of its element type; weight, post_weight, gamma       */
-/*   [cols] fp32.                                                            */
+/*   [cols] fp32, as every parameter vector here (small, and their gradients */
+/*   are sums over all rows).                                                */
 /* out_q, out_scale (both or neither): the 8-bit form of out as stored, see  */
 /*   mss_pack8.                                                              */
 /* Supported: io and res both fp32, both bf16, or io bf16 with res fp32;     */

@@ -2,9 +2,10 @@
 //
 // 16 columns x 64 slices of the partial rows per workgroup of 1024 threads:
 // each thread sums its slice's rows in order, the slices' sums meet in LDS in a
-// fixed order.  The partials were just written and come out of the caches: 4 to
-// 5 us, most of it latency (256 rows of 2560 to 1024 rows of 2 x 1001; a layout
-// with 256 rows in flight took the same).
+// fixed order.  4 to 6 us (256 rows of 2560 to 1024 rows of 2 x 1001), of latency
+// and of reading: 16 columns are 64 bytes, so each 128-byte line is read by two
+// workgroups, or three where rows are not whole lines (24.2 MB for the 8.2 MB of
+// 1024 x 2 x 1001).  A layout with 256 rows in flight took the same.
 #include "norm_common.hpp"
 
 namespace mss {

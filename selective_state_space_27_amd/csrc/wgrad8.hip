@@ -11,15 +11,16 @@
 // then lie in different banks.
 //
 // What bounds it: the power that the matrix cores may draw.  With random operands
-// the clock falls to about 1.7 GHz of 2.4 (matrix cores busy 66% of the cycles);
-// the same call with dY zero takes 1.12 ms, with both zero 1.03 ms.  256 x 256
-// tiles, eight waves of 128 x 64: a wave reads 6 KB of LDS for 8 products, so LDS
-// (1050 cycles for 64 steps by its counter, reads and writes) stays well under the
-// matrix cores' 2048.  With dY loaded straight into LDS five
-// stages ahead, the next stage's first operands read before the barrier, and
-// LDS reads and the widening of X issued between the products, 32768 x 10576 x
-// 2560 takes 1.43 ms, 1240 TFLOP/s (a bf16 matrix product of 8192^3 by the
-// vendor's library, many in a row, reaches 1390, 1790 on zeros; its product of
+// the clock falls to 1.6 to 1.7 GHz of 2.4, by the card (matrix cores busy 71% of the
+// cycles); with dY zero the same call, in the same cycles to 4%, runs at 2.0 GHz, with
+// both zero at 2.24 GHz (1.50, 1.15 and 1.01 ms on one card).  256 x 256 tiles, eight
+// waves of 128 x 64: a wave reads 6 KB of LDS for 8 products, so LDS (1026 cycles for
+// 64 steps by its counter, reads and writes) stays well under the matrix cores'
+// 2048.  With dY loaded straight into LDS five stages ahead, the next stage's first
+// operands read before the barrier, and LDS reads and the widening of X issued
+// between the products, 32768 x 10576 x 2560 takes 1.43 to 1.50 ms by the card,
+// 1240 TFLOP/s at best (a bf16 matrix product of 8192^3 by the vendor's
+// library, many in a row, reaches 1390, 1790 on zeros; its product of
 // this very shape and layout 812).  On the way: 623 TFLOP/s with one stage ahead
 // through registers, 665 without bounds checks inside, 886 with the transfers
 // into LDS, 989 with their addresses kept instead of computed, 1033 and 1163 with
@@ -495,7 +496,8 @@ struct Plan {
 // number of parts that takes the least time: a CU takes 0.88 us for a stage of a
 // 256-wide tile and 0.28 us for one of a 128-wide (whether it holds one or two of
 // them), 3 us to start, the join 3 us and the parts' sums, written and read, 5
-// TB/s; a part has 8 stages or more.  (Counting the CUs' turns alone cut the
+// TB/s; a part has 8 stages or more.  (That parts run whole groups of six stages is
+// left out.  Counting the CUs' turns alone cut the
 // in_proj shape above in 14 where 3 is best: 1.69 ms.)
 Plan plan_with(bool big, int64_t tokens, int64_t outs, int64_t ins) {
   Plan p;
