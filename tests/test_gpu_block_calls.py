@@ -50,7 +50,7 @@ def operators(g):
 @pytest.mark.parametrize("name", ["add_norm_fwd", "add_norm_bwd", "gated_norm_fwd", "gated_norm_bwd", "pack8", "unpack8",
                                   "wgrad8", "wgrad8 of unaligned rows"])
 def test_a_call_runs_on_the_stream_it_is_given(name):
-    """The input is written on a side stream, behind work of some 30 ms, and the
+    """The input is written on a side stream, behind work of some 100 ms, and the
     call follows on that stream alone: on any other it would read the old values."""
     g = gen(1)
     f = operators(g)[name]
@@ -62,7 +62,7 @@ def test_a_call_runs_on_the_stream_it_is_given(name):
     torch.cuda.synchronize()
     side = torch.cuda.Stream()
     with torch.cuda.stream(side):
-        for _ in range(4):
+        for _ in range(12):
             a = a @ a
         x.copy_(new)
     got = f(x, side)
