@@ -620,10 +620,163 @@ size_t mss_wgrad8_workspace_size(const void* dy, int64_t dy_stride, int64_t toke
                                  int64_t ins);
 
 /* ------------------------------------------------------------------------ */
+/* Gated linear recurrence: a mixer with one state per channel whose decay   */
+/* has a gate of its own, computed as a scan over whole sequences.            */
+/*                                                                          */
+/* The selective scan's recurrence h_t = Abar_t h_{t-1} + Bbar_t x_t         */
+/* ("Mamba-1/2/3 visual guide", section 1) with input dependent coefficients  */
+/* (section 2) and a state of one number per channel.  Per (b, t, d):        */
+/*   r = sigmoid(gate_a), i = sigmoid(gate_x)                                */
+/*   a = exp(-c softplus(lam[d]) r)                                          */
+/*   h_t = a h_{t-1} + sqrt(1 - a^2) i x;   y = h_t                          */
+/* with h before the first step h0 (NULL: zero).  sqrt(1 - a^2) keeps the    */
+/* state's size whatever the decay.  Where starts[b, t] is not zero, a       */
+/* sequence packed into the row begins: h_{t-1} counts as zero there,        */
+/* whatever it holds.                                                         */
+/*                                                                          */
+/* Layouts: x, gate_a, gate_x, y [batch, seqlen, dim] io_dtype, rows         */
+/*   (b * seqlen + t) with a row stride each (elements, at least dim) and    */
+/*   any alignment of their type (slices of one projection's output);        */
+/*   lam [dim], h0, h_last [batch, dim] fp32; starts [batch, seqlen] bytes;  */
+/*   states [batch, ceil(seqlen / MSS_RECURRENCE_CHUNK), dim] fp32: the      */
+/*   state before every chunk's first step (and before any start there),     */
+/*   which mss_gated_recurrence_bwd needs.                                   */
+/* h0, starts, h_last and states may be NULL.  States, sums and gates are in */
+/* fp32; y is rounded once.                                                  */
+/* Supported: c > 0 and finite (else MSS_ERR_UNSUPPORTED); batch * seqlen *  */
+/* stride below 2^47, batch * ceil(seqlen / 64) * ceil(dim / 64) below 2^23  */
+/* (else MSS_ERR_SHAPE).  `flags` must be 0.  Outputs must not overlap       */
+/* inputs or each other (slices of one buffer with the same stride may       */
+/* interleave).  The workspace (16-byte aligned, the size of the query) need */
+/* not be zeroed; its first word is the call's status word                   */
+/* (mss_workspace_status): long sequences are cut into pieces that hand      */
+/* their state on.                                                            */
+/* ------------------------------------------------------------------------ */
+#define MSS_RECURRENCE_CHUNK 64
+mss_status mss_gated_recurrence_fwd(const void* x, int64_t x_stride, const void* gate_a,
+                                    int64_t gate_a_stride, const void* gate_x, int64_t gate_x_stride,
+                                    const float* lam, float c, const float* h0, const uint8_t* starts,
+                                    void* y, int64_t y_stride, float* h_last, float* states,
+                                    int64_t batch, int64_t seqlen, int64_t dim, mss_dtype io_dtype,
+                                    uint32_t flags, void* workspace, size_t workspace_bytes,
+                                    void* hip_stream);
+
+/* Bytes of device workspace mss_gated_recurrence_fwd needs (0 when unsupported). */
+size_t mss_gated_recurrence_workspace_size(int64_t batch, int64_t seqlen, int64_t dim, mss_dtype io_dtype);
+
+/* ------------------------------------------------------------------------ */
+/* Its backward: the gradients of a loss given dy = dloss/dy and dh_last =   */
+/* dloss/dh_last (NULL: zero).  With g_t = dy_t + a_{t+1} g_{t+1} (no second */
+/* term across a start; after the last step dh_last instead), beta =         */
+/* sqrt(1 - a^2), s = c softplus(lam) r:                                     */
+/*   dx = g beta i;  dgate_x = g beta i x (1 - i)                            */
+/*   G = g (a^2 (s / beta) i x - s a h_{t-1})      (= s dloss/ds)            */
+/*   dgate_a = G (1 - r);  dlam = sum G sigmoid(lam) / softplus(lam)         */
+/*   dh0 = a_0 g_0 (0 when a sequence starts there)                          */
+/* States are recomputed from `states`, the forward's, chunk by chunk.  Sums */
+/* run in fp32 in a fixed order: bitwise repeatable.                         */
+/* dy, dx, dgate_a, dgate_x as x, with strides of their own; dh_last, dh0    */
+/* (NULL: not computed) [batch, dim] fp32; dlam [dim] fp32.  Limits, errors, */
+/* workspace and status word as in the forward.                              */
+/* ------------------------------------------------------------------------ */
+mss_status mss_gated_recurrence_bwd(const void* dy, int64_t dy_stride, const void* x, int64_t x_stride,
+                                    const void* gate_a, int64_t gate_a_stride, const void* gate_x,
+                                    int64_t gate_x_stride, const float* lam, float c,
+                                    const uint8_t* starts, const float* states, const float* dh_last,
+                                    void* dx, int64_t dx_stride, void* dgate_a, int64_t dgate_a_stride,
+                                    void* dgate_x, int64_t dgate_x_stride, float* dlam, float* dh0,
+                                    int64_t batch, int64_t seqlen, int64_t dim, mss_dtype io_dtype,
+                                    uint32_t flags, void* workspace, size_t workspace_bytes,
+                                    void* hip_stream);
+
+/* Bytes of device workspace mss_gated_recurrence_bwd needs (0 when unsupported). */
+size_t mss_gated_recurrence_bwd_workspace_size(int64_t batch, int64_t seqlen, int64_t dim,
+                                               mss_dtype io_dtype);
+
+/* ------------------------------------------------------------------------ */
+/* One generated token of the gated linear recurrence, for `batch` sequences */
+/* of `beams` beams each (rows b * beams + k; beams = 1 without a search):   */
+/*   h_out = a h + sqrt(1 - a^2) i x;   y = h_out                            */
+/* With parents [batch, beams] the row's h is that of beam parents[b, k] of  */
+/* its sequence (beam search continues some beams and drops others); an      */
+/* index outside 0 .. beams - 1 stands for the row itself.                   */
+/* h, h_out [batch * beams, dim] fp32; h_out may be h when parents is NULL,  */
+/* else the two must not overlap.  x, gate_a, gate_x, y [batch * beams, dim] */
+/* io_dtype with row strides, any alignment of their type; lam [dim].        */
+/* Supported: c > 0 and finite (else MSS_ERR_UNSUPPORTED); batch * beams *   */
+/* dim at most 2^31, rows * stride below 2^47 (else MSS_ERR_SHAPE).  `flags` */
+/* must be 0.  Outputs must not overlap inputs or each other otherwise.      */
+/* ------------------------------------------------------------------------ */
+mss_status mss_gated_recurrence_step(const float* h, const int64_t* parents, const void* x,
+                                     int64_t x_stride, const void* gate_a, int64_t gate_a_stride,
+                                     const void* gate_x, int64_t gate_x_stride, const float* lam, float c,
+                                     float* h_out, void* y, int64_t y_stride, int64_t batch,
+                                     int64_t beams, int64_t dim, mss_dtype io_dtype, uint32_t flags,
+                                     void* hip_stream);
+
+/* ------------------------------------------------------------------------ */
+/* Beam search: selection over beams and vocabulary.                         */
+/*                                                                          */
+/* Generation carries only a state of fixed size ("Mamba-1/2/3 visual        */
+/* guide", section 1); a search over several continuations keeps one per     */
+/* beam.  Per sequence b, beam k and token v                                 */
+/*   total[k, v] = scores[b, k] + logits[b, k, v]                            */
+/*                 - log sum_v' exp(logits[b, k, v'])                        */
+/* and the n_out largest over k and v are taken, in descending order, ties   */
+/* by the lower k * vocab + v: out_scores (rounded to fp32), parents (k) and */
+/* tokens (v), [batch, n_out] each.  Totals are compared in 64 bits; within  */
+/* a beam the order is that of the logits.                                   */
+/*   A logit of -infinity (a banned token) has total -infinity.              */
+/*   finished[b, k] not zero: the beam's only candidate is the token eos,    */
+/*     with total scores[b, k]; its other totals are -infinity and its       */
+/*     logits are not looked at.                                             */
+/*   A beam whose score is NaN or an infinity, or one of whose logits is NaN */
+/*     or +infinity, or whose logits are all -infinity, has totals of        */
+/*     -infinity.                                                             */
+/* Totals of -infinity come after all others, in order of k * vocab + v.     */
+/* out_finished[b, j] (NULL: not written): whether token j is eos or its     */
+/* parent was finished.                                                       */
+/* logits: rows b * beams + k of `vocab` elements with a row stride, any     */
+/* alignment of their type; scores [batch, beams] fp32; finished [batch,     */
+/* beams] and out_finished [batch, n_out] bytes.  eos: -1 for none, needed   */
+/* with finished and out_finished (else MSS_ERR_UNSUPPORTED).                */
+/* Supported: beams and n_out up to 64, n_out at most beams * vocab, eos     */
+/* below vocab (else MSS_ERR_UNSUPPORTED); vocab up to 2^24, batch up to     */
+/* 65535, rows * stride below 2^47 (else MSS_ERR_SHAPE).  `flags` must be 0. */
+/* Outputs must not overlap inputs or each other.  The workspace (16-byte    */
+/* aligned, the size of the query) need not be zeroed.                       */
+/* ------------------------------------------------------------------------ */
+mss_status mss_beam_select(const void* logits, int64_t logits_stride, const float* scores,
+                           const uint8_t* finished, int64_t eos, float* out_scores, int64_t* parents,
+                           int64_t* tokens, uint8_t* out_finished, int64_t batch, int64_t beams,
+                           int64_t vocab, int64_t n_out, mss_dtype io_dtype, uint32_t flags,
+                           void* workspace, size_t workspace_bytes, void* hip_stream);
+
+/* Bytes of device workspace mss_beam_select needs (0 when unsupported). */
+size_t mss_beam_select_workspace_size(int64_t batch, int64_t beams, int64_t vocab, int64_t n_out);
+
+/* ------------------------------------------------------------------------ */
+/* Beam search: reordering of the beams' states, in place:                   */
+/*   states[s][b, k] = states[s][b, parents[b, k]]                           */
+/* for each of `count` state tensors [batch, beams, row_bytes[s] bytes],     */
+/* dense, of any type and alignment (the states of mss_state_update and      */
+/* mss_mamba3_state_update, convolution inputs).  Rows whose parent is their */
+/* own beam are not touched; an index outside 0 .. beams - 1 leaves the row  */
+/* as it is.  `states` (device pointers) and `row_bytes` are HOST arrays,    */
+/* read before the call returns.                                             */
+/* Supported: beams up to 64 (else MSS_ERR_UNSUPPORTED); batch up to 65535,  */
+/* row_bytes up to 2^30 (else MSS_ERR_SHAPE).  The tensors must not overlap  */
+/* each other or parents.                                                     */
+/* ------------------------------------------------------------------------ */
+mss_status mss_reorder_states(void* const* states, const int64_t* row_bytes, int64_t count,
+                              const int64_t* parents, int64_t batch, int64_t beams, void* hip_stream);
+
+/* ------------------------------------------------------------------------ */
 /* Status of a call that used `workspace`.                                   */
 /*                                                                          */
-/* The selective scan (forward, fused, backward) hands states between        */
-/* workgroups through flags in its workspace; each wait for such a flag is   */
+/* The selective scan (forward, fused, backward) and the gated recurrence    */
+/* (forward, backward) hand states between                                    */
+/* workgroups through flags in their workspace; each wait for such a flag is */
 /* bounded, and a wait that gives up (never expected) leaves the call's      */
 /* outputs invalid and sets the status word, the workspace's first 4 bytes, */
 /* which every call of the library clears in its first kernel (the SSD      */

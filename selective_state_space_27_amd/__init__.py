@@ -23,6 +23,13 @@ Around the mixer (norms.py):
   gated_norm_fwd, gated_norm_bwd  norm after a mixer with its gate
   pack8, unpack8, Packed8         8-bit activation checkpoints
   wgrad8              weight gradient from an 8-bit checkpoint, on MFMA
+A mixer with one state per channel (recurrence.py):
+  gated_recurrence_fwd, gated_recurrence_bwd  gated linear recurrence over
+                      whole sequences, its gradient
+  gated_recurrence_step  one generated token
+Beam search on recurrent states (beam.py):
+  beam_select         selection over beams and vocabulary
+  reorder_states      the beams' states follow their parents, in place
 """
 from __future__ import annotations
 
@@ -60,6 +67,9 @@ EXPORTS = ("mss_selective_scan_fwd", "mss_selective_scan_fwd_noalloc", "mss_sele
            "mss_add_norm_fwd", "mss_add_norm_bwd", "mss_add_norm_bwd_workspace_size",
            "mss_gated_norm_fwd", "mss_gated_norm_bwd", "mss_gated_norm_bwd_workspace_size",
            "mss_pack8", "mss_unpack8", "mss_wgrad8", "mss_wgrad8_workspace_size",
+           "mss_gated_recurrence_fwd", "mss_gated_recurrence_workspace_size", "mss_gated_recurrence_bwd",
+           "mss_gated_recurrence_bwd_workspace_size", "mss_gated_recurrence_step",
+           "mss_beam_select", "mss_beam_select_workspace_size", "mss_reorder_states",
            "mss_workspace_status", "mss_status_string",
            "mss_last_hip_error", "mss_abi_version")
 
@@ -147,6 +157,23 @@ def lib() -> ctypes.CDLL:
     L.mss_wgrad8.restype = ci
     L.mss_wgrad8_workspace_size.argtypes = [vp, i64, i64, i64, i64]
     L.mss_wgrad8_workspace_size.restype = sz
+    L.mss_gated_recurrence_fwd.argtypes = [vp, i64, vp, i64, vp, i64, fp, cf, fp, vp, vp, i64, fp, fp, i64, i64, i64,
+                                           ci, u32, vp, sz, vp]
+    L.mss_gated_recurrence_fwd.restype = ci
+    L.mss_gated_recurrence_bwd.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, fp, cf, vp, fp, fp, vp, i64, vp, i64,
+                                           vp, i64, fp, fp, i64, i64, i64, ci, u32, vp, sz, vp]
+    L.mss_gated_recurrence_bwd.restype = ci
+    for query in (L.mss_gated_recurrence_workspace_size, L.mss_gated_recurrence_bwd_workspace_size):
+        query.argtypes, query.restype = [i64, i64, i64, ci], sz
+    L.mss_gated_recurrence_step.argtypes = [fp, vp, vp, i64, vp, i64, vp, i64, fp, cf, fp, vp, i64, i64, i64, i64, ci,
+                                            u32, vp]
+    L.mss_gated_recurrence_step.restype = ci
+    L.mss_beam_select.argtypes = [vp, i64, fp, vp, i64, fp, vp, vp, vp, i64, i64, i64, i64, ci, u32, vp, sz, vp]
+    L.mss_beam_select.restype = ci
+    L.mss_beam_select_workspace_size.argtypes = [i64, i64, i64, i64]
+    L.mss_beam_select_workspace_size.restype = sz
+    L.mss_reorder_states.argtypes = [vp, vp, i64, vp, i64, i64, vp]
+    L.mss_reorder_states.restype = ci
     L.mss_workspace_status.argtypes = [vp, vp]
     L.mss_workspace_status.restype = ctypes.c_int
     L.mss_status_string.argtypes = [ctypes.c_int]
@@ -626,3 +653,6 @@ def ssd_chunk_bwd(x, delta, A, B, C, D=None, z=None, h0=None, *, dy, dh_last=Non
 
 from .norms import (Packed8, add_norm_bwd, add_norm_fwd, gated_norm_bwd, gated_norm_fwd, pack8,  # noqa: E402
                     unpack8, wgrad8)
+from .recurrence import (RECURRENCE_CHUNK, gated_recurrence_bwd, gated_recurrence_fwd,  # noqa: E402
+                         gated_recurrence_step)
+from .beam import beam_select, reorder_states  # noqa: E402

@@ -26,7 +26,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmambascan.so")
 SOURCES = ["scan.hip", "scan_bwd.hip", "scan_bwd_wide.hip", "scan_fused_bwd.hip", "state_update.hip", "ssd.hip",
            "ssd_bwd.hip", "ssd_bwd_halves.hip", "mamba3.hip", "add_norm.hip", "gated_norm.hip", "norm_sums.hip", "ckpt8.hip",
-           "wgrad8.hip", "api.cpp"]
+           "wgrad8.hip", "recurrence.hip", "recurrence_step.hip", "beam_select.hip", "reorder.hip", "api.cpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

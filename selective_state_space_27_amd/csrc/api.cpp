@@ -773,6 +773,7 @@ bool stride_ok(const void* p, int64_t stride, int64_t rows, int64_t cols) {
 
 bool elem_aligned(const void* p, mss_dtype t) { return (reinterpret_cast<uintptr_t>(p) & (elem_size(t) - 1)) == 0; }
 bool f32_aligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+bool i64_aligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 
 int64_t pitch8(int64_t cols) { return (cols + 31) / 32 * 32; }
 RowSet q_set(const void* q, int64_t rows, int64_t cols) { return dense_set(q, rows * pitch8(cols)); }
@@ -1094,6 +1095,267 @@ mss_status mss_wgrad8(const void* dy, int64_t dy_stride, const int8_t* q, const 
   const mss::Wgrad8Params p{dy,   q,    scale, dw, dy_stride, tokens, outs, ins, dw_dtype == MSS_BF16,
                             (flags & MSS_FLAG_ACCUMULATE) != 0, workspace};
   return hip_status(mss::launch_wgrad8(p, static_cast<hipStream_t>(hip_stream)));
+}
+
+// ------------------------------------------------- gated linear recurrence
+namespace {
+
+bool rate_ok(float c) { return c > 0.f && c < __builtin_inff(); }
+
+mss_status recurrence_shape(int64_t batch, int64_t seqlen, int64_t dim, mss_dtype t) {
+  if (!dtype_ok(t)) return MSS_ERR_DTYPE;
+  if (batch <= 0 || seqlen <= 0 || dim <= 0) return MSS_ERR_SHAPE;
+  // Workgroups of a launch, each of up to 512 threads: fewer than 2^32 threads.
+  constexpr int64_t most = 1LL << 23;
+  if (batch >= most || seqlen >= most * 64 || dim >= (1LL << 29)) return MSS_ERR_SHAPE;
+  const int64_t chunks = batch * ((seqlen + 63) / 64);
+  if (chunks >= most || chunks * ((dim + 63) / 64) >= most) return MSS_ERR_SHAPE;
+  return rows_ok(batch * seqlen, dim) ? MSS_OK : MSS_ERR_SHAPE;
+}
+
+}  // namespace
+
+size_t mss_gated_recurrence_workspace_size(int64_t batch, int64_t seqlen, int64_t dim, mss_dtype io_dtype) {
+  if (recurrence_shape(batch, seqlen, dim, io_dtype) != MSS_OK) return 0;
+  return mss::recurrence_fwd_workspace_bytes(batch, seqlen, dim, io_dtype == MSS_BF16);
+}
+
+size_t mss_gated_recurrence_bwd_workspace_size(int64_t batch, int64_t seqlen, int64_t dim, mss_dtype io_dtype) {
+  if (recurrence_shape(batch, seqlen, dim, io_dtype) != MSS_OK) return 0;
+  return mss::recurrence_bwd_workspace_bytes(batch, seqlen, dim, io_dtype == MSS_BF16);
+}
+
+mss_status mss_gated_recurrence_fwd(const void* x, int64_t x_stride, const void* gate_a, int64_t gate_a_stride,
+                                    const void* gate_x, int64_t gate_x_stride, const float* lam, float c,
+                                    const float* h0, const uint8_t* starts, void* y, int64_t y_stride, float* h_last,
+                                    float* states, int64_t batch, int64_t seqlen, int64_t dim, mss_dtype io_dtype,
+                                    uint32_t flags, void* workspace, size_t workspace_bytes, void* hip_stream) {
+  if (!x || !gate_a || !gate_x || !lam || !y) return MSS_ERR_NULL;
+  const mss_status st = recurrence_shape(batch, seqlen, dim, io_dtype);
+  if (st != MSS_OK) return st;
+  const int64_t rows = batch * seqlen;
+  if (!stride_ok(x, x_stride, rows, dim) || !stride_ok(gate_a, gate_a_stride, rows, dim) ||
+      !stride_ok(gate_x, gate_x_stride, rows, dim) || !stride_ok(y, y_stride, rows, dim))
+    return MSS_ERR_SHAPE;
+  if (flags != 0 || !rate_ok(c)) return MSS_ERR_UNSUPPORTED;
+  if (!elem_aligned(x, io_dtype) || !elem_aligned(gate_a, io_dtype) || !elem_aligned(gate_x, io_dtype) ||
+      !elem_aligned(y, io_dtype) || !f32_aligned(lam) || !f32_aligned(h0) || !f32_aligned(h_last) ||
+      !f32_aligned(states) || !aligned16(workspace))
+    return MSS_ERR_ALIGN;
+  const size_t need = mss::recurrence_fwd_workspace_bytes(batch, seqlen, dim, io_dtype == MSS_BF16);
+  if (!workspace || workspace_bytes < need) return MSS_ERR_WORKSPACE;
+  const int64_t chunks = batch * ((seqlen + mss::kRecurrenceChunk - 1) / mss::kRecurrenceChunk);
+  const RowSet ins[] = {row_set(x, x_stride, rows, dim, io_dtype), row_set(gate_a, gate_a_stride, rows, dim, io_dtype),
+                        row_set(gate_x, gate_x_stride, rows, dim, io_dtype), dense_set(lam, dim * 4),
+                        dense_set(h0, batch * dim * 4), dense_set(starts, rows),
+                        dense_set(workspace, (int64_t)need)};
+  const RowSet outs[] = {row_set(y, y_stride, rows, dim, io_dtype), dense_set(h_last, batch * dim * 4),
+                         dense_set(states, chunks * dim * 4)};
+  if (!outputs_clear(outs, 3, ins, 7)) return MSS_ERR_ALIAS;
+  mss::RecurrenceFwdParams p;
+  p.x = x;
+  p.gate_a = gate_a;
+  p.gate_x = gate_x;
+  p.lam = lam;
+  p.h0 = h0;
+  p.starts = starts;
+  p.y = y;
+  p.h_last = h_last;
+  p.states = states;
+  p.x_stride = x_stride;
+  p.gate_a_stride = gate_a_stride;
+  p.gate_x_stride = gate_x_stride;
+  p.y_stride = y_stride;
+  p.batch = batch;
+  p.seqlen = seqlen;
+  p.dim = dim;
+  p.c = c;
+  p.bf16 = io_dtype == MSS_BF16;
+  p.workspace = workspace;
+  return hip_status(mss::launch_recurrence_fwd(p, static_cast<hipStream_t>(hip_stream)));
+}
+
+mss_status mss_gated_recurrence_bwd(const void* dy, int64_t dy_stride, const void* x, int64_t x_stride,
+                                    const void* gate_a, int64_t gate_a_stride, const void* gate_x,
+                                    int64_t gate_x_stride, const float* lam, float c, const uint8_t* starts,
+                                    const float* states, const float* dh_last, void* dx, int64_t dx_stride,
+                                    void* dgate_a, int64_t dgate_a_stride, void* dgate_x, int64_t dgate_x_stride,
+                                    float* dlam, float* dh0, int64_t batch, int64_t seqlen, int64_t dim,
+                                    mss_dtype io_dtype, uint32_t flags, void* workspace, size_t workspace_bytes,
+                                    void* hip_stream) {
+  if (!dy || !x || !gate_a || !gate_x || !lam || !states || !dx || !dgate_a || !dgate_x || !dlam) return MSS_ERR_NULL;
+  const mss_status st = recurrence_shape(batch, seqlen, dim, io_dtype);
+  if (st != MSS_OK) return st;
+  const int64_t rows = batch * seqlen;
+  if (!stride_ok(dy, dy_stride, rows, dim) || !stride_ok(x, x_stride, rows, dim) ||
+      !stride_ok(gate_a, gate_a_stride, rows, dim) || !stride_ok(gate_x, gate_x_stride, rows, dim) ||
+      !stride_ok(dx, dx_stride, rows, dim) || !stride_ok(dgate_a, dgate_a_stride, rows, dim) ||
+      !stride_ok(dgate_x, dgate_x_stride, rows, dim))
+    return MSS_ERR_SHAPE;
+  if (flags != 0 || !rate_ok(c)) return MSS_ERR_UNSUPPORTED;
+  if (!elem_aligned(dy, io_dtype) || !elem_aligned(x, io_dtype) || !elem_aligned(gate_a, io_dtype) ||
+      !elem_aligned(gate_x, io_dtype) || !elem_aligned(dx, io_dtype) || !elem_aligned(dgate_a, io_dtype) ||
+      !elem_aligned(dgate_x, io_dtype) || !f32_aligned(lam) || !f32_aligned(states) || !f32_aligned(dh_last) ||
+      !f32_aligned(dlam) || !f32_aligned(dh0) || !aligned16(workspace))
+    return MSS_ERR_ALIGN;
+  const size_t need = mss::recurrence_bwd_workspace_bytes(batch, seqlen, dim, io_dtype == MSS_BF16);
+  if (!workspace || workspace_bytes < need) return MSS_ERR_WORKSPACE;
+  const int64_t chunks = batch * ((seqlen + mss::kRecurrenceChunk - 1) / mss::kRecurrenceChunk);
+  const RowSet ins[] = {row_set(dy, dy_stride, rows, dim, io_dtype), row_set(x, x_stride, rows, dim, io_dtype),
+                        row_set(gate_a, gate_a_stride, rows, dim, io_dtype),
+                        row_set(gate_x, gate_x_stride, rows, dim, io_dtype), dense_set(lam, dim * 4),
+                        dense_set(starts, rows), dense_set(states, chunks * dim * 4),
+                        dense_set(dh_last, batch * dim * 4), dense_set(workspace, (int64_t)need)};
+  const RowSet outs[] = {row_set(dx, dx_stride, rows, dim, io_dtype),
+                         row_set(dgate_a, dgate_a_stride, rows, dim, io_dtype),
+                         row_set(dgate_x, dgate_x_stride, rows, dim, io_dtype), dense_set(dlam, dim * 4),
+                         dense_set(dh0, batch * dim * 4)};
+  if (!outputs_clear(outs, 5, ins, 9)) return MSS_ERR_ALIAS;
+  mss::RecurrenceBwdParams p;
+  p.dy = dy;
+  p.x = x;
+  p.gate_a = gate_a;
+  p.gate_x = gate_x;
+  p.lam = lam;
+  p.starts = starts;
+  p.states = states;
+  p.dh_last = dh_last;
+  p.dx = dx;
+  p.dgate_a = dgate_a;
+  p.dgate_x = dgate_x;
+  p.dlam = dlam;
+  p.dh0 = dh0;
+  p.dy_stride = dy_stride;
+  p.x_stride = x_stride;
+  p.gate_a_stride = gate_a_stride;
+  p.gate_x_stride = gate_x_stride;
+  p.dx_stride = dx_stride;
+  p.dgate_a_stride = dgate_a_stride;
+  p.dgate_x_stride = dgate_x_stride;
+  p.batch = batch;
+  p.seqlen = seqlen;
+  p.dim = dim;
+  p.c = c;
+  p.bf16 = io_dtype == MSS_BF16;
+  p.workspace = workspace;
+  return hip_status(mss::launch_recurrence_bwd(p, static_cast<hipStream_t>(hip_stream)));
+}
+
+mss_status mss_gated_recurrence_step(const float* h, const int64_t* parents, const void* x, int64_t x_stride,
+                                     const void* gate_a, int64_t gate_a_stride, const void* gate_x,
+                                     int64_t gate_x_stride, const float* lam, float c, float* h_out, void* y,
+                                     int64_t y_stride, int64_t batch, int64_t beams, int64_t dim, mss_dtype io_dtype,
+                                     uint32_t flags, void* hip_stream) {
+  if (!h || !x || !gate_a || !gate_x || !lam || !h_out || !y) return MSS_ERR_NULL;
+  if (!dtype_ok(io_dtype)) return MSS_ERR_DTYPE;
+  constexpr int64_t most = 1LL << 31;
+  if (batch <= 0 || beams <= 0 || dim <= 0 || batch > most / beams || batch * beams > most / dim) return MSS_ERR_SHAPE;
+  const int64_t rows = batch * beams;
+  if (!stride_ok(x, x_stride, rows, dim) || !stride_ok(gate_a, gate_a_stride, rows, dim) ||
+      !stride_ok(gate_x, gate_x_stride, rows, dim) || !stride_ok(y, y_stride, rows, dim))
+    return MSS_ERR_SHAPE;
+  if (flags != 0 || !rate_ok(c)) return MSS_ERR_UNSUPPORTED;
+  if (!elem_aligned(x, io_dtype) || !elem_aligned(gate_a, io_dtype) || !elem_aligned(gate_x, io_dtype) ||
+      !elem_aligned(y, io_dtype) || !f32_aligned(h) || !f32_aligned(h_out) || !f32_aligned(lam) || !i64_aligned(parents))
+    return MSS_ERR_ALIGN;
+  // In place each thread reads its own element of h before it writes it.
+  const bool in_place = h_out == h && parents == nullptr;
+  const RowSet ins[] = {row_set(x, x_stride, rows, dim, io_dtype), row_set(gate_a, gate_a_stride, rows, dim, io_dtype),
+                        row_set(gate_x, gate_x_stride, rows, dim, io_dtype), dense_set(lam, dim * 4),
+                        dense_set(parents, rows * 8), dense_set(in_place ? nullptr : h, rows * dim * 4)};
+  const RowSet outs[] = {dense_set(h_out, rows * dim * 4), row_set(y, y_stride, rows, dim, io_dtype)};
+  if (!outputs_clear(outs, 2, ins, 6)) return MSS_ERR_ALIAS;
+  mss::RecurrenceStepParams p;
+  p.h = h;
+  p.parents = parents;
+  p.x = x;
+  p.gate_a = gate_a;
+  p.gate_x = gate_x;
+  p.lam = lam;
+  p.h_out = h_out;
+  p.y = y;
+  p.x_stride = x_stride;
+  p.gate_a_stride = gate_a_stride;
+  p.gate_x_stride = gate_x_stride;
+  p.y_stride = y_stride;
+  p.rows = rows;
+  p.beams = beams;
+  p.dim = dim;
+  p.c = c;
+  p.bf16 = io_dtype == MSS_BF16;
+  return hip_status(mss::launch_recurrence_step(p, static_cast<hipStream_t>(hip_stream)));
+}
+
+// ------------------------------------------------- beam search
+static mss_status beam_shape(int64_t batch, int64_t beams, int64_t vocab, int64_t n_out) {
+  if (batch <= 0 || beams <= 0 || vocab <= 0 || n_out <= 0 || batch > 65535 || vocab > (1LL << 24)) return MSS_ERR_SHAPE;
+  return beams > 64 || n_out > 64 || n_out > beams * vocab ? MSS_ERR_UNSUPPORTED : MSS_OK;
+}
+
+size_t mss_beam_select_workspace_size(int64_t batch, int64_t beams, int64_t vocab, int64_t n_out) {
+  return beam_shape(batch, beams, vocab, n_out) == MSS_OK ? mss::beam_select_workspace_bytes(batch, beams, vocab, n_out)
+                                                          : 0;
+}
+
+mss_status mss_beam_select(const void* logits, int64_t logits_stride, const float* scores, const uint8_t* finished,
+                           int64_t eos, float* out_scores, int64_t* parents, int64_t* tokens, uint8_t* out_finished,
+                           int64_t batch, int64_t beams, int64_t vocab, int64_t n_out, mss_dtype io_dtype,
+                           uint32_t flags, void* workspace, size_t workspace_bytes, void* hip_stream) {
+  if (!logits || !scores || !out_scores || !parents || !tokens) return MSS_ERR_NULL;
+  if (!dtype_ok(io_dtype)) return MSS_ERR_DTYPE;
+  const mss_status st = beam_shape(batch, beams, vocab, n_out);
+  if (st != MSS_OK) return st;
+  const int64_t rows = batch * beams;
+  if (!stride_ok(logits, logits_stride, rows, vocab)) return MSS_ERR_SHAPE;
+  if (flags != 0 || eos < -1 || eos >= vocab || (eos < 0 && (finished || out_finished))) return MSS_ERR_UNSUPPORTED;
+  if (!elem_aligned(logits, io_dtype) || !f32_aligned(scores) || !f32_aligned(out_scores) || !i64_aligned(parents) ||
+      !i64_aligned(tokens) || !aligned16(workspace))
+    return MSS_ERR_ALIGN;
+  const size_t need = mss::beam_select_workspace_bytes(batch, beams, vocab, n_out);
+  if (!workspace || workspace_bytes < need) return MSS_ERR_WORKSPACE;
+  const RowSet ins[] = {row_set(logits, logits_stride, rows, vocab, io_dtype), dense_set(scores, rows * 4),
+                        dense_set(finished, rows), dense_set(workspace, (int64_t)need)};
+  const RowSet outs[] = {dense_set(out_scores, batch * n_out * 4), dense_set(parents, batch * n_out * 8),
+                         dense_set(tokens, batch * n_out * 8), dense_set(out_finished, batch * n_out)};
+  if (!outputs_clear(outs, 4, ins, 4)) return MSS_ERR_ALIAS;
+  mss::BeamSelectParams p;
+  p.logits = logits;
+  p.scores = scores;
+  p.finished = finished;
+  p.out_scores = out_scores;
+  p.parents = parents;
+  p.tokens = tokens;
+  p.out_finished = out_finished;
+  p.stride = logits_stride;
+  p.batch = batch;
+  p.beams = beams;
+  p.vocab = vocab;
+  p.n_out = n_out;
+  p.eos = eos;
+  p.bf16 = io_dtype == MSS_BF16;
+  p.workspace = workspace;
+  return hip_status(mss::launch_beam_select(p, static_cast<hipStream_t>(hip_stream)));
+}
+
+mss_status mss_reorder_states(void* const* states, const int64_t* row_bytes, int64_t count, const int64_t* parents,
+                              int64_t batch, int64_t beams, void* hip_stream) {
+  if (!states || !row_bytes || !parents) return MSS_ERR_NULL;
+  if (count <= 0 || batch <= 0 || batch > 65535 || beams <= 0) return MSS_ERR_SHAPE;
+  if (beams > 64) return MSS_ERR_UNSUPPORTED;
+  for (int64_t s = 0; s < count; ++s) {
+    if (!states[s]) return MSS_ERR_NULL;
+    if (row_bytes[s] <= 0 || row_bytes[s] > (1LL << 30)) return MSS_ERR_SHAPE;
+  }
+  if (!i64_aligned(parents)) return MSS_ERR_ALIGN;
+  const int64_t rows = batch * beams;
+  for (int64_t s = 0; s < count; ++s) {
+    const Range r = range_of(states[s], (size_t)(rows * row_bytes[s]));
+    if (overlaps(r, range_of(parents, (size_t)rows * 8))) return MSS_ERR_ALIAS;
+    for (int64_t o = 0; o < s; ++o)
+      if (overlaps(r, range_of(states[o], (size_t)(rows * row_bytes[o])))) return MSS_ERR_ALIAS;
+  }
+  const mss::ReorderParams p{states, row_bytes, count, parents, batch, beams};
+  return hip_status(mss::launch_reorder_states(p, static_cast<hipStream_t>(hip_stream)));
 }
 
 }  // extern "C"

@@ -306,4 +306,92 @@ struct Wgrad8Params {
 size_t wgrad8_workspace_bytes(const void* dy, int64_t dy_stride, int64_t tokens, int64_t outs, int64_t ins);
 hipError_t launch_wgrad8(const Wgrad8Params& p, hipStream_t stream);
 
+// Gated linear recurrence (recurrence.hip, recurrence_step.hip).  Strides are of
+// rows ([batch * seqlen] of them), in elements.
+constexpr int kRecurrenceChunk = 64;  // steps between two of the states that the forward keeps
+struct RecurrenceFwdParams {
+  const void* x;
+  const void* gate_a;
+  const void* gate_x;
+  const float* lam;
+  const float* h0;            // nullable
+  const uint8_t* starts;      // nullable
+  void* y;
+  float* h_last;              // nullable
+  float* states;              // nullable, [batch][chunks][dim]
+  int64_t x_stride, gate_a_stride, gate_x_stride, y_stride;
+  int64_t batch, seqlen, dim;
+  float c;
+  bool bf16;
+  void* workspace;
+};
+size_t recurrence_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, bool bf16);
+hipError_t launch_recurrence_fwd(const RecurrenceFwdParams& p, hipStream_t stream);
+
+struct RecurrenceBwdParams {
+  const void* dy;
+  const void* x;
+  const void* gate_a;
+  const void* gate_x;
+  const float* lam;
+  const uint8_t* starts;      // nullable
+  const float* states;
+  const float* dh_last;       // nullable
+  void* dx;
+  void* dgate_a;
+  void* dgate_x;
+  float* dlam;
+  float* dh0;                 // nullable
+  int64_t dy_stride, x_stride, gate_a_stride, gate_x_stride, dx_stride, dgate_a_stride, dgate_x_stride;
+  int64_t batch, seqlen, dim;
+  float c;
+  bool bf16;
+  void* workspace;
+};
+size_t recurrence_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, bool bf16);
+hipError_t launch_recurrence_bwd(const RecurrenceBwdParams& p, hipStream_t stream);
+
+struct RecurrenceStepParams {
+  const float* h;
+  const int64_t* parents;     // nullable
+  const void* x;
+  const void* gate_a;
+  const void* gate_x;
+  const float* lam;
+  float* h_out;               // may be h without parents
+  void* y;
+  int64_t x_stride, gate_a_stride, gate_x_stride, y_stride;
+  int64_t rows, beams, dim;
+  float c;
+  bool bf16;
+};
+hipError_t launch_recurrence_step(const RecurrenceStepParams& p, hipStream_t stream);
+
+// Beam search (beam_select.hip, reorder.hip).
+struct BeamSelectParams {
+  const void* logits;         // rows of `stride` elements
+  const float* scores;
+  const uint8_t* finished;    // nullable
+  float* out_scores;
+  int64_t* parents;
+  int64_t* tokens;
+  uint8_t* out_finished;      // nullable
+  int64_t stride;
+  int64_t batch, beams, vocab, n_out;
+  int64_t eos;                // negative: none
+  bool bf16;
+  void* workspace;
+};
+size_t beam_select_workspace_bytes(int64_t batch, int64_t beams, int64_t vocab, int64_t n_out);
+hipError_t launch_beam_select(const BeamSelectParams& p, hipStream_t stream);
+
+struct ReorderParams {
+  void* const* states;        // host array of `count` device pointers
+  const int64_t* row_bytes;   // host array
+  int64_t count;
+  const int64_t* parents;
+  int64_t batch, beams;
+};
+hipError_t launch_reorder_states(const ReorderParams& p, hipStream_t stream);
+
 }  // namespace mss

@@ -29,6 +29,7 @@ enum : int { kSrcBf16 = 0, kSrcF32 = 1, kSrcP8 = 2 };
 
 // Rows at any element alignment: the hardware takes 16-byte accesses at any
 // address, the type only tells the compiler not to assume 16-byte alignment.
+typedef uint32_t u32x4_a1 __attribute__((ext_vector_type(4), aligned(1)));
 typedef uint32_t u32x4_a2 __attribute__((ext_vector_type(4), aligned(2)));
 typedef uint32_t u32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
 

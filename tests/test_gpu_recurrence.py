@@ -1,0 +1,378 @@
+"""GPU parity of the gated linear recurrence (scan, gradient, one-token step)
+against the fp64 reference.
+
+Tolerance, per element: the bound that oracle/recurrence.py carries along with
+each value (units of fp32 roundings through the same steps), plus half a bf16
+step of the value where it is stored in bf16."""
+import numpy as np
+import pytest
+import torch
+
+import selective_state_space_27_amd as mss
+from block_util import half_step
+from gpu_util import host64
+from oracle import recurrence as orec
+
+pytestmark = pytest.mark.gpu
+DT = {"bf16": torch.bfloat16, "fp32": torch.float32}
+GRADS = ("dx", "dgate_a", "dgate_x", "dlam", "dh0")
+
+
+def close(got, ref, bound, what):
+    dtype, got = got.dtype, host64(got)
+    assert got.shape == ref.shape, (what, got.shape, ref.shape)
+    tol = bound + 1e-37
+    tol = tol + (half_step(np.abs(ref) + tol) if dtype == torch.bfloat16 else 0.0)
+    off = np.abs(got - ref) - tol
+    assert np.isfinite(got).all() and off.max() <= 0, (
+        f"{what}: {np.abs(got - ref).max():.3e} off at {np.unravel_index(off.argmax(), off.shape)}, tol there "
+        f"{tol.reshape(-1)[off.argmax()]:.3e}")
+
+
+def gen(seed):
+    g = torch.Generator(device="cuda:0")
+    g.manual_seed(seed)
+    return g
+
+
+def randn(g, *shape):
+    return torch.randn(*shape, generator=g, device="cuda:0")
+
+
+def sliced(t, pad, shift=0):
+    """The same values as columns of a wider buffer of NaN: any row stride, any alignment."""
+    wide = torch.full((*t.shape[:-1], t.shape[-1] + pad), float("nan"), dtype=t.dtype, device=t.device)
+    view = wide[..., shift:shift + t.shape[-1]]
+    view.copy_(t)
+    return view
+
+
+def make(batch, length, dim, io, seed, h0=True, starts=0.0, pad=0, shift=0, lam=-4.0):
+    g = gen(seed)
+    d = {"x": randn(g, batch, length, dim) * torch.exp(randn(g, dim)), "gate_a": 1.5 * randn(g, batch, length, dim),
+         "gate_x": 1.5 * randn(g, batch, length, dim)}
+    d = {k: sliced(v.to(DT[io]), pad, shift) if pad else v.to(DT[io]) for k, v in d.items()}
+    d["lam"] = randn(g, dim) + lam
+    d["h0"] = randn(g, batch, dim) if h0 else None
+    d["starts"] = torch.rand(batch, length, generator=g, device="cuda:0") < starts if starts else None
+    d["dy"] = randn(g, batch, length, dim).to(DT[io])
+    d["dh_last"] = randn(g, batch, dim)
+    return d
+
+
+FWD = ("x", "gate_a", "gate_x", "lam")
+
+
+def host(d, *names):
+    out = {}
+    for k in names:
+        out[k] = None if d[k] is None else d[k].cpu().numpy() if k == "starts" else host64(d[k])
+    return out
+
+
+def check(d, io, c=8.0, adds=256):
+    exact = io == "fp32"
+    batch, length, dim = d["x"].shape
+    y, last, states = mss.gated_recurrence_fwd(*(d[k] for k in FWD), c=c, h0=d["h0"], starts=d["starts"],
+                                               return_last_state=True, keep_states=True, check_waits=True)
+    g = mss.gated_recurrence_bwd(d["dy"], *(d[k] for k in FWD), states, c=c, starts=d["starts"], dh_last=d["dh_last"],
+                                 want_dh0=True, check_waits=True)
+    ref, bound = orec.forward(**host(d, *FWD, "h0", "starts"), c=c, exact=exact)
+    close(y, ref, bound, "y")
+    close(last, ref[:, -1], bound[:, -1], "h_last")
+    first = np.zeros((batch, 1, dim)) if d["h0"] is None else host64(d["h0"])[:, None]
+    at = np.arange(0, length, mss.RECURRENCE_CHUNK)
+    close(states, np.concatenate([first, ref], 1)[:, at], np.concatenate([0 * first, bound], 1)[:, at], "states")
+    want = orec.backward(host64(d["dy"]), **host(d, *FWD, "h0", "starts", "dh_last"), c=c, exact=exact, adds=adds)
+    for k in GRADS:
+        close(g[k], *want[k], k)
+    return y, last, states, g
+
+
+# Lengths around the pieces a sequence is cut into, widths around what a workgroup holds; one step, one channel.
+SIZES = [(1, 1, 1), (2, 1, 64), (1, 2, 3), (3, 15, 16), (1, 16, 65), (2, 17, 2), (1, 63, 130), (2, 64, 127), (1, 65, 128),
+         (2, 127, 129), (1, 128, 255), (1, 129, 256), (2, 191, 257), (1, 193, 7), (3, 255, 40), (1, 257, 33),
+         (5, 300, 1), (2, 513, 96), (1, 1000, 1001), (1, 4099, 5), (4, 700, 130)]
+
+
+@pytest.mark.parametrize("batch,length,dim", SIZES)
+def test_sizes(batch, length, dim):
+    k = batch + length + dim
+    io = ("bf16", "fp32")[k % 2]
+    check(make(batch, length, dim, io, k, h0=k % 3 != 0, starts=0.02 if k % 5 < 2 else 0.0), io)
+
+
+@pytest.mark.parametrize("io", ["bf16", "fp32"])
+@pytest.mark.parametrize("pad,shift", [(1, 0), (2, 2), (7, 3), (64, 1), (128, 64)])
+def test_strides_and_alignments(io, pad, shift):
+    check(make(2, 150, 130, io, pad, starts=0.01, pad=pad, shift=shift), io)
+    check(make(1, 70, 129, io, pad + 1, pad=pad, shift=shift), io)
+
+
+@pytest.mark.parametrize("io", ["bf16", "fp32"])
+@pytest.mark.parametrize("lam", [-30.0, -10.0, 0.0, 3.0])
+def test_slow_and_fast_decays(io, lam):
+    """From a state that is hardly touched to one that holds a step or two."""
+    check(make(2, 400, 70, io, 17, lam=lam), io)
+
+
+@pytest.mark.parametrize("io", ["bf16", "fp32"])
+def test_long_sequences(io):
+    """Many pieces of one sequence, and of several at once."""
+    check(make(1, 20000, 66, io, 5, starts=0.0005, lam=-6.0), io, adds=1024)
+    check(make(3, 9000, 200, io, 6, lam=-6.0), io, adds=1024)
+
+
+def test_other_rate():
+    check(make(2, 130, 50, "fp32", 3), "fp32", c=1.0)
+
+
+def test_starts_at_every_place():
+    for at in ([0], [63], [64], [65], [127, 128, 129], [199], list(range(200))):
+        d = make(1, 200, 70, "fp32", at[0])
+        d["starts"] = torch.zeros(1, 200, dtype=torch.uint8, device="cuda:0")
+        d["starts"][0, at] = 1
+        check(d, "fp32")
+
+
+@pytest.mark.parametrize("at", [0, 64, 100, 640])
+def test_a_start_forgets_whatever_was_before(at):
+    """NaN and infinities before a start change nothing after it, forward; nothing before it, backward."""
+    d = make(1, 900, 70, "fp32", at + 1)
+    d["starts"] = torch.zeros(1, 900, dtype=torch.bool, device="cuda:0")
+    d["starts"][0, at] = True
+    y, states = mss.gated_recurrence_fwd(*(d[k] for k in FWD), h0=d["h0"], starts=d["starts"], keep_states=True)
+    g = mss.gated_recurrence_bwd(d["dy"], *(d[k] for k in FWD), states, starts=d["starts"])
+    e = dict(d, x=d["x"].clone(), h0=d["h0"].clone(), dy=d["dy"].clone())
+    e["h0"][0, ::2], e["h0"][0, 1::2] = float("nan"), float("inf")
+    if at:
+        e["x"][0, at - 1] = float("nan")
+        e["x"][0, at // 2] = float("-inf")
+    z, last, _ = mss.gated_recurrence_fwd(*(e[k] for k in FWD), h0=e["h0"], starts=e["starts"], return_last_state=True,
+                                          keep_states=True)
+    assert torch.equal(z[:, at:], y[:, at:]) and torch.isfinite(last).all()
+    assert at == 0 or not torch.isfinite(z[:, at - 1]).any()
+    f = dict(d, dy=d["dy"].clone())
+    f["dy"][0, at] = float("nan")
+    h = mss.gated_recurrence_bwd(f["dy"], *(d[k] for k in FWD), states, starts=d["starts"], want_dh0=True)
+    for k in ("dx", "dgate_a", "dgate_x"):
+        assert torch.equal(h[k][:, :at], g[k][:, :at]), k
+        assert torch.isnan(h[k][:, at]).all(), k
+    assert torch.isfinite(h["dh0"]).all()
+
+
+def test_a_nan_stays_in_its_channel_and_after_its_step():
+    d = make(2, 700, 130, "fp32", 8, lam=0.0)  # fast decays: products of many steps underflow
+    y = mss.gated_recurrence_fwd(*(d[k] for k in FWD), h0=d["h0"])
+    d["x"][1, 200, 77] = float("nan")
+    z = mss.gated_recurrence_fwd(*(d[k] for k in FWD), h0=d["h0"])
+    gone = torch.isnan(z)
+    assert gone[1, 200:, 77].all() and int(gone.sum()) == 500
+    assert torch.equal(z[~gone], y[~gone])
+    for gate in ("gate_a", "gate_x"):
+        d = make(1, 300, 66, "bf16", 9)
+        d[gate][0, 150, 3] = float("nan")
+        z = mss.gated_recurrence_fwd(*(d[k] for k in FWD), h0=d["h0"])
+        assert torch.isnan(z[0, 150:, 3]).all() and int(torch.isnan(z).sum()) == 150
+
+
+@pytest.mark.parametrize("io", ["bf16", "fp32"])
+def test_gates_fully_open_and_closed(io):
+    d = make(1, 200, 64, io, 10)
+    inf = float("inf")
+    d["gate_a"][0, 50:60], d["gate_a"][0, 60:70] = inf, -inf
+    d["gate_x"][0, 55:65:2], d["gate_x"][0, 56:66:2] = inf, -inf
+    d["gate_a"][0, 100:104], d["gate_x"][0, 102:106] = -120.0, -120.0
+    d["lam"][:8] = torch.tensor([-200.0, -100.0, -60.0, 60.0, 100.0, 200.0, 1e30, 88.0])
+    y, last, states = mss.gated_recurrence_fwd(*(d[k] for k in FWD), h0=d["h0"], return_last_state=True,
+                                               keep_states=True)
+    g = mss.gated_recurrence_bwd(d["dy"], *(d[k] for k in FWD), states, want_dh0=True)
+    assert torch.isfinite(y).all() and all(torch.isfinite(g[k]).all() for k in GRADS)
+    ref = mss.gated_recurrence_fwd(*(d[k].clamp(-150, 150) if k.startswith("gate") else d[k] for k in FWD),
+                                   h0=d["h0"])
+    assert torch.equal(y, ref)
+    assert (g["dgate_a"][0, 50:70] == 0).all() and (g["dgate_x"][0, 55:65] == 0).all()
+
+
+def test_an_open_gate_of_a_slow_channel_in_a_fast_one_s_row():
+    """Decays of both kinds in one row: whatever is chosen for a workgroup's channels holds for each."""
+    d = make(1, 150, 128, "fp32", 12)
+    d["lam"] = torch.linspace(-12, 6, 128, device="cuda:0")
+    check(d, "fp32")
+
+
+@pytest.mark.parametrize("io", ["bf16", "fp32"])
+def test_given_outputs_and_their_surroundings(io):
+    """Slices of one gradient buffer as outputs; what lies around them stays."""
+    batch, length, dim = 2, 130, 67
+    d = make(batch, length, dim, io, 20)
+    y, states = mss.gated_recurrence_fwd(*(d[k] for k in FWD), h0=d["h0"], keep_states=True)
+    g = mss.gated_recurrence_bwd(d["dy"], *(d[k] for k in FWD), states)
+    wide = torch.full((batch, length, 3 * dim + 10), 7.0, dtype=DT[io], device="cuda:0")
+    out = wide[..., 5:5 + dim]
+    got = mss.gated_recurrence_fwd(*(d[k] for k in FWD), h0=d["h0"], out=out)
+    assert got is out and torch.equal(out, y)
+    assert (wide[..., :5] == 7).all() and (wide[..., 5 + dim:] == 7).all()
+    wide.fill_(7.0)
+    cuts = {k: wide[..., 4 + j * (dim + 1):4 + j * (dim + 1) + dim] for j, k in enumerate(("dx", "dgate_a", "dgate_x"))}
+    mss.gated_recurrence_bwd(d["dy"], *(d[k] for k in FWD), states, **cuts)
+    for k, v in cuts.items():
+        assert torch.equal(v, g[k]), k
+        v.fill_(7.0)
+    assert (wide == 7).all()
+
+
+def test_same_call_same_bits():
+    d = make(2, 6000, 300, "bf16", 30)
+
+    def once():
+        y, last, states = mss.gated_recurrence_fwd(*(d[k] for k in FWD), h0=d["h0"], return_last_state=True,
+                                                   keep_states=True)
+        g = mss.gated_recurrence_bwd(d["dy"], *(d[k] for k in FWD), states, dh_last=d["dh_last"], want_dh0=True)
+        return [y, last, states] + [g[k] for k in GRADS]
+
+    first = once()
+    for _ in range(4):
+        assert all(torch.equal(a, b) for a, b in zip(first, once()))
+
+
+def test_two_streams_at_once():
+    a, b = make(1, 8000, 200, "bf16", 31), make(2, 5000, 130, "fp32", 32)
+    want = [mss.gated_recurrence_fwd(*(d[k] for k in FWD), h0=d["h0"]) for d in (a, b)]
+    torch.cuda.synchronize()
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    got = [[], []]
+    for _ in range(5):
+        for i, d in enumerate((a, b)):
+            got[i].append(mss.gated_recurrence_fwd(*(d[k] for k in FWD), h0=d["h0"], stream=streams[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(t, want[i]) for t in got[i])
+
+
+def test_captured_and_replayed():
+    """Forward and backward in one graph, replayed on new inputs with eager work between."""
+    d = make(2, 3000, 150, "bf16", 33, starts=0.001)
+    e = make(2, 3000, 150, "bf16", 34, starts=0.001)
+    names = FWD + ("h0", "starts", "dy", "dh_last")
+
+    def once():
+        y, last, states = mss.gated_recurrence_fwd(*(d[k] for k in FWD), h0=d["h0"], starts=d["starts"],
+                                                   return_last_state=True, keep_states=True)
+        g = mss.gated_recurrence_bwd(d["dy"], *(d[k] for k in FWD), states, starts=d["starts"], dh_last=d["dh_last"],
+                                     want_dh0=True)
+        return [y, last] + [g[k] for k in GRADS]
+
+    kept = {k: d[k].clone() for k in names}
+    sets = kept, {k: e[k] for k in names}
+    want = []
+    for s in sets:
+        for k in names:
+            d[k].copy_(s[k])
+        want.append([t.clone() for t in once()])
+    graph = torch.cuda.CUDAGraph()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        once()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        got = once()
+    for i in (0, 1, 1, 0, 1):
+        for k in names:
+            d[k].copy_(sets[i][k])
+        graph.replay()
+        eager = once()
+        torch.cuda.synchronize()
+        for a, b, c in zip(got, want[i], eager):
+            assert torch.equal(a, b) and torch.equal(c, b)
+
+
+# ------------------------------------------------------------------------------------------------- one token
+@pytest.mark.parametrize("io", ["bf16", "fp32"])
+@pytest.mark.parametrize("rows,dim", [(1, 1), (1, 2560), (3, 65), (7, 128), (128, 127), (2, 1001)])
+def test_step(io, rows, dim):
+    d = make(rows, 1, dim, io, rows + dim, pad=(rows + dim) % 4, shift=(rows + dim) % 4 // 2)
+    one = [d[k][:, 0] for k in FWD[:3]]
+    ref, bound = orec.forward(**host(d, *FWD, "h0"), exact=io == "fp32")
+    h = d["h0"].clone()
+    y, new = mss.gated_recurrence_step(h, *one, d["lam"])
+    assert new is h
+    close(y, ref[:, 0], bound[:, 0], "y")
+    close(h, ref[:, 0], bound[:, 0], "h")
+    out = torch.empty_like(h)
+    y2, new = mss.gated_recurrence_step(d["h0"], *one, d["lam"], h_out=out)
+    assert new is out and torch.equal(out, h) and torch.equal(y2, y)
+
+
+@pytest.mark.parametrize("dim", [64, 67, 130])
+def test_step_from_parents(dim):
+    batch, beams = 3, 5
+    d = make(batch * beams, 1, dim, "bf16", dim)
+    one = [d[k][:, 0] for k in FWD[:3]]
+    parents = torch.randint(0, beams, (batch, beams), generator=gen(dim), device="cuda:0")
+    rows = (torch.arange(batch, device="cuda:0")[:, None] * beams + parents).flatten()
+    y, h = mss.gated_recurrence_step(d["h0"], *one, d["lam"], parents=parents)
+    z, want = mss.gated_recurrence_step(d["h0"][rows].contiguous(), *one, d["lam"])
+    assert torch.equal(y, z) and torch.equal(h, want)
+    # An index outside the beams stands for the row itself.
+    bad = parents.clone()
+    bad[0, 1], bad[1, 0], bad[2, 4], bad[2, 0] = -1, beams, 1 << 40, -(1 << 40)
+    own = torch.arange(beams, device="cuda:0").expand(batch, beams)
+    y, h = mss.gated_recurrence_step(d["h0"], *one, d["lam"], parents=bad)
+    fixed = torch.where((bad < 0) | (bad >= beams), own, bad)
+    z, want = mss.gated_recurrence_step(d["h0"], *one, d["lam"], parents=fixed)
+    assert torch.equal(y, z) and torch.equal(h, want)
+
+
+def test_prompt_then_tokens():
+    """The scan's last state carries on in the one-token step."""
+    d = make(2, 90, 140, "bf16", 40, pad=6, shift=1)
+    y = mss.gated_recurrence_fwd(*(d[k] for k in FWD), h0=d["h0"])
+    _, h = mss.gated_recurrence_fwd(*(d[k][:, :70].contiguous() if k != "lam" else d[k] for k in FWD), h0=d["h0"],
+                                    return_last_state=True)
+    ref, bound = orec.forward(**host(d, *FWD, "h0"), exact=False)
+    for t in range(70, 90):
+        out, h = mss.gated_recurrence_step(h, *(d[k][:, t] for k in FWD[:3]), d["lam"])
+        close(out, ref[:, t], bound[:, t], f"step {t}")
+    close(y, ref, bound, "y")
+
+
+# -------------------------------------------------------------------------------------------------- refusals
+def test_refusals():
+    d = make(2, 5, 8, "fp32", 50)
+    x, a, i, lam = (d[k] for k in FWD)
+    with pytest.raises(TypeError):
+        mss.gated_recurrence_fwd(x, a.bfloat16(), i, lam)
+    with pytest.raises(TypeError):
+        mss.gated_recurrence_fwd(x.half(), a.half(), i.half(), lam)
+    with pytest.raises(ValueError):
+        mss.gated_recurrence_fwd(x, a[:, :4], i, lam)
+    with pytest.raises(ValueError):
+        mss.gated_recurrence_fwd(x[0], a[0], i[0], lam)
+    with pytest.raises(ValueError):
+        mss.gated_recurrence_fwd(x[:, :0], a[:, :0], i[:, :0], lam)
+    with pytest.raises(ValueError):
+        mss.gated_recurrence_fwd(x, a, i, lam[:7])
+    with pytest.raises(TypeError):
+        mss.gated_recurrence_fwd(x, a, i, lam, starts=torch.zeros(2, 5, device="cuda:0"))
+    with pytest.raises(mss.MambaScanError):
+        mss.gated_recurrence_fwd(x, a, i, lam, c=0.0)
+    with pytest.raises(mss.MambaScanError):
+        mss.gated_recurrence_fwd(x, a, i, lam, out=x)
+    _, states = mss.gated_recurrence_fwd(x, a, i, lam, keep_states=True)
+    with pytest.raises(ValueError):
+        mss.gated_recurrence_bwd(d["dy"], x, a, i, lam, states[:, :, :7])
+    with pytest.raises(TypeError):
+        mss.gated_recurrence_bwd(d["dy"], x, a, None, lam, states)
+    with pytest.raises(mss.MambaScanError):
+        mss.gated_recurrence_bwd(d["dy"], x, a, i, lam, states, dx=d["dy"])
+    h, one = d["h0"].clone(), [t[:, 0] for t in (x, a, i)]
+    parents = torch.zeros(1, 2, dtype=torch.int64, device="cuda:0")
+    with pytest.raises(mss.MambaScanError):
+        mss.gated_recurrence_step(h, *one, lam, parents=parents, h_out=h)
+    with pytest.raises(ValueError):
+        mss.gated_recurrence_step(h, *one, lam, parents=parents[:, :1])
+    with pytest.raises(TypeError):
+        mss.gated_recurrence_step(h, *one, lam, parents=parents.int())
+    with pytest.raises(ValueError):
+        mss.gated_recurrence_step(h[:, :7].contiguous(), *one, lam)
