@@ -1,7 +1,17 @@
 // Gated linear recurrence: scan over whole sequences and its gradient (gfx950).
 // Definitions in include/mambascan.h, arithmetic in recurrence.hpp.
 //
-// A thread walks one channel of one sequence.
+// h_t = a_t h_{t-1} + b_t is cut along t: a wave holds T steps of 64 V channels
+// (V neighbouring ones a lane) in registers and runs them from a zero state,
+// which gives per channel the product A of its decays and its end state H; a
+// workgroup's W waves, side by side in time, fold these in LDS; workgroups hand
+// states on through memory (Chain).  Then every wave adds what its entering
+// state has become at each step.  Inputs are read once and outputs written once,
+// whatever the length.
+//
+// Where a packed sequence starts, what was before counts as zero even if it is
+// NaN: A is not multiplied in but skipped (a start is the same for all channels,
+// so the choice is a scalar one).
 #include "launch.hpp"
 #include "norm_common.hpp"
 #include "recurrence.hpp"
@@ -9,115 +19,621 @@
 namespace mss {
 namespace {
 
-template <bool BF16>
-__device__ __forceinline__ float load_el(const void* p, int64_t i) {
-  if constexpr (BF16) return bf16_to_f32(static_cast<const uint16_t*>(p)[i]);
-  else return static_cast<const float*>(p)[i];
-}
-template <bool BF16>
-__device__ __forceinline__ void store_el(void* p, int64_t i, float v) {
-  if constexpr (BF16) static_cast<uint16_t*>(p)[i] = f32_to_bf16(v);
-  else static_cast<float*>(p)[i] = v;
+// ------------------------------------------------------------ pieces in order
+// A piece is one workgroup's steps of one stream (64 V channels of a batch row).
+// Pieces take their place in order of start (a ticket): s-th in its stream, all
+// streams' s-th before any (s+1)-th.  A piece that has its own A and H publishes
+// them (kOwn), looks back for the nearest piece whose end state is known (kEnd),
+// folds what lies between from there on, and publishes its own end state.  The
+// fold is the same sequence of operations wherever it begins, so results do not
+// depend on timing.  What is waited for belongs to pieces that have started and
+// that publish it before they wait themselves.
+//
+// Values and flags move through relaxed agent-scope atomics, coherent across the
+// dies: the values are stored and waited for before the flag is set, and loaded
+// after the flag has been seen.
+enum : int { kOwn = 1, kEnd = 2 };
+constexpr int kMaxSpinsChain = 1 << 22;
+constexpr int kChainHeader = 64;  // ints before the flags: status word, ticket
+
+struct Chain {
+  int* status;   // null: one piece a stream, nothing is handed on
+  int* ticket;
+  int* flags;    // [place][stream]
+  float* own;    // [place][stream][2][64 V]: A, H
+  float* end;    // [place][stream][64 V]
+  int streams;
+};
+
+__global__ void __launch_bounds__(256) chain_clear_kernel(int* p, int64_t n) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) p[i] = 0;
 }
 
-template <bool BF16>
-__global__ void __launch_bounds__(64) recurrence_fwd_kernel(RecurrenceFwdParams p) {
-  const int64_t d = (int64_t)blockIdx.x * 64 + threadIdx.x;
-  if (d == 0 && blockIdx.y == 0) *static_cast<int*>(p.workspace) = 0;  // the status word: nothing waits here
-  if (d >= p.dim) return;
-  const int64_t b = blockIdx.y, nchunks = (p.seqlen + kRecurrenceChunk - 1) / kRecurrenceChunk;
-  const float k = p.c * softplus_of(p.lam[d]);
-  float h = p.h0 != nullptr ? p.h0[b * p.dim + d] : 0.f;
-  for (int64_t t = 0; t < p.seqlen; ++t) {
-    const int64_t row = b * p.seqlen + t;
-    if (p.states != nullptr && t % kRecurrenceChunk == 0)
-      p.states[(b * nchunks + t / kRecurrenceChunk) * p.dim + d] = h;
-    const float x = load_el<BF16>(p.x, row * p.x_stride + d);
-    const float m = one_minus_exp<false>(k * sigmoid_of<!BF16>(load_el<BF16>(p.gate_a, row * p.gate_a_stride + d)));
-    const float in = sqrtf(m * (2.0f - m)) * sigmoid_of<!BF16>(load_el<BF16>(p.gate_x, row * p.gate_x_stride + d)) * x;
-    const bool start = p.starts != nullptr && p.starts[row] != 0;
-    h = (start ? 0.f : __builtin_fmaf(-m, h, h)) + in;
-    store_el<BF16>(p.y, row * p.y_stride + d, h);
+template <int V>
+__device__ __forceinline__ void put(float* p, const float (&v)[V]) {
+  if constexpr (V == 2) {
+    const uint64_t w = (uint64_t)__float_as_uint(v[1]) << 32 | __float_as_uint(v[0]);
+    __hip_atomic_store(reinterpret_cast<uint64_t*>(p), w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  } else {
+    __hip_atomic_store(p, v[0], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
-  if (p.h_last != nullptr) p.h_last[b * p.dim + d] = h;
+}
+template <int V>
+__device__ __forceinline__ void take(const float* p, float (&v)[V]) {
+  if constexpr (V == 2) {
+    const uint64_t w = __hip_atomic_load(reinterpret_cast<const uint64_t*>(p), __ATOMIC_RELAXED,
+                                         __HIP_MEMORY_SCOPE_AGENT);
+    v[0] = __uint_as_float((uint32_t)w), v[1] = __uint_as_float((uint32_t)(w >> 32));
+  } else {
+    v[0] = __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+}
+__device__ __forceinline__ void set_flag(int* f, int lane, int v) {
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // what the flag stands for has been stored
+  if (lane == 0) __hip_atomic_store(f, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-template <bool BF16>
-__global__ void __launch_bounds__(64) recurrence_bwd_kernel(RecurrenceBwdParams p, float* part) {
-  __shared__ float before[kRecurrenceChunk][64];
-  const int64_t d = (int64_t)blockIdx.x * 64 + threadIdx.x;
-  if (d == 0 && blockIdx.y == 0) *static_cast<int*>(p.workspace) = 0;  // the status word: nothing waits here
-  if (d >= p.dim) return;
-  const int64_t b = blockIdx.y, nchunks = (p.seqlen + kRecurrenceChunk - 1) / kRecurrenceChunk;
-  const float sp = softplus_of(p.lam[d]), k = p.c * sp;
-  float e = p.dh_last != nullptr ? p.dh_last[b * p.dim + d] : 0.f;  // gradient of the state after the step
-  float dlam = 0.f;
-  for (int64_t ch = nchunks - 1; ch >= 0; --ch) {
-    const int64_t t0 = ch * kRecurrenceChunk;
-    const int n = (int)(p.seqlen - t0 < kRecurrenceChunk ? p.seqlen - t0 : kRecurrenceChunk);
-    float h = p.states[(b * nchunks + ch) * p.dim + d];
-    for (int j = 0; j < n; ++j) {
-      const int64_t row = b * p.seqlen + t0 + j;
-      before[j][threadIdx.x] = h;
-      const float m = one_minus_exp<false>(k * sigmoid_of<!BF16>(load_el<BF16>(p.gate_a, row * p.gate_a_stride + d)));
-      const float in = sqrtf(m * (2.0f - m)) *
-                       sigmoid_of<!BF16>(load_el<BF16>(p.gate_x, row * p.gate_x_stride + d)) *
-                       load_el<BF16>(p.x, row * p.x_stride + d);
-      const bool start = p.starts != nullptr && p.starts[row] != 0;
-      h = (start ? 0.f : __builtin_fmaf(-m, h, h)) + in;
+// What enters the piece at `place` of `stream` (wave 0's lanes; `first` at place
+// 0), given its own A and H; publishes what later pieces need.  `cut`: a sequence
+// starts inside, so its end state does not depend on what enters.
+template <int V>
+__device__ __forceinline__ void chain_carry(const Chain& c, int place, int stream, bool last, bool cut,
+                                            const float (&own_a)[V], const float (&own_h)[V], const float (&first)[V],
+                                            float (&carry)[V]) {
+  const int lane = threadIdx.x & 63;
+  const int64_t id = (int64_t)place * c.streams + stream;
+  float* end = c.end + id * (64 * V) + lane * V;
+  float h[V];
+  if (place == 0) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) carry[v] = first[v];
+  } else {
+    if (!last) {
+      if (cut) {
+        put<V>(end, own_h);
+      } else {
+        float* own = c.own + id * (128 * V) + lane * V;
+        put<V>(own, own_a);
+        put<V>(own + 64 * V, own_h);
+      }
+      set_flag(c.flags + id, lane, cut ? kEnd : kOwn);
     }
-    for (int j = n - 1; j >= 0; --j) {
-      const int64_t row = b * p.seqlen + t0 + j;
-      const bool start = p.starts != nullptr && p.starts[row] != 0;
-      float rr, ri;
-      const float r = sigmoid_of<!BF16>(load_el<BF16>(p.gate_a, row * p.gate_a_stride + d), rr);
-      const float i = sigmoid_of<!BF16>(load_el<BF16>(p.gate_x, row * p.gate_x_stride + d), ri);
-      const float x = load_el<BF16>(p.x, row * p.x_stride + d);
-      const float s = finite_decay(k * r), m = one_minus_exp<false>(s), beta = sqrtf(m * (2.0f - m)), a = 1.0f - m;
-      const float g = load_el<BF16>(p.dy, row * p.dy_stride + d) + e;
-      const float gi = g * i, gix = gi * x;
-      const float from_beta = m > 0.f ? a * a * (s / beta) * gix : (s - s) * gix;
-      const float big = from_beta - (start ? 0.f : s * a * (g * before[j][threadIdx.x]));
-      store_el<BF16>(p.dx, row * p.dx_stride + d, gi * beta);
-      store_el<BF16>(p.dgate_x, row * p.dgate_x_stride + d, gix * beta * ri);
-      store_el<BF16>(p.dgate_a, row * p.dgate_a_stride + d, big * rr);
-      dlam += big;
-      e = start ? 0.f : __builtin_fmaf(-m, g, g);
+    // Lane l looks at the piece l + 1 places back.
+    const int back = place - 1 - lane;
+    const int* flag = c.flags + (int64_t)(back > 0 ? back : 0) * c.streams + stream;
+    int near = 0;  // of the nearest known end state
+    for (int spins = 0;; ++spins) {
+      const int f = back >= 0 ? __hip_atomic_load(flag, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0;
+      const uint64_t ends = __ballot(f == kEnd), ready = __ballot(f != 0);
+      near = ends != 0 ? __builtin_ctzll(ends) : 0;
+      if (ends != 0 && (~ready & ((1ull << near) - 1)) == 0) break;
+      if (spins > kMaxSpinsChain) {  // never expected; keeps every wait finite, reported through the status word
+        if (lane == 0) __hip_atomic_store(c.status, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        near = 0;
+        break;
+      }
+      __builtin_amdgcn_s_sleep(1);
+    }
+    int64_t at = (int64_t)(place - 1 - near) * c.streams + stream;
+    take<V>(c.end + at * (64 * V) + lane * V, carry);
+    for (int i = near; i > 0; i -= 4) {
+      float a[4][V], b[4][V];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int64_t from = at + (int64_t)(j + 1 <= i ? j + 1 : i) * c.streams;
+        const float* own = c.own + from * (128 * V) + lane * V;
+        take<V>(own, a[j]);
+        take<V>(own + 64 * V, b[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j + 1 <= i)
+#pragma unroll
+          for (int v = 0; v < V; ++v) carry[v] = __builtin_fmaf(a[j][v], carry[v], b[j][v]);
+      at += (int64_t)4 * c.streams;
     }
   }
-  if (p.dh0 != nullptr) p.dh0[b * p.dim + d] = e;
-  part[b * p.dim + d] = dlam * softplus_rate(p.lam[d], sp);
+  if (last || (cut && place != 0)) return;
+#pragma unroll
+  for (int v = 0; v < V; ++v) h[v] = cut ? own_h[v] : __builtin_fmaf(own_a[v], carry[v], own_h[v]);
+  put<V>(end, h);
+  set_flag(c.flags + id, lane, kEnd);
 }
 
-dim3 grid_of(int64_t batch, int64_t dim) { return dim3((unsigned)((dim + 63) / 64), (unsigned)batch); }
+// ------------------------------------------------------------ rows
+// V neighbouring channels of a row as loaded: two bf16 in a word, or one value.
+template <bool BF16, int V>
+__device__ __forceinline__ uint32_t load_raw_at(const void* row, uint32_t ch) {
+  if constexpr (BF16 && V == 1) return static_cast<const uint16_t*>(row)[ch];
+  else if constexpr (BF16) return *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(row) + ch);
+  else return static_cast<const uint32_t*>(row)[ch];
+}
+template <bool BF16, int V>
+__device__ __forceinline__ float widen_at(uint32_t w, int v) {
+  if constexpr (!BF16) return __uint_as_float(w);
+  else return v == 0 ? bf16_lo(w) : bf16_hi(w);
+}
+template <bool BF16, int V>
+__device__ __forceinline__ void store_at(void* row, uint32_t ch, const float (&o)[V]) {
+  if constexpr (BF16 && V == 1) static_cast<uint16_t*>(row)[ch] = f32_to_bf16(o[0]);
+  else if constexpr (BF16) *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(row) + ch) = pack_bf16x2(o[0], o[1]);
+  else static_cast<float*>(row)[ch] = o[0];
+}
+template <bool BF16>
+__device__ __forceinline__ const void* row_at(const void* p, int64_t row, int64_t stride) {
+  return static_cast<const char*>(p) + row * stride * (BF16 ? 2 : 4);
+}
+template <bool BF16>
+__device__ __forceinline__ void* row_at(void* p, int64_t row, int64_t stride) {
+  return static_cast<char*>(p) + row * stride * (BF16 ? 2 : 4);
+}
 
-}  // namespace
+// Where a wave works: which piece, its steps, its lane's channels.
+template <int V, int W, int T>
+struct WavePlace {
+  int place, stream, wave;
+  int64_t b, t0;     // batch row, first step
+  int n;             // steps that exist
+  uint32_t ch;       // first channel, kept inside the row
+  bool ok;           // whether it exists
+};
 
-size_t recurrence_fwd_workspace_bytes(int64_t, int64_t, int64_t, bool) { return 256; }
+// `piece` in order along time; a lane past the last channel repeats it.
+template <int V, int W, int T>
+__device__ __forceinline__ WavePlace<V, W, T> wave_place(int64_t id, int streams, int blocks, int64_t pieces,
+                                                         bool reversed, int64_t seqlen, int64_t dim) {
+  WavePlace<V, W, T> w;
+  w.place = (int)(id / streams);
+  w.stream = (int)(id - (int64_t)w.place * streams);
+  w.wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  w.b = w.stream / blocks;
+  const int64_t piece = reversed ? pieces - 1 - w.place : w.place;
+  w.t0 = piece * (W * T) + w.wave * T;
+  const int64_t left = seqlen - w.t0;
+  w.n = left < 0 ? 0 : left < T ? (int)left : T;
+  const int64_t c = (int64_t)(w.stream - (int)w.b * blocks) * (64 * V) + (threadIdx.x & 63) * V;
+  w.ok = c < dim;
+  w.ch = (uint32_t)(w.ok ? c : dim - V);
+  return w;
+}
 
-hipError_t launch_recurrence_fwd(const RecurrenceFwdParams& p, hipStream_t stream) {
-  if (p.bf16) hipLaunchKernelGGL(recurrence_fwd_kernel<true>, grid_of(p.batch, p.dim), dim3(64), 0, stream, p);
-  else hipLaunchKernelGGL(recurrence_fwd_kernel<false>, grid_of(p.batch, p.dim), dim3(64), 0, stream, p);
+// Bit j: a sequence starts at the wave's step j.
+template <int T>
+__device__ __forceinline__ uint64_t start_bits(const uint8_t* starts, int64_t row, int n) {
+  if (starts == nullptr) return 0;
+  const int lane = threadIdx.x & 63;
+  return __ballot(lane < n && starts[row + (lane < n ? lane : 0)] != 0);
+}
+
+// ------------------------------------------------------------ forward
+struct FwdArgs {
+  RecurrenceFwdParams p;
+  Chain chain;
+  int blocks;      // of channels
+  int64_t pieces;  // of a stream
+};
+
+template <bool BF16, int V, int W, int T>
+__global__ void __launch_bounds__(W * 64) recurrence_fwd_kernel(FwdArgs a) {
+  __shared__ float lds_a[W][64 * V], lds_h[W][64 * V], lds_carry[64 * V];
+  __shared__ int lds_cut[W], lds_id;
+  const RecurrenceFwdParams& p = a.p;
+  int64_t id = blockIdx.x;
+  if (a.chain.status != nullptr) {
+    if (threadIdx.x == 0) lds_id = atomicAdd(a.chain.ticket, 1);
+    __syncthreads();
+    id = __builtin_amdgcn_readfirstlane(lds_id);
+  } else if (id == 0 && threadIdx.x == 0) {
+    *static_cast<int*>(p.workspace) = 0;  // the status word: nothing waits
+  }
+  const auto w = wave_place<V, W, T>(id, a.chain.streams, a.blocks, a.pieces, false, p.seqlen, p.dim);
+  const int lane = threadIdx.x & 63;
+  const int64_t row0 = w.b * p.seqlen + w.t0;
+
+  uint32_t rx[T], ra[T], ri[T];
+  if (w.n > 0) {
+#pragma unroll
+    for (int j = 0; j < T; ++j) {
+      const int64_t row = row0 + (j < w.n ? j : w.n - 1);
+      ra[j] = load_raw_at<BF16, V>(row_at<BF16>(p.gate_a, row, p.gate_a_stride), w.ch);
+      ri[j] = load_raw_at<BF16, V>(row_at<BF16>(p.gate_x, row, p.gate_x_stride), w.ch);
+      rx[j] = load_raw_at<BF16, V>(row_at<BF16>(p.x, row, p.x_stride), w.ch);
+    }
+  }
+  const uint64_t starts = w.n > 0 ? start_bits<T>(p.starts, row0, w.n) : 0;
+  float k[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) k[v] = p.c * softplus_of(p.lam[w.ch + v]);
+
+  float m[T][V], hl[T][V], ha[V], hh[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) ha[v] = 1.0f, hh[v] = 0.0f;
+  if (w.n > 0) {
+#pragma unroll
+    for (int j = 0; j < T; ++j) {
+      const bool live = j < w.n, start = starts >> j & 1;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float mj = one_minus_exp<false>(k[v] * sigmoid_of<!BF16>(widen_at<BF16, V>(ra[j], v)));
+        const float in = __builtin_amdgcn_sqrtf(mj * (2.0f - mj)) * sigmoid_of<!BF16>(widen_at<BF16, V>(ri[j], v)) *
+                         widen_at<BF16, V>(rx[j], v);
+        m[j][v] = mj;
+        const float h = (start ? 0.0f : __builtin_fmaf(-mj, hh[v], hh[v])) + in;
+        hh[v] = live ? h : hh[v];
+        ha[v] = live ? __builtin_fmaf(-mj, ha[v], ha[v]) : ha[v];
+        hl[j][v] = hh[v];
+      }
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) lds_a[w.wave][lane * V + v] = ha[v], lds_h[w.wave][lane * V + v] = hh[v];
+  if (lane == 0) lds_cut[w.wave] = starts != 0;
+  __syncthreads();
+
+  if (w.wave == 0) {
+    float first[V], carry[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) first[v] = p.h0 != nullptr && w.place == 0 ? p.h0[w.b * p.dim + w.ch + v] : 0.0f;
+    if (a.chain.status == nullptr) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) carry[v] = first[v];
+    } else {
+      bool cut = starts != 0;
+      for (int i = 1; i < W; ++i) {
+        const bool c = lds_cut[i] != 0;
+        cut |= c;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const float ai = lds_a[i][lane * V + v], hi = lds_h[i][lane * V + v];
+          hh[v] = c ? hi : __builtin_fmaf(ai, hh[v], hi);
+          ha[v] *= ai;
+        }
+      }
+      chain_carry<V>(a.chain, w.place, w.stream, w.place + 1 == a.pieces, cut, ha, hh, first, carry);
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) lds_carry[lane * V + v] = carry[v];
+  }
+  __syncthreads();
+
+  if (w.n == 0) return;
+  float q[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) q[v] = lds_carry[lane * V + v];
+  for (int i = 0; i < w.wave; ++i) {
+    const bool c = lds_cut[i] != 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const float hi = lds_h[i][lane * V + v];
+      q[v] = c ? hi : __builtin_fmaf(lds_a[i][lane * V + v], q[v], hi);
+    }
+  }
+  if (!w.ok) return;
+  if (p.states != nullptr && w.t0 % kRecurrenceChunk == 0) {
+    const int64_t chunks = (p.seqlen + kRecurrenceChunk - 1) / kRecurrenceChunk;
+#pragma unroll
+    for (int v = 0; v < V; ++v) p.states[(w.b * chunks + w.t0 / kRecurrenceChunk) * p.dim + w.ch + v] = q[v];
+  }
+#pragma unroll
+  for (int j = 0; j < T; ++j) {
+    if (j >= w.n) break;
+    const bool start = starts >> j & 1;
+    float o[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      q[v] = start ? 0.0f : __builtin_fmaf(-m[j][v], q[v], q[v]);
+      o[v] = hl[j][v] + q[v];
+    }
+    store_at<BF16, V>(row_at<BF16>(p.y, row0 + j, p.y_stride), w.ch, o);
+    if (p.h_last != nullptr && w.t0 + j == p.seqlen - 1)
+#pragma unroll
+      for (int v = 0; v < V; ++v) p.h_last[w.b * p.dim + w.ch + v] = o[v];
+  }
+}
+
+// ------------------------------------------------------------ backward
+struct BwdArgs {
+  RecurrenceBwdParams p;
+  Chain chain;
+  float* part;     // [batch][pieces][dim]
+  int blocks;
+  int64_t pieces;
+};
+
+// Below, beta = sqrt(2 m) and s / beta = sqrt(m / 2) add nothing to what they meet
+// (the reciprocal root takes such an m for 0).
+constexpr float kLeastNormal = 1.1754944e-38f;
+
+// One piece is one chunk: W T = kRecurrenceChunk.
+template <bool BF16, int V, int W, int T>
+__global__ void __launch_bounds__(W * 64) recurrence_bwd_kernel(BwdArgs a) {
+  static_assert(W * T == kRecurrenceChunk, "");
+  __shared__ float lds_a[W][64 * V], lds_h[W][64 * V], lds_e[W][64 * V], lds_carry[64 * V];
+  __shared__ int lds_cut[W], lds_id;
+  const RecurrenceBwdParams& p = a.p;
+  int64_t id = blockIdx.x;
+  if (a.chain.status != nullptr) {
+    if (threadIdx.x == 0) lds_id = atomicAdd(a.chain.ticket, 1);
+    __syncthreads();
+    id = __builtin_amdgcn_readfirstlane(lds_id);
+  } else if (id == 0 && threadIdx.x == 0) {
+    *static_cast<int*>(p.workspace) = 0;  // the status word: nothing waits
+  }
+  const auto w = wave_place<V, W, T>(id, a.chain.streams, a.blocks, a.pieces, true, p.seqlen, p.dim);
+  const int lane = threadIdx.x & 63;
+  const int64_t row0 = w.b * p.seqlen + w.t0, piece = a.pieces - 1 - w.place;
+
+  uint32_t rx[T], ra[T], ri[T], rd[T];
+  if (w.n > 0) {
+#pragma unroll
+    for (int j = 0; j < T; ++j) {
+      const int64_t row = row0 + (j < w.n ? j : w.n - 1);
+      ra[j] = load_raw_at<BF16, V>(row_at<BF16>(p.gate_a, row, p.gate_a_stride), w.ch);
+      ri[j] = load_raw_at<BF16, V>(row_at<BF16>(p.gate_x, row, p.gate_x_stride), w.ch);
+      rx[j] = load_raw_at<BF16, V>(row_at<BF16>(p.x, row, p.x_stride), w.ch);
+      rd[j] = load_raw_at<BF16, V>(row_at<BF16>(p.dy, row, p.dy_stride), w.ch);
+    }
+  }
+  const uint64_t starts = w.n > 0 ? start_bits<T>(p.starts, row0, w.n) : 0;
+  float k[V], sp[V], before[V];  // before: the state entering the piece, then this wave's steps
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    sp[v] = softplus_of(p.lam[w.ch + v]);
+    k[v] = p.c * sp[v];
+    before[v] = p.states[(w.b * a.pieces + piece) * p.dim + w.ch + v];
+  }
+
+  // From a zero state forwards (hl), from a zero gradient backwards (e).
+  float m[T][V], hl[T][V], ha[V], hh[V], e[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) ha[v] = 1.0f, hh[v] = 0.0f, e[v] = 0.0f;
+  if (w.n > 0) {
+#pragma unroll
+    for (int j = 0; j < T; ++j) {
+      const bool live = j < w.n, start = starts >> j & 1;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float mj = one_minus_exp<false>(k[v] * sigmoid_of<!BF16>(widen_at<BF16, V>(ra[j], v)));
+        const float in = __builtin_amdgcn_sqrtf(mj * (2.0f - mj)) * sigmoid_of<!BF16>(widen_at<BF16, V>(ri[j], v)) *
+                         widen_at<BF16, V>(rx[j], v);
+        m[j][v] = mj;
+        const float h = (start ? 0.0f : __builtin_fmaf(-mj, hh[v], hh[v])) + in;
+        hh[v] = live ? h : hh[v];
+        ha[v] = live ? __builtin_fmaf(-mj, ha[v], ha[v]) : ha[v];
+        hl[j][v] = hh[v];
+      }
+    }
+#pragma unroll
+    for (int j = T - 1; j >= 0; --j) {
+      const bool live = j < w.n, start = starts >> j & 1;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float g = widen_at<BF16, V>(rd[j], v) + e[v];
+        const float f = start ? 0.0f : __builtin_fmaf(-m[j][v], g, g);
+        e[v] = live ? f : e[v];
+      }
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    lds_a[w.wave][lane * V + v] = ha[v];
+    lds_h[w.wave][lane * V + v] = hh[v];
+    lds_e[w.wave][lane * V + v] = e[v];
+  }
+  if (lane == 0) lds_cut[w.wave] = starts != 0;
+  __syncthreads();
+
+  if (w.wave == 0) {
+    float first[V], carry[V], ea[V], ee[V];
+    bool cut = false;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      first[v] = p.dh_last != nullptr && w.place == 0 ? p.dh_last[w.b * p.dim + w.ch + v] : 0.0f;
+      ea[v] = 1.0f, ee[v] = 0.0f;
+    }
+    if (a.chain.status == nullptr) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) carry[v] = first[v];
+    } else {
+      for (int i = W - 1; i >= 0; --i) {
+        const bool c = lds_cut[i] != 0;
+        cut |= c;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const float ai = lds_a[i][lane * V + v], ei = lds_e[i][lane * V + v];
+          ee[v] = c ? ei : __builtin_fmaf(ai, ee[v], ei);
+          ea[v] *= ai;
+        }
+      }
+      chain_carry<V>(a.chain, w.place, w.stream, w.place + 1 == a.pieces, cut, ea, ee, first, carry);
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) lds_carry[lane * V + v] = carry[v];
+  }
+  // The states before each step, from the one that enters the piece.
+  for (int i = 0; i < w.wave; ++i) {
+    const bool c = lds_cut[i] != 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const float hi = lds_h[i][lane * V + v];
+      before[v] = c ? hi : __builtin_fmaf(lds_a[i][lane * V + v], before[v], hi);
+    }
+  }
+  float q[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) q[v] = before[v];
+#pragma unroll
+  for (int j = 0; j < T; ++j) {
+    const bool start = starts >> j & 1;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      q[v] = start ? 0.0f : __builtin_fmaf(-m[j][v], q[v], q[v]);
+      hl[j][v] += q[v];
+    }
+  }
+  __syncthreads();
+
+#pragma unroll
+  for (int v = 0; v < V; ++v) e[v] = lds_carry[lane * V + v];
+  for (int i = W - 1; i > w.wave; --i) {
+    const bool c = lds_cut[i] != 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const float ei = lds_e[i][lane * V + v];
+      e[v] = c ? ei : __builtin_fmaf(lds_a[i][lane * V + v], e[v], ei);
+    }
+  }
+  float dlam[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) dlam[v] = 0.0f;
+#pragma unroll
+  for (int j = T - 1; j >= 0; --j) {
+    if (j >= w.n) continue;
+    const bool start = starts >> j & 1;
+    float ox[V], oa[V], oi[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      float rr, rest;
+      const float r = sigmoid_of<!BF16>(widen_at<BF16, V>(ra[j], v), rr);
+      const float i = sigmoid_of<!BF16>(widen_at<BF16, V>(ri[j], v), rest);
+      const float s = finite_decay(k[v] * r), mj = m[j][v], dec = 1.0f - mj, beta2 = mj * (2.0f - mj);
+      const float inv = __builtin_amdgcn_rsqf(beta2), beta = mj >= kLeastNormal ? beta2 * inv : mj;
+      const float g = widen_at<BF16, V>(rd[j], v) + e[v];
+      const float gi = g * i, gix = gi * widen_at<BF16, V>(rx[j], v);
+      const float from_beta = dec * dec * (mj >= kLeastNormal ? s * inv : mj) * gix;
+      const float prev = j > 0 ? hl[j > 0 ? j - 1 : 0][v] : before[v];
+      const float big = from_beta - (start ? 0.0f : s * dec * (g * prev));
+      ox[v] = gi * beta;
+      oi[v] = gix * beta * rest;
+      oa[v] = big * rr;
+      dlam[v] += big;
+      e[v] = start ? 0.0f : __builtin_fmaf(-mj, g, g);
+    }
+    if (w.ok) {
+      store_at<BF16, V>(row_at<BF16>(p.dx, row0 + j, p.dx_stride), w.ch, ox);
+      store_at<BF16, V>(row_at<BF16>(p.dgate_a, row0 + j, p.dgate_a_stride), w.ch, oa);
+      store_at<BF16, V>(row_at<BF16>(p.dgate_x, row0 + j, p.dgate_x_stride), w.ch, oi);
+    }
+  }
+  if (w.wave == 0 && piece == 0 && p.dh0 != nullptr && w.ok)
+#pragma unroll
+    for (int v = 0; v < V; ++v) p.dh0[w.b * p.dim + w.ch + v] = e[v];
+  __syncthreads();  // lds_h has been read
+#pragma unroll
+  for (int v = 0; v < V; ++v) lds_h[w.wave][lane * V + v] = dlam[v];
+  __syncthreads();
+  if (w.wave == 0 && w.ok) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      float sum = 0.0f;
+      for (int i = 0; i < W; ++i) sum += lds_h[i][lane * V + v];
+      a.part[(w.b * a.pieces + piece) * p.dim + w.ch + v] = sum * softplus_rate(p.lam[w.ch + v], sp[v]);
+    }
+  }
+}
+
+// ------------------------------------------------------------ launch
+constexpr int kWaves = 8;
+constexpr int kFwdSteps = 16, kBwdSteps = kRecurrenceChunk / kWaves;  // of a wave
+
+struct Cut {
+  int64_t blocks, pieces, streams, ints;
+  size_t own, end, bytes;  // offsets in the workspace
+};
+Cut cut_of(int64_t batch, int64_t seqlen, int64_t dim, int v, int steps) {
+  Cut c;
+  c.blocks = (dim + 64 * v - 1) / (64 * v);
+  c.streams = batch * c.blocks;
+  c.pieces = (seqlen + steps - 1) / steps;
+  const int64_t n = c.pieces > 1 ? c.streams * c.pieces : 0;
+  c.ints = kChainHeader + n;
+  c.own = ((size_t)c.ints * 4 + 255) / 256 * 256;
+  c.end = c.own + (size_t)n * (128 * v) * 4;
+  c.bytes = c.end + (size_t)n * (64 * v) * 4;
+  return c;
+}
+
+hipError_t start_chain(const Cut& c, void* workspace, Chain& chain, hipStream_t stream) {
+  int* ints = static_cast<int*>(workspace);
+  char* base = static_cast<char*>(workspace);
+  chain.streams = (int)c.streams;
+  chain.status = nullptr;
+  if (c.pieces == 1) return hipSuccess;
+  chain.status = ints;
+  chain.ticket = ints + 1;
+  chain.flags = ints + kChainHeader;
+  chain.own = reinterpret_cast<float*>(base + c.own);
+  chain.end = reinterpret_cast<float*>(base + c.end);
+  const int64_t groups = (c.ints + 255) / 256;
+  hipLaunchKernelGGL(chain_clear_kernel, dim3((unsigned)(groups < 1024 ? groups : 1024)), dim3(256), 0, stream, ints,
+                     c.ints);
   return hipGetLastError();
 }
 
-size_t recurrence_bwd_workspace_bytes(int64_t batch, int64_t, int64_t dim, bool) {
-  return 256 + (size_t)batch * dim * sizeof(float);
+// Two bf16 channels a lane need rows of whole words.
+bool pairs(const void* p, int64_t stride) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0 && stride % 2 == 0; }
+
+template <bool BF16, int V>
+hipError_t launch_fwd(const RecurrenceFwdParams& p, hipStream_t stream) {
+  const Cut c = cut_of(p.batch, p.seqlen, p.dim, V, kWaves * kFwdSteps);
+  FwdArgs a{p, {}, (int)c.blocks, c.pieces};
+  const hipError_t e = start_chain(c, p.workspace, a.chain, stream);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((recurrence_fwd_kernel<BF16, V, kWaves, kFwdSteps>), dim3((unsigned)(c.streams * c.pieces)),
+                     dim3(kWaves * 64), 0, stream, a);
+  return hipGetLastError();
+}
+
+size_t bwd_part_offset(const Cut& c) { return (c.bytes + 255) / 256 * 256; }
+
+template <bool BF16, int V>
+hipError_t launch_bwd(const RecurrenceBwdParams& p, hipStream_t stream) {
+  const Cut c = cut_of(p.batch, p.seqlen, p.dim, V, kRecurrenceChunk);
+  BwdArgs a{p, {}, reinterpret_cast<float*>(static_cast<char*>(p.workspace) + bwd_part_offset(c)), (int)c.blocks,
+            c.pieces};
+  hipError_t e = start_chain(c, p.workspace, a.chain, stream);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((recurrence_bwd_kernel<BF16, V, kWaves, kBwdSteps>), dim3((unsigned)(c.streams * c.pieces)),
+                     dim3(kWaves * 64), 0, stream, a);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  SumPartialsArgs s{};
+  s.part = a.part;
+  s.dweight = p.dlam;
+  s.nparts = p.batch * c.pieces;
+  s.cols = p.dim;
+  s.nout = 1;
+  return launch_sum_partials(s, stream);
+}
+
+}  // namespace
+
+// Whether channels go in pairs depends on the call's addresses: room for either.
+size_t recurrence_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, bool bf16) {
+  const size_t one = cut_of(batch, seqlen, dim, 1, kWaves * kFwdSteps).bytes;
+  const size_t two = bf16 ? cut_of(batch, seqlen, dim, 2, kWaves * kFwdSteps).bytes : 0;
+  return one > two ? one : two;
+}
+
+hipError_t launch_recurrence_fwd(const RecurrenceFwdParams& p, hipStream_t stream) {
+  if (!p.bf16) return launch_fwd<false, 1>(p, stream);
+  const bool two = p.dim % 2 == 0 && pairs(p.x, p.x_stride) && pairs(p.gate_a, p.gate_a_stride) &&
+                   pairs(p.gate_x, p.gate_x_stride) && pairs(p.y, p.y_stride);
+  return two ? launch_fwd<true, 2>(p, stream) : launch_fwd<true, 1>(p, stream);
+}
+
+size_t recurrence_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, bool bf16) {
+  const Cut one = cut_of(batch, seqlen, dim, 1, kRecurrenceChunk), two = cut_of(batch, seqlen, dim, 2, kRecurrenceChunk);
+  const size_t a = bwd_part_offset(one), b = bf16 ? bwd_part_offset(two) : 0;
+  return (a > b ? a : b) + (size_t)(batch * one.pieces * dim) * sizeof(float);
 }
 
 hipError_t launch_recurrence_bwd(const RecurrenceBwdParams& p, hipStream_t stream) {
-  float* part = reinterpret_cast<float*>(static_cast<char*>(p.workspace) + 256);
-  if (p.bf16) hipLaunchKernelGGL(recurrence_bwd_kernel<true>, grid_of(p.batch, p.dim), dim3(64), 0, stream, p, part);
-  else hipLaunchKernelGGL(recurrence_bwd_kernel<false>, grid_of(p.batch, p.dim), dim3(64), 0, stream, p, part);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  SumPartialsArgs a{};
-  a.part = part;
-  a.dweight = p.dlam;
-  a.nparts = p.batch;
-  a.cols = p.dim;
-  a.nout = 1;
-  return launch_sum_partials(a, stream);
+  if (!p.bf16) return launch_bwd<false, 1>(p, stream);
+  const bool two = p.dim % 2 == 0 && pairs(p.dy, p.dy_stride) && pairs(p.x, p.x_stride) &&
+                   pairs(p.gate_a, p.gate_a_stride) && pairs(p.gate_x, p.gate_x_stride) && pairs(p.dx, p.dx_stride) &&
+                   pairs(p.dgate_a, p.dgate_a_stride) && pairs(p.dgate_x, p.dgate_x_stride);
+  return two ? launch_bwd<true, 2>(p, stream) : launch_bwd<true, 1>(p, stream);
 }
 
 }  // namespace mss
