@@ -159,13 +159,18 @@ __device__ __forceinline__ void store_at(void* row, uint32_t ch, const float (&o
   else if constexpr (BF16) *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(row) + ch) = pack_bf16x2(o[0], o[1]);
   else static_cast<float*>(row)[ch] = o[0];
 }
-template <bool BF16>
-__device__ __forceinline__ const void* row_at(const void* p, int64_t row, int64_t stride) {
-  return static_cast<const char*>(p) + row * stride * (BF16 ? 2 : 4);
-}
-template <bool BF16>
-__device__ __forceinline__ void* row_at(void* p, int64_t row, int64_t stride) {
-  return static_cast<char*>(p) + row * stride * (BF16 ? 2 : 4);
+// Rows r0, r0 + 1, .. of a tensor, a wave's lanes at channel ch; past the last of n
+// rows the last is repeated.  WHOLE: there are T.
+template <bool BF16, int V, int T, bool WHOLE>
+__device__ __forceinline__ void load_rows(const void* p, int64_t r0, int64_t stride, uint32_t ch, int n,
+                                          uint32_t (&raw)[T]) {
+  const char* row = static_cast<const char*>(p) + r0 * stride * (BF16 ? 2 : 4);
+  const int64_t step = stride * (BF16 ? 2 : 4);
+#pragma unroll
+  for (int j = 0; j < T; ++j) {
+    raw[j] = load_raw_at<BF16, V>(row, ch);
+    if (WHOLE || j + 1 < n) row += step;
+  }
 }
 
 // Where a wave works: which piece, its steps, its lane's channels.
@@ -231,39 +236,49 @@ __global__ void __launch_bounds__(W * 64) recurrence_fwd_kernel(FwdArgs a) {
   const int64_t row0 = w.b * p.seqlen + w.t0;
 
   uint32_t rx[T], ra[T], ri[T];
-  if (w.n > 0) {
-#pragma unroll
-    for (int j = 0; j < T; ++j) {
-      const int64_t row = row0 + (j < w.n ? j : w.n - 1);
-      ra[j] = load_raw_at<BF16, V>(row_at<BF16>(p.gate_a, row, p.gate_a_stride), w.ch);
-      ri[j] = load_raw_at<BF16, V>(row_at<BF16>(p.gate_x, row, p.gate_x_stride), w.ch);
-      rx[j] = load_raw_at<BF16, V>(row_at<BF16>(p.x, row, p.x_stride), w.ch);
-    }
-  }
+  const auto load = [&](auto whole) {
+    load_rows<BF16, V, T, whole()>(p.gate_a, row0, p.gate_a_stride, w.ch, w.n, ra);
+    load_rows<BF16, V, T, whole()>(p.gate_x, row0, p.gate_x_stride, w.ch, w.n, ri);
+    load_rows<BF16, V, T, whole()>(p.x, row0, p.x_stride, w.ch, w.n, rx);
+  };
+  if (w.n == T) load(std::true_type{});
+  else if (w.n > 0) load(std::false_type{});
   const uint64_t starts = w.n > 0 ? start_bits<T>(p.starts, row0, w.n) : 0;
+  const bool plain = w.n == T && starts == 0;
   float k[V];
+  bool low = true;
 #pragma unroll
-  for (int v = 0; v < V; ++v) k[v] = p.c * softplus_of(p.lam[w.ch + v]);
+  for (int v = 0; v < V; ++v) {
+    k[v] = p.c * softplus_of(p.lam[w.ch + v]);
+    low = low && k[v] <= kPolySmall;
+  }
 
-  float m[T][V], hl[T][V], ha[V], hh[V];
+  // From a zero state: after each step the state and the product of the decays.
+  float pr[T][V], hl[T][V], ha[V], hh[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) ha[v] = 1.0f, hh[v] = 0.0f;
-  if (w.n > 0) {
+  const auto local = [&](auto whole, auto small) {
 #pragma unroll
     for (int j = 0; j < T; ++j) {
-      const bool live = j < w.n, start = starts >> j & 1;
+      if (!whole() && j >= w.n) break;
+      const bool start = !whole() && (starts >> j & 1);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const float mj = one_minus_exp<false>(k[v] * sigmoid_of<!BF16>(widen_at<BF16, V>(ra[j], v)));
+        const float mj = one_minus_exp<small()>(k[v] * sigmoid_of<!BF16>(widen_at<BF16, V>(ra[j], v)));
         const float in = __builtin_amdgcn_sqrtf(mj * (2.0f - mj)) * sigmoid_of<!BF16>(widen_at<BF16, V>(ri[j], v)) *
                          widen_at<BF16, V>(rx[j], v);
-        m[j][v] = mj;
-        const float h = (start ? 0.0f : __builtin_fmaf(-mj, hh[v], hh[v])) + in;
-        hh[v] = live ? h : hh[v];
-        ha[v] = live ? __builtin_fmaf(-mj, ha[v], ha[v]) : ha[v];
+        hh[v] = (start ? 0.0f : __builtin_fmaf(-mj, hh[v], hh[v])) + in;
+        ha[v] = __builtin_fmaf(-mj, ha[v], ha[v]);
         hl[j][v] = hh[v];
+        pr[j][v] = ha[v];
       }
     }
+  };
+  if (plain) {
+    if (__all(low)) local(std::true_type{}, std::true_type{});
+    else local(std::true_type{}, std::false_type{});
+  } else if (w.n > 0) {
+    local(std::false_type{}, std::false_type{});
   }
 #pragma unroll
   for (int v = 0; v < V; ++v) lds_a[w.wave][lane * V + v] = ha[v], lds_h[w.wave][lane * V + v] = hh[v];
@@ -314,21 +329,24 @@ __global__ void __launch_bounds__(W * 64) recurrence_fwd_kernel(FwdArgs a) {
 #pragma unroll
     for (int v = 0; v < V; ++v) p.states[(w.b * chunks + w.t0 / kRecurrenceChunk) * p.dim + w.ch + v] = q[v];
   }
+  char* y = static_cast<char*>(p.y) + row0 * p.y_stride * (BF16 ? 2 : 4);
+  const auto apply = [&](auto whole) {
 #pragma unroll
-  for (int j = 0; j < T; ++j) {
-    if (j >= w.n) break;
-    const bool start = starts >> j & 1;
-    float o[V];
+    for (int j = 0; j < T; ++j) {
+      if (!whole() && j >= w.n) break;
+      const bool cut = !whole() && (starts & ((2ull << j) - 1)) != 0;
+      float o[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      q[v] = start ? 0.0f : __builtin_fmaf(-m[j][v], q[v], q[v]);
-      o[v] = hl[j][v] + q[v];
+      for (int v = 0; v < V; ++v) o[v] = cut ? hl[j][v] : __builtin_fmaf(pr[j][v], q[v], hl[j][v]);
+      store_at<BF16, V>(y, w.ch, o);
+      y += p.y_stride * (BF16 ? 2 : 4);
+      if (p.h_last != nullptr && w.t0 + j == p.seqlen - 1)
+#pragma unroll
+        for (int v = 0; v < V; ++v) p.h_last[w.b * p.dim + w.ch + v] = o[v];
     }
-    store_at<BF16, V>(row_at<BF16>(p.y, row0 + j, p.y_stride), w.ch, o);
-    if (p.h_last != nullptr && w.t0 + j == p.seqlen - 1)
-#pragma unroll
-      for (int v = 0; v < V; ++v) p.h_last[w.b * p.dim + w.ch + v] = o[v];
-  }
+  };
+  if (plain) apply(std::true_type{});
+  else apply(std::false_type{});
 }
 
 // ------------------------------------------------------------ backward
@@ -364,22 +382,23 @@ __global__ void __launch_bounds__(W * 64) recurrence_bwd_kernel(BwdArgs a) {
   const int64_t row0 = w.b * p.seqlen + w.t0, piece = a.pieces - 1 - w.place;
 
   uint32_t rx[T], ra[T], ri[T], rd[T];
-  if (w.n > 0) {
-#pragma unroll
-    for (int j = 0; j < T; ++j) {
-      const int64_t row = row0 + (j < w.n ? j : w.n - 1);
-      ra[j] = load_raw_at<BF16, V>(row_at<BF16>(p.gate_a, row, p.gate_a_stride), w.ch);
-      ri[j] = load_raw_at<BF16, V>(row_at<BF16>(p.gate_x, row, p.gate_x_stride), w.ch);
-      rx[j] = load_raw_at<BF16, V>(row_at<BF16>(p.x, row, p.x_stride), w.ch);
-      rd[j] = load_raw_at<BF16, V>(row_at<BF16>(p.dy, row, p.dy_stride), w.ch);
-    }
-  }
+  const auto load = [&](auto whole) {
+    load_rows<BF16, V, T, whole()>(p.gate_a, row0, p.gate_a_stride, w.ch, w.n, ra);
+    load_rows<BF16, V, T, whole()>(p.gate_x, row0, p.gate_x_stride, w.ch, w.n, ri);
+    load_rows<BF16, V, T, whole()>(p.x, row0, p.x_stride, w.ch, w.n, rx);
+    load_rows<BF16, V, T, whole()>(p.dy, row0, p.dy_stride, w.ch, w.n, rd);
+  };
+  if (w.n == T) load(std::true_type{});
+  else if (w.n > 0) load(std::false_type{});
   const uint64_t starts = w.n > 0 ? start_bits<T>(p.starts, row0, w.n) : 0;
+  const bool plain = w.n == T && starts == 0;
   float k[V], sp[V], before[V];  // before: the state entering the piece, then this wave's steps
+  bool low = true;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     sp[v] = softplus_of(p.lam[w.ch + v]);
     k[v] = p.c * sp[v];
+    low = low && k[v] <= kPolySmall;
     before[v] = p.states[(w.b * a.pieces + piece) * p.dim + w.ch + v];
   }
 
@@ -387,32 +406,38 @@ __global__ void __launch_bounds__(W * 64) recurrence_bwd_kernel(BwdArgs a) {
   float m[T][V], hl[T][V], ha[V], hh[V], e[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) ha[v] = 1.0f, hh[v] = 0.0f, e[v] = 0.0f;
-  if (w.n > 0) {
+  const auto local = [&](auto whole, auto small) {
 #pragma unroll
     for (int j = 0; j < T; ++j) {
-      const bool live = j < w.n, start = starts >> j & 1;
+      if (!whole() && j >= w.n) break;
+      const bool start = !whole() && (starts >> j & 1);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const float mj = one_minus_exp<false>(k[v] * sigmoid_of<!BF16>(widen_at<BF16, V>(ra[j], v)));
+        const float mj = one_minus_exp<small()>(k[v] * sigmoid_of<!BF16>(widen_at<BF16, V>(ra[j], v)));
         const float in = __builtin_amdgcn_sqrtf(mj * (2.0f - mj)) * sigmoid_of<!BF16>(widen_at<BF16, V>(ri[j], v)) *
                          widen_at<BF16, V>(rx[j], v);
         m[j][v] = mj;
-        const float h = (start ? 0.0f : __builtin_fmaf(-mj, hh[v], hh[v])) + in;
-        hh[v] = live ? h : hh[v];
-        ha[v] = live ? __builtin_fmaf(-mj, ha[v], ha[v]) : ha[v];
+        hh[v] = (start ? 0.0f : __builtin_fmaf(-mj, hh[v], hh[v])) + in;
+        ha[v] = __builtin_fmaf(-mj, ha[v], ha[v]);
         hl[j][v] = hh[v];
       }
     }
 #pragma unroll
     for (int j = T - 1; j >= 0; --j) {
-      const bool live = j < w.n, start = starts >> j & 1;
+      if (!whole() && j >= w.n) continue;
+      const bool start = !whole() && (starts >> j & 1);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const float g = widen_at<BF16, V>(rd[j], v) + e[v];
-        const float f = start ? 0.0f : __builtin_fmaf(-m[j][v], g, g);
-        e[v] = live ? f : e[v];
+        e[v] = start ? 0.0f : __builtin_fmaf(-m[j][v], g, g);
       }
     }
+  };
+  if (plain) {
+    if (__all(low)) local(std::true_type{}, std::true_type{});
+    else local(std::true_type{}, std::false_type{});
+  } else if (w.n > 0) {
+    local(std::false_type{}, std::false_type{});
   }
 #pragma unroll
   for (int v = 0; v < V; ++v) {
@@ -459,18 +484,23 @@ __global__ void __launch_bounds__(W * 64) recurrence_bwd_kernel(BwdArgs a) {
       before[v] = c ? hi : __builtin_fmaf(lds_a[i][lane * V + v], before[v], hi);
     }
   }
-  float q[V];
+  const auto enter = [&](auto whole) {
+    float q[V];
 #pragma unroll
-  for (int v = 0; v < V; ++v) q[v] = before[v];
+    for (int v = 0; v < V; ++v) q[v] = before[v];
 #pragma unroll
-  for (int j = 0; j < T; ++j) {
-    const bool start = starts >> j & 1;
+    for (int j = 0; j < T; ++j) {
+      if (!whole() && j >= w.n) break;
+      const bool start = !whole() && (starts >> j & 1);
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      q[v] = start ? 0.0f : __builtin_fmaf(-m[j][v], q[v], q[v]);
-      hl[j][v] += q[v];
+      for (int v = 0; v < V; ++v) {
+        q[v] = start ? 0.0f : __builtin_fmaf(-m[j][v], q[v], q[v]);
+        hl[j][v] += q[v];
+      }
     }
-  }
+  };
+  if (plain) enter(std::true_type{});
+  else if (w.n > 0) enter(std::false_type{});
   __syncthreads();
 
 #pragma unroll
@@ -486,35 +516,44 @@ __global__ void __launch_bounds__(W * 64) recurrence_bwd_kernel(BwdArgs a) {
   float dlam[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) dlam[v] = 0.0f;
+  const int64_t es = BF16 ? 2 : 4;
+  char* dx = static_cast<char*>(p.dx) + (row0 + w.n) * p.dx_stride * es;
+  char* da = static_cast<char*>(p.dgate_a) + (row0 + w.n) * p.dgate_a_stride * es;
+  char* di = static_cast<char*>(p.dgate_x) + (row0 + w.n) * p.dgate_x_stride * es;
+  const auto grads = [&](auto whole) {
 #pragma unroll
-  for (int j = T - 1; j >= 0; --j) {
-    if (j >= w.n) continue;
-    const bool start = starts >> j & 1;
-    float ox[V], oa[V], oi[V];
+    for (int j = T - 1; j >= 0; --j) {
+      if (!whole() && j >= w.n) continue;
+      const bool start = !whole() && (starts >> j & 1);
+      float ox[V], oa[V], oi[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      float rr, rest;
-      const float r = sigmoid_of<!BF16>(widen_at<BF16, V>(ra[j], v), rr);
-      const float i = sigmoid_of<!BF16>(widen_at<BF16, V>(ri[j], v), rest);
-      const float s = finite_decay(k[v] * r), mj = m[j][v], dec = 1.0f - mj, beta2 = mj * (2.0f - mj);
-      const float inv = __builtin_amdgcn_rsqf(beta2), beta = mj >= kLeastNormal ? beta2 * inv : mj;
-      const float g = widen_at<BF16, V>(rd[j], v) + e[v];
-      const float gi = g * i, gix = gi * widen_at<BF16, V>(rx[j], v);
-      const float from_beta = dec * dec * (mj >= kLeastNormal ? s * inv : mj) * gix;
-      const float prev = j > 0 ? hl[j > 0 ? j - 1 : 0][v] : before[v];
-      const float big = from_beta - (start ? 0.0f : s * dec * (g * prev));
-      ox[v] = gi * beta;
-      oi[v] = gix * beta * rest;
-      oa[v] = big * rr;
-      dlam[v] += big;
-      e[v] = start ? 0.0f : __builtin_fmaf(-mj, g, g);
+      for (int v = 0; v < V; ++v) {
+        float rr, rest;
+        const float r = sigmoid_of<!BF16>(widen_at<BF16, V>(ra[j], v), rr);
+        const float i = sigmoid_of<!BF16>(widen_at<BF16, V>(ri[j], v), rest);
+        const float s = finite_decay(k[v] * r), mj = m[j][v], dec = 1.0f - mj, beta2 = mj * (2.0f - mj);
+        const float inv = __builtin_amdgcn_rsqf(beta2), beta = mj >= kLeastNormal ? beta2 * inv : mj;
+        const float g = widen_at<BF16, V>(rd[j], v) + e[v];
+        const float gi = g * i, gix = gi * widen_at<BF16, V>(rx[j], v);
+        const float from_beta = dec * dec * (mj >= kLeastNormal ? s * inv : mj) * gix;
+        const float prev = j > 0 ? hl[j > 0 ? j - 1 : 0][v] : before[v];
+        const float big = from_beta - (start ? 0.0f : s * dec * (g * prev));
+        ox[v] = gi * beta;
+        oi[v] = gix * beta * rest;
+        oa[v] = big * rr;
+        dlam[v] += big;
+        e[v] = start ? 0.0f : __builtin_fmaf(-mj, g, g);
+      }
+      dx -= p.dx_stride * es, da -= p.dgate_a_stride * es, di -= p.dgate_x_stride * es;
+      if (w.ok) {
+        store_at<BF16, V>(dx, w.ch, ox);
+        store_at<BF16, V>(da, w.ch, oa);
+        store_at<BF16, V>(di, w.ch, oi);
+      }
     }
-    if (w.ok) {
-      store_at<BF16, V>(row_at<BF16>(p.dx, row0 + j, p.dx_stride), w.ch, ox);
-      store_at<BF16, V>(row_at<BF16>(p.dgate_a, row0 + j, p.dgate_a_stride), w.ch, oa);
-      store_at<BF16, V>(row_at<BF16>(p.dgate_x, row0 + j, p.dgate_x_stride), w.ch, oi);
-    }
-  }
+  };
+  if (plain) grads(std::true_type{});
+  else if (w.n > 0) grads(std::false_type{});
   if (w.wave == 0 && piece == 0 && p.dh0 != nullptr && w.ok)
 #pragma unroll
     for (int v = 0; v < V; ++v) p.dh0[w.b * p.dim + w.ch + v] = e[v];
