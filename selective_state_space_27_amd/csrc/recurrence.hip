@@ -23,54 +23,108 @@ namespace {
 // A piece is one workgroup's steps of one stream (64 V channels of a batch row).
 // Pieces take their place in order of start (a ticket): s-th in its stream, all
 // streams' s-th before any (s+1)-th.  A piece that has its own A and H publishes
-// them (kOwn), looks back for the nearest piece whose end state is known (kEnd),
-// folds what lies between from there on, and publishes its own end state.  The
-// fold is the same sequence of operations wherever it begins, so results do not
-// depend on timing.  What is waited for belongs to pieces that have started and
-// that publish it before they wait themselves.
+// them, looks back for the nearest piece whose end state is known, folds what
+// lies between from there on, and publishes its own end state.  The fold is the
+// same sequence of operations wherever it begins, so results do not depend on
+// timing.  What is waited for belongs to pieces that have started and that
+// publish it before they wait themselves.
 //
-// Values and flags move through relaxed agent-scope atomics, coherent across the
-// dies: the values are stored and waited for before the flag is set, and loaded
-// after the flag has been seen.
-enum : int { kOwn = 1, kEnd = 2 };
-constexpr int kMaxSpinsChain = 1 << 22;
-constexpr int kChainHeader = 64;  // ints before the flags: status word, ticket
+// Values move through relaxed agent-scope atomics, coherent across the dies.  A
+// word that is all ones has not been written: the buffers are filled with that
+// before, and a NaN of those bits is replaced by another.  So one load tells
+// whether a value is there and what it is; flags beside the values took a wait
+// for the stores, one load more for each look and two more for each hand-over.
+constexpr int kMaxSpinsChain = 1 << 20;
+constexpr uint32_t kUnset = 0xffffffffu;
+constexpr int kChainHeader = 64;  // bytes before the values: status word, ticket
+
+constexpr int kManyStreams = 96;
 
 struct Chain {
-  int* status;   // null: one piece a stream, nothing is handed on
+  int* status;    // null: one piece a stream, nothing is handed on
   int* ticket;
-  int* flags;    // [place][stream]
-  float* own;    // [place][stream][2][64 V]: A, H
-  float* end;    // [place][stream][64 V]
+  uint64_t* own;  // [place][stream][64 V]: A, H
+  float* end;     // [place][stream][64 V]
   int streams;
 };
 
-__global__ void __launch_bounds__(256) chain_clear_kernel(int* p, int64_t n) {
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) p[i] = 0;
+// Status word and ticket to 0, the rest (n times 16 bytes) to unset.
+__global__ void __launch_bounds__(256) chain_clear_kernel(u32x4* p, int64_t n) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    const uint32_t v = i < kChainHeader / 16 ? 0u : kUnset;
+    p[i] = u32x4{v, v, v, v};
+  }
 }
 
+__device__ __forceinline__ uint32_t set_bits(float v) {
+  const uint32_t u = __float_as_uint(v);
+  return u == kUnset ? 0x7fc00000u : u;
+}
 template <int V>
-__device__ __forceinline__ void put(float* p, const float (&v)[V]) {
+__device__ __forceinline__ void put_end(float* p, const float (&h)[V]) {
   if constexpr (V == 2) {
-    const uint64_t w = (uint64_t)__float_as_uint(v[1]) << 32 | __float_as_uint(v[0]);
-    __hip_atomic_store(reinterpret_cast<uint64_t*>(p), w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __hip_atomic_store(reinterpret_cast<uint64_t*>(p), (uint64_t)set_bits(h[1]) << 32 | set_bits(h[0]),
+                       __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   } else {
-    __hip_atomic_store(p, v[0], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __hip_atomic_store(reinterpret_cast<uint32_t*>(p), set_bits(h[0]), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
 }
 template <int V>
-__device__ __forceinline__ void take(const float* p, float (&v)[V]) {
-  if constexpr (V == 2) {
-    const uint64_t w = __hip_atomic_load(reinterpret_cast<const uint64_t*>(p), __ATOMIC_RELAXED,
-                                         __HIP_MEMORY_SCOPE_AGENT);
-    v[0] = __uint_as_float((uint32_t)w), v[1] = __uint_as_float((uint32_t)(w >> 32));
-  } else {
-    v[0] = __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  }
+__device__ __forceinline__ void put_own(uint64_t* p, const float (&a)[V], const float (&h)[V]) {
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+    __hip_atomic_store(p + v, (uint64_t)set_bits(h[v]) << 32 | set_bits(a[v]), __ATOMIC_RELAXED,
+                       __HIP_MEMORY_SCOPE_AGENT);
 }
-__device__ __forceinline__ void set_flag(int* f, int lane, int v) {
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // what the flag stands for has been stored
-  if (lane == 0) __hip_atomic_store(f, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+template <int V>
+__device__ __forceinline__ uint64_t load_end(const float* p) {
+  if constexpr (V == 2)
+    return __hip_atomic_load(reinterpret_cast<const uint64_t*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  else
+    return __hip_atomic_load(reinterpret_cast<const uint32_t*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ bool is_set(uint64_t w) { return (uint32_t)w != kUnset; }
+
+// One look at the last N places before `place`: whether an end state is there and
+// everything after it, and if so what enters the piece.
+template <int V, int N>
+__device__ __forceinline__ bool chain_look(const Chain& c, int place, int stream, float (&carry)[V]) {
+  const int lane = threadIdx.x & 63;
+  uint64_t end[N], own[N][V];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int at = place - 1 - i > 0 ? place - 1 - i : 0;
+    const int64_t off = ((int64_t)at * c.streams + stream) * (64 * V) + lane * V;
+    end[i] = load_end<V>(c.end + off);
+    if (i + 1 < N)
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        own[i][v] = __hip_atomic_load(c.own + off + v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  int near = -1;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if (near >= 0) break;
+    if (__all(is_set(end[i]))) near = i;
+    bool there = i + 1 < N;
+#pragma unroll
+    for (int v = 0; v < V; ++v) there = there && is_set(own[i + 1 < N ? i : 0][v]);
+    if (near < 0 && !__all(there)) return false;
+  }
+  if (near < 0) return false;
+#pragma unroll
+  for (int i = N - 1; i >= 0; --i) {
+    if (i == near) {
+      carry[0] = __uint_as_float((uint32_t)end[i]);
+      if constexpr (V == 2) carry[1] = __uint_as_float((uint32_t)(end[i] >> 32));
+    }
+    if (i < near)
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        carry[v] = __builtin_fmaf(__uint_as_float((uint32_t)own[i][v]), carry[v],
+                                  __uint_as_float((uint32_t)(own[i][v] >> 32)));
+  }
+  return true;
 }
 
 // What enters the piece at `place` of `stream` (wave 0's lanes; `first` at place
@@ -80,64 +134,31 @@ template <int V>
 __device__ __forceinline__ void chain_carry(const Chain& c, int place, int stream, bool last, bool cut,
                                             const float (&own_a)[V], const float (&own_h)[V], const float (&first)[V],
                                             float (&carry)[V]) {
-  const int lane = threadIdx.x & 63;
-  const int64_t id = (int64_t)place * c.streams + stream;
-  float* end = c.end + id * (64 * V) + lane * V;
-  float h[V];
+  const int64_t off = ((int64_t)place * c.streams + stream) * (64 * V) + (threadIdx.x & 63) * V;
+  if (cut && !last) put_end<V>(c.end + off, own_h);
   if (place == 0) {
 #pragma unroll
     for (int v = 0; v < V; ++v) carry[v] = first[v];
   } else {
-    if (!last) {
-      if (cut) {
-        put<V>(end, own_h);
-      } else {
-        float* own = c.own + id * (128 * V) + lane * V;
-        put<V>(own, own_a);
-        put<V>(own + 64 * V, own_h);
-      }
-      set_flag(c.flags + id, lane, cut ? kEnd : kOwn);
-    }
-    // Lane l looks at the piece l + 1 places back.
-    const int back = place - 1 - lane;
-    const int* flag = c.flags + (int64_t)(back > 0 ? back : 0) * c.streams + stream;
-    int near = 0;  // of the nearest known end state
-    for (int spins = 0;; ++spins) {
-      const int f = back >= 0 ? __hip_atomic_load(flag, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0;
-      const uint64_t ends = __ballot(f == kEnd), ready = __ballot(f != 0);
-      near = ends != 0 ? __builtin_ctzll(ends) : 0;
-      if (ends != 0 && (~ready & ((1ull << near) - 1)) == 0) break;
-      if (spins > kMaxSpinsChain) {  // never expected; keeps every wait finite, reported through the status word
-        if (lane == 0) __hip_atomic_store(c.status, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        near = 0;
+    if (!cut && !last) put_own<V>(c.own + off, own_a, own_h);
+    // With many streams the piece before has mostly ended; with few, several of a
+    // stream are under way at once.
+    bool found = c.streams >= kManyStreams && chain_look<V, 1>(c, place, stream, carry);
+    for (int spins = 0; !found; ++spins) {
+      found = chain_look<V, 4>(c, place, stream, carry);
+      if (!found && spins > kMaxSpinsChain) {  // never expected; keeps every wait finite, reported through the status word
+        if ((threadIdx.x & 63) == 0) __hip_atomic_store(c.status, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+        for (int v = 0; v < V; ++v) carry[v] = 0.0f;
         break;
       }
-      __builtin_amdgcn_s_sleep(1);
-    }
-    int64_t at = (int64_t)(place - 1 - near) * c.streams + stream;
-    take<V>(c.end + at * (64 * V) + lane * V, carry);
-    for (int i = near; i > 0; i -= 4) {
-      float a[4][V], b[4][V];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int64_t from = at + (int64_t)(j + 1 <= i ? j + 1 : i) * c.streams;
-        const float* own = c.own + from * (128 * V) + lane * V;
-        take<V>(own, a[j]);
-        take<V>(own + 64 * V, b[j]);
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (j + 1 <= i)
-#pragma unroll
-          for (int v = 0; v < V; ++v) carry[v] = __builtin_fmaf(a[j][v], carry[v], b[j][v]);
-      at += (int64_t)4 * c.streams;
     }
   }
-  if (last || (cut && place != 0)) return;
+  if (cut || last) return;
+  float h[V];
 #pragma unroll
-  for (int v = 0; v < V; ++v) h[v] = cut ? own_h[v] : __builtin_fmaf(own_a[v], carry[v], own_h[v]);
-  put<V>(end, h);
-  set_flag(c.flags + id, lane, kEnd);
+  for (int v = 0; v < V; ++v) h[v] = __builtin_fmaf(own_a[v], carry[v], own_h[v]);
+  put_end<V>(c.end + off, h);
 }
 
 // ------------------------------------------------------------ rows
@@ -576,7 +597,7 @@ constexpr int kWaves = 8;
 constexpr int kFwdSteps = 16, kBwdSteps = kRecurrenceChunk / kWaves;  // of a wave
 
 struct Cut {
-  int64_t blocks, pieces, streams, ints;
+  int64_t blocks, pieces, streams;
   size_t own, end, bytes;  // offsets in the workspace
 };
 Cut cut_of(int64_t batch, int64_t seqlen, int64_t dim, int v, int steps) {
@@ -584,28 +605,25 @@ Cut cut_of(int64_t batch, int64_t seqlen, int64_t dim, int v, int steps) {
   c.blocks = (dim + 64 * v - 1) / (64 * v);
   c.streams = batch * c.blocks;
   c.pieces = (seqlen + steps - 1) / steps;
-  const int64_t n = c.pieces > 1 ? c.streams * c.pieces : 0;
-  c.ints = kChainHeader + n;
-  c.own = ((size_t)c.ints * 4 + 255) / 256 * 256;
-  c.end = c.own + (size_t)n * (128 * v) * 4;
-  c.bytes = c.end + (size_t)n * (64 * v) * 4;
+  const size_t n = c.pieces > 1 ? (size_t)(c.streams * c.pieces) * (64 * v) : 0;
+  c.own = kChainHeader;
+  c.end = c.own + n * sizeof(uint64_t);
+  c.bytes = c.end + n * sizeof(float);
   return c;
 }
 
 hipError_t start_chain(const Cut& c, void* workspace, Chain& chain, hipStream_t stream) {
-  int* ints = static_cast<int*>(workspace);
   char* base = static_cast<char*>(workspace);
   chain.streams = (int)c.streams;
   chain.status = nullptr;
   if (c.pieces == 1) return hipSuccess;
-  chain.status = ints;
-  chain.ticket = ints + 1;
-  chain.flags = ints + kChainHeader;
-  chain.own = reinterpret_cast<float*>(base + c.own);
+  chain.status = reinterpret_cast<int*>(base);
+  chain.ticket = chain.status + 1;
+  chain.own = reinterpret_cast<uint64_t*>(base + c.own);
   chain.end = reinterpret_cast<float*>(base + c.end);
-  const int64_t groups = (c.ints + 255) / 256;
-  hipLaunchKernelGGL(chain_clear_kernel, dim3((unsigned)(groups < 1024 ? groups : 1024)), dim3(256), 0, stream, ints,
-                     c.ints);
+  const int64_t n = (int64_t)(c.bytes / 16), groups = (n + 1023) / 1024;
+  hipLaunchKernelGGL(chain_clear_kernel, dim3((unsigned)(groups < 2048 ? groups : 2048)), dim3(256), 0, stream,
+                     reinterpret_cast<u32x4*>(base), n);
   return hipGetLastError();
 }
 
