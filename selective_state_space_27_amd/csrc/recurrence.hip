@@ -162,36 +162,53 @@ __device__ __forceinline__ void chain_carry(const Chain& c, int place, int strea
 }
 
 // ------------------------------------------------------------ rows
-// V neighbouring channels of a row as loaded: two bf16 in a word, or one value.
-template <bool BF16, int V>
-__device__ __forceinline__ uint32_t load_raw_at(const void* row, uint32_t ch) {
-  if constexpr (BF16 && V == 1) return static_cast<const uint16_t*>(row)[ch];
-  else if constexpr (BF16) return *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(row) + ch);
-  else return static_cast<const uint32_t*>(row)[ch];
+// Rows r0, r0 + 1, .. of a tensor, one descriptor each (its base in scalar
+// registers, a lane's channel as the offset: no address arithmetic in the vector
+// unit).  A row's bytes fit 32 bits.
+template <bool BF16>
+struct Rows {
+  char* at;
+  int64_t step;
+  uint32_t bytes;
+  __device__ __forceinline__ Rows(const void* p, int64_t r0, int64_t stride, int64_t dim)
+      : at(static_cast<char*>(const_cast<void*>(p)) + r0 * stride * (BF16 ? 2 : 4)),
+        step(stride * (BF16 ? 2 : 4)),
+        bytes((uint32_t)dim * (BF16 ? 2 : 4)) {}
+  __device__ __forceinline__ rsrc_t row(int j) const { return make_rsrc(at + j * step, bytes); }
+};
+
+// V neighbouring channels as loaded: two bf16 in a word, or one value.  Of T rows
+// only n exist; the rest read as `none`.
+template <bool BF16, int V, int T>
+__device__ __forceinline__ void load_rows(const Rows<BF16>& r, uint32_t off, int n, uint32_t none, uint32_t (&raw)[T]) {
+  const auto load = [&](int j) -> uint32_t {
+    if constexpr (BF16 && V == 1) return buf_load_u16(r.row(j), off);
+    else return buf_load_u32(r.row(j), off);
+  };
+  if (n == T) {
+#pragma unroll
+    for (int j = 0; j < T; ++j) raw[j] = load(j);
+  } else {
+#pragma unroll
+    for (int j = 0; j < T; ++j) raw[j] = j < n ? load(j < n ? j : 0) : none;
+  }
 }
+// Gates of minus infinity and inputs of zero make a step that changes nothing.
+template <bool BF16>
+constexpr uint32_t kClosed = BF16 ? 0xff80ff80u : 0xff800000u;
+
 template <bool BF16, int V>
 __device__ __forceinline__ float widen_at(uint32_t w, int v) {
   if constexpr (!BF16) return __uint_as_float(w);
   else return v == 0 ? bf16_lo(w) : bf16_hi(w);
 }
+// Rows past the n-th are not stored, nor what a lane without channels has.
 template <bool BF16, int V>
-__device__ __forceinline__ void store_at(void* row, uint32_t ch, const float (&o)[V]) {
-  if constexpr (BF16 && V == 1) static_cast<uint16_t*>(row)[ch] = f32_to_bf16(o[0]);
-  else if constexpr (BF16) *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(row) + ch) = pack_bf16x2(o[0], o[1]);
-  else static_cast<float*>(row)[ch] = o[0];
-}
-// Rows r0, r0 + 1, .. of a tensor, a wave's lanes at channel ch; past the last of n
-// rows the last is repeated.  WHOLE: there are T.
-template <bool BF16, int V, int T, bool WHOLE>
-__device__ __forceinline__ void load_rows(const void* p, int64_t r0, int64_t stride, uint32_t ch, int n,
-                                          uint32_t (&raw)[T]) {
-  const char* row = static_cast<const char*>(p) + r0 * stride * (BF16 ? 2 : 4);
-  const int64_t step = stride * (BF16 ? 2 : 4);
-#pragma unroll
-  for (int j = 0; j < T; ++j) {
-    raw[j] = load_raw_at<BF16, V>(row, ch);
-    if (WHOLE || j + 1 < n) row += step;
-  }
+__device__ __forceinline__ void store_row(const Rows<BF16>& r, int j, int n, uint32_t off, const float (&o)[V]) {
+  const rsrc_t d = make_rsrc(r.at + j * r.step, j < n ? r.bytes : 0u);
+  if constexpr (BF16 && V == 1) buf_store_u16(d, off, f32_to_bf16(o[0]));
+  else if constexpr (BF16) buf_store_u32(d, off, pack_bf16x2(o[0], o[1]));
+  else buf_store_u32(d, off, __float_as_uint(o[0]));
 }
 
 // Where a wave works: which piece, its steps, its lane's channels.
@@ -202,10 +219,11 @@ struct WavePlace {
   int n;             // steps that exist
   uint32_t ch;       // first channel, kept inside the row
   bool ok;           // whether it exists
+  uint32_t in, out;  // its offset in a row for loads, and for stores
 };
 
 // `piece` in order along time; a lane past the last channel repeats it.
-template <int V, int W, int T>
+template <bool BF16, int V, int W, int T>
 __device__ __forceinline__ WavePlace<V, W, T> wave_place(int64_t id, int streams, int blocks, int64_t pieces,
                                                          bool reversed, int64_t seqlen, int64_t dim) {
   WavePlace<V, W, T> w;
@@ -216,10 +234,12 @@ __device__ __forceinline__ WavePlace<V, W, T> wave_place(int64_t id, int streams
   const int64_t piece = reversed ? pieces - 1 - w.place : w.place;
   w.t0 = piece * (W * T) + w.wave * T;
   const int64_t left = seqlen - w.t0;
-  w.n = left < 0 ? 0 : left < T ? (int)left : T;
+  w.n = left < 0 ? 0 : left < T ? __builtin_amdgcn_readfirstlane((int)left) : T;
   const int64_t c = (int64_t)(w.stream - (int)w.b * blocks) * (64 * V) + (threadIdx.x & 63) * V;
   w.ok = c < dim;
   w.ch = (uint32_t)(w.ok ? c : dim - V);
+  w.in = w.ch * (BF16 ? 2u : 4u);
+  w.out = w.ok ? w.in : kOffNone;
   return w;
 }
 
@@ -231,6 +251,43 @@ __device__ __forceinline__ uint64_t start_bits(const uint8_t* starts, int64_t ro
   return __ballot(lane < n && starts[row + (lane < n ? lane : 0)] != 0);
 }
 
+// Bit i: a sequence starts in wave i's steps.
+template <int W>
+__device__ __forceinline__ uint32_t cut_bits(const int* lds_cut) {
+  return (uint32_t)__ballot(lds_cut[threadIdx.x & (W - 1)] != 0) & ((1u << W) - 1);
+}
+
+// Folds the waves lo .. hi - 1, in order (REVERSED: from the last), onto (a, x):
+// x <- A x + X, a <- A a; where a sequence starts x is X alone (and a has no
+// meaning any more).  Four waves' values are read at a time: one after the other
+// the fold would take eight times LDS's latency.
+template <int V, int W, bool REVERSED>
+__device__ __forceinline__ void fold_waves(const float (*lds_a)[64 * V], const float (*lds_x)[64 * V], uint32_t cuts,
+                                           int lo, int hi, float (&a)[V], float (&x)[V]) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int g = 0; g < W; g += 4) {
+    float la[4][V], lx[4][V];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int i = REVERSED ? W - 1 - g - q : g + q;
+#pragma unroll
+      for (int v = 0; v < V; ++v) la[q][v] = lds_a[i][lane * V + v], lx[q][v] = lds_x[i][lane * V + v];
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int i = REVERSED ? W - 1 - g - q : g + q;
+      if (i < lo || i >= hi) continue;
+      const bool cut = cuts >> i & 1;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        x[v] = cut ? lx[q][v] : __builtin_fmaf(la[q][v], x[v], lx[q][v]);
+        a[v] *= la[q][v];
+      }
+    }
+  }
+}
+
 // ------------------------------------------------------------ forward
 struct FwdArgs {
   RecurrenceFwdParams p;
@@ -239,8 +296,8 @@ struct FwdArgs {
   int64_t pieces;  // of a stream
 };
 
-template <bool BF16, int V, int W, int T>
-__global__ void __launch_bounds__(W * 64) recurrence_fwd_kernel(FwdArgs a) {
+template <bool BF16, int V, int W, int T, bool STARTS>
+__global__ void __launch_bounds__(W * 64) __attribute__((amdgpu_waves_per_eu(4))) recurrence_fwd_kernel(FwdArgs a) {
   __shared__ float lds_a[W][64 * V], lds_h[W][64 * V], lds_carry[64 * V];
   __shared__ int lds_cut[W], lds_id;
   const RecurrenceFwdParams& p = a.p;
@@ -252,59 +309,52 @@ __global__ void __launch_bounds__(W * 64) recurrence_fwd_kernel(FwdArgs a) {
   } else if (id == 0 && threadIdx.x == 0) {
     *static_cast<int*>(p.workspace) = 0;  // the status word: nothing waits
   }
-  const auto w = wave_place<V, W, T>(id, a.chain.streams, a.blocks, a.pieces, false, p.seqlen, p.dim);
+  const auto w = wave_place<BF16, V, W, T>(id, a.chain.streams, a.blocks, a.pieces, false, p.seqlen, p.dim);
   const int lane = threadIdx.x & 63;
   const int64_t row0 = w.b * p.seqlen + w.t0;
 
+  float lam[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) lam[v] = p.lam[w.ch + v];
   uint32_t rx[T], ra[T], ri[T];
-  const auto load = [&](auto whole) {
-    load_rows<BF16, V, T, whole()>(p.gate_a, row0, p.gate_a_stride, w.ch, w.n, ra);
-    load_rows<BF16, V, T, whole()>(p.gate_x, row0, p.gate_x_stride, w.ch, w.n, ri);
-    load_rows<BF16, V, T, whole()>(p.x, row0, p.x_stride, w.ch, w.n, rx);
-  };
-  if (w.n == T) load(std::true_type{});
-  else if (w.n > 0) load(std::false_type{});
-  const uint64_t starts = w.n > 0 ? start_bits<T>(p.starts, row0, w.n) : 0;
-  const bool plain = w.n == T && starts == 0;
+  load_rows<BF16, V, T>(Rows<BF16>(p.gate_a, row0, p.gate_a_stride, p.dim), w.in, w.n, kClosed<BF16>, ra);
+  load_rows<BF16, V, T>(Rows<BF16>(p.gate_x, row0, p.gate_x_stride, p.dim), w.in, w.n, kClosed<BF16>, ri);
+  load_rows<BF16, V, T>(Rows<BF16>(p.x, row0, p.x_stride, p.dim), w.in, w.n, 0u, rx);
+  const uint64_t starts = STARTS ? start_bits<T>(p.starts, row0, w.n) : 0;
   float k[V];
-  bool low = true;
+  bool slow = true;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    k[v] = p.c * softplus_of(p.lam[w.ch + v]);
-    low = low && k[v] <= kPolySmall;
+    k[v] = decay_rate(p.c, lam[v]);
+    slow = slow && k[v] <= kPolySmall;
   }
 
   // From a zero state: after each step the state and the product of the decays.
   float pr[T][V], hl[T][V], ha[V], hh[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) ha[v] = 1.0f, hh[v] = 0.0f;
-  const auto local = [&](auto whole, auto small) {
+  const auto local = [&](auto small) {
 #pragma unroll
     for (int j = 0; j < T; ++j) {
-      if (!whole() && j >= w.n) break;
-      const bool start = !whole() && (starts >> j & 1);
+      const bool start = STARTS && (starts >> j & 1);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const float mj = one_minus_exp<small()>(k[v] * sigmoid_of<!BF16>(widen_at<BF16, V>(ra[j], v)));
-        const float in = __builtin_amdgcn_sqrtf(mj * (2.0f - mj)) * sigmoid_of<!BF16>(widen_at<BF16, V>(ri[j], v)) *
-                         widen_at<BF16, V>(rx[j], v);
-        hh[v] = (start ? 0.0f : __builtin_fmaf(-mj, hh[v], hh[v])) + in;
-        ha[v] = __builtin_fmaf(-mj, ha[v], ha[v]);
+        const float n = exp_less_one<small()>(k[v] * sigmoid_of<!BF16>(widen_at<BF16, V>(ra[j], v)));
+        const float u = beta_of(n) * sigmoid_of<!BF16>(widen_at<BF16, V>(ri[j], v));
+        hh[v] = __builtin_fmaf(u, widen_at<BF16, V>(rx[j], v), start ? 0.0f : __builtin_fmaf(n, hh[v], hh[v]));
+        ha[v] = __builtin_fmaf(n, ha[v], ha[v]);
         hl[j][v] = hh[v];
         pr[j][v] = ha[v];
       }
     }
   };
-  if (plain) {
-    if (__all(low)) local(std::true_type{}, std::true_type{});
-    else local(std::true_type{}, std::false_type{});
-  } else if (w.n > 0) {
-    local(std::false_type{}, std::false_type{});
-  }
+  if (__all(slow)) local(std::true_type{});
+  else local(std::false_type{});
 #pragma unroll
   for (int v = 0; v < V; ++v) lds_a[w.wave][lane * V + v] = ha[v], lds_h[w.wave][lane * V + v] = hh[v];
-  if (lane == 0) lds_cut[w.wave] = starts != 0;
+  if (STARTS && lane == 0) lds_cut[w.wave] = starts != 0;
   __syncthreads();
+  const uint32_t cuts = STARTS ? cut_bits<W>(lds_cut) : 0u;
 
   if (w.wave == 0) {
     float first[V], carry[V];
@@ -314,60 +364,40 @@ __global__ void __launch_bounds__(W * 64) recurrence_fwd_kernel(FwdArgs a) {
 #pragma unroll
       for (int v = 0; v < V; ++v) carry[v] = first[v];
     } else {
-      bool cut = starts != 0;
-      for (int i = 1; i < W; ++i) {
-        const bool c = lds_cut[i] != 0;
-        cut |= c;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const float ai = lds_a[i][lane * V + v], hi = lds_h[i][lane * V + v];
-          hh[v] = c ? hi : __builtin_fmaf(ai, hh[v], hi);
-          ha[v] *= ai;
-        }
-      }
-      chain_carry<V>(a.chain, w.place, w.stream, w.place + 1 == a.pieces, cut, ha, hh, first, carry);
+      fold_waves<V, W, false>(lds_a, lds_h, cuts, 1, W, ha, hh);
+      chain_carry<V>(a.chain, w.place, w.stream, w.place + 1 == a.pieces, cuts != 0, ha, hh, first, carry);
     }
 #pragma unroll
-    for (int v = 0; v < V; ++v) lds_carry[lane * V + v] = carry[v];
+    for (int v = 0; v < V; ++v) lds_carry[lane * V + v] = carry[v], ha[v] = 1.0f, hh[v] = 0.0f;
+  } else {  // from the piece's first step to the wave's
+#pragma unroll
+    for (int v = 0; v < V; ++v) ha[v] = 1.0f, hh[v] = 0.0f;
+    fold_waves<V, W, false>(lds_a, lds_h, cuts, 0, w.wave, ha, hh);
   }
   __syncthreads();
 
   if (w.n == 0) return;
   float q[V];
+  const bool apart = (cuts & ((1u << w.wave) - 1)) != 0;
 #pragma unroll
-  for (int v = 0; v < V; ++v) q[v] = lds_carry[lane * V + v];
-  for (int i = 0; i < w.wave; ++i) {
-    const bool c = lds_cut[i] != 0;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const float hi = lds_h[i][lane * V + v];
-      q[v] = c ? hi : __builtin_fmaf(lds_a[i][lane * V + v], q[v], hi);
-    }
-  }
-  if (!w.ok) return;
-  if (p.states != nullptr && w.t0 % kRecurrenceChunk == 0) {
+  for (int v = 0; v < V; ++v) q[v] = apart ? hh[v] : __builtin_fmaf(ha[v], lds_carry[lane * V + v], hh[v]);
+  if (p.states != nullptr && w.ok && w.t0 % kRecurrenceChunk == 0) {
     const int64_t chunks = (p.seqlen + kRecurrenceChunk - 1) / kRecurrenceChunk;
 #pragma unroll
     for (int v = 0; v < V; ++v) p.states[(w.b * chunks + w.t0 / kRecurrenceChunk) * p.dim + w.ch + v] = q[v];
   }
-  char* y = static_cast<char*>(p.y) + row0 * p.y_stride * (BF16 ? 2 : 4);
-  const auto apply = [&](auto whole) {
+  const Rows<BF16> y(p.y, row0, p.y_stride, p.dim);
 #pragma unroll
-    for (int j = 0; j < T; ++j) {
-      if (!whole() && j >= w.n) break;
-      const bool cut = !whole() && (starts & ((2ull << j) - 1)) != 0;
-      float o[V];
+  for (int j = 0; j < T; ++j) {
+    const bool cut = STARTS && (starts & ((2ull << j) - 1)) != 0;
+    float o[V];
 #pragma unroll
-      for (int v = 0; v < V; ++v) o[v] = cut ? hl[j][v] : __builtin_fmaf(pr[j][v], q[v], hl[j][v]);
-      store_at<BF16, V>(y, w.ch, o);
-      y += p.y_stride * (BF16 ? 2 : 4);
-      if (p.h_last != nullptr && w.t0 + j == p.seqlen - 1)
+    for (int v = 0; v < V; ++v) o[v] = cut ? hl[j][v] : __builtin_fmaf(pr[j][v], q[v], hl[j][v]);
+    store_row<BF16, V>(y, j, w.n, w.out, o);
+    if (p.h_last != nullptr && w.ok && w.t0 + j == p.seqlen - 1)
 #pragma unroll
-        for (int v = 0; v < V; ++v) p.h_last[w.b * p.dim + w.ch + v] = o[v];
-    }
-  };
-  if (plain) apply(std::true_type{});
-  else apply(std::false_type{});
+      for (int v = 0; v < V; ++v) p.h_last[w.b * p.dim + w.ch + v] = o[v];
+  }
 }
 
 // ------------------------------------------------------------ backward
@@ -379,14 +409,18 @@ struct BwdArgs {
   int64_t pieces;
 };
 
-// Below, beta = sqrt(2 m) and s / beta = sqrt(m / 2) add nothing to what they meet
-// (the reciprocal root takes such an m for 0).
+// Least beta^2 whose reciprocal root is taken: below, what it is multiplied by is next to
+// nothing or 0, which must not meet an infinity.
 constexpr float kLeastNormal = 1.1754944e-38f;
 
-// One piece is one chunk: W T = kRecurrenceChunk.
-template <bool BF16, int V, int W, int T>
-__global__ void __launch_bounds__(W * 64) recurrence_bwd_kernel(BwdArgs a) {
+// One piece is one chunk: W T = kRecurrenceChunk.  Of a step, n and h_{t-1} stay in
+// registers until the gradients, the gates' exponentials in LDS (each lane its
+// own).  With w = dx x:
+//   dx = g i beta,  dgate_x = w (1 - i),  G = s a (a w / beta^2 - g h_{t-1}).
+template <bool BF16, int V, int W, int T, bool STARTS>
+__global__ void __launch_bounds__(W * 64) __attribute__((amdgpu_waves_per_eu(4))) recurrence_bwd_kernel(BwdArgs a) {
   static_assert(W * T == kRecurrenceChunk, "");
+  extern __shared__ __align__(16) float lds_kept[];  // [2][W][T][64 V]
   __shared__ float lds_a[W][64 * V], lds_h[W][64 * V], lds_e[W][64 * V], lds_carry[64 * V];
   __shared__ int lds_cut[W], lds_id;
   const RecurrenceBwdParams& p = a.p;
@@ -398,187 +432,151 @@ __global__ void __launch_bounds__(W * 64) recurrence_bwd_kernel(BwdArgs a) {
   } else if (id == 0 && threadIdx.x == 0) {
     *static_cast<int*>(p.workspace) = 0;  // the status word: nothing waits
   }
-  const auto w = wave_place<V, W, T>(id, a.chain.streams, a.blocks, a.pieces, true, p.seqlen, p.dim);
+  const auto w = wave_place<BF16, V, W, T>(id, a.chain.streams, a.blocks, a.pieces, true, p.seqlen, p.dim);
   const int lane = threadIdx.x & 63;
   const int64_t row0 = w.b * p.seqlen + w.t0, piece = a.pieces - 1 - w.place;
 
-  uint32_t rx[T], ra[T], ri[T], rd[T];
-  const auto load = [&](auto whole) {
-    load_rows<BF16, V, T, whole()>(p.gate_a, row0, p.gate_a_stride, w.ch, w.n, ra);
-    load_rows<BF16, V, T, whole()>(p.gate_x, row0, p.gate_x_stride, w.ch, w.n, ri);
-    load_rows<BF16, V, T, whole()>(p.x, row0, p.x_stride, w.ch, w.n, rx);
-    load_rows<BF16, V, T, whole()>(p.dy, row0, p.dy_stride, w.ch, w.n, rd);
-  };
-  if (w.n == T) load(std::true_type{});
-  else if (w.n > 0) load(std::false_type{});
-  const uint64_t starts = w.n > 0 ? start_bits<T>(p.starts, row0, w.n) : 0;
-  const bool plain = w.n == T && starts == 0;
-  float k[V], sp[V], before[V];  // before: the state entering the piece, then this wave's steps
-  bool low = true;
+  float lam[V], before[V];  // before: the state entering the piece, then this wave's steps
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    sp[v] = softplus_of(p.lam[w.ch + v]);
-    k[v] = p.c * sp[v];
-    low = low && k[v] <= kPolySmall;
+    lam[v] = p.lam[w.ch + v];
     before[v] = p.states[(w.b * a.pieces + piece) * p.dim + w.ch + v];
   }
+  uint32_t rx[T], ra[T], ri[T], rd[T];
+  load_rows<BF16, V, T>(Rows<BF16>(p.gate_a, row0, p.gate_a_stride, p.dim), w.in, w.n, kClosed<BF16>, ra);
+  load_rows<BF16, V, T>(Rows<BF16>(p.gate_x, row0, p.gate_x_stride, p.dim), w.in, w.n, kClosed<BF16>, ri);
+  load_rows<BF16, V, T>(Rows<BF16>(p.x, row0, p.x_stride, p.dim), w.in, w.n, 0u, rx);
+  load_rows<BF16, V, T>(Rows<BF16>(p.dy, row0, p.dy_stride, p.dim), w.in, w.n, 0u, rd);
+  const uint64_t starts = STARTS ? start_bits<T>(p.starts, row0, w.n) : 0;
+  float k[V];
+  bool slow = true;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    k[v] = decay_rate(p.c, lam[v]);
+    slow = slow && k[v] <= kPolySmall;
+  }
 
-  // From a zero state forwards (hl), from a zero gradient backwards (e).
-  float m[T][V], hl[T][V], ha[V], hh[V], e[V];
+  // From a zero state forwards (hl); what the gradients of dy here leave behind, e =
+  // sum a_0 .. a_j dy_j up to a start.
+  typedef float vec __attribute__((ext_vector_type(V)));
+  vec* const exp_a = reinterpret_cast<vec*>(lds_kept) + w.wave * (T * 64) + lane;
+  vec* const exp_x = exp_a + W * T * 64;
+  float n[T][V], hl[T][V], ha[V], hh[V], e[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) ha[v] = 1.0f, hh[v] = 0.0f, e[v] = 0.0f;
-  const auto local = [&](auto whole, auto small) {
+  const auto local = [&](auto small) {
 #pragma unroll
     for (int j = 0; j < T; ++j) {
-      if (!whole() && j >= w.n) break;
-      const bool start = !whole() && (starts >> j & 1);
+      const bool start = STARTS && (starts >> j & 1), cut = STARTS && (starts & ((2ull << j) - 1)) != 0;
+      vec ea, ex;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const float mj = one_minus_exp<small()>(k[v] * sigmoid_of<!BF16>(widen_at<BF16, V>(ra[j], v)));
-        const float in = __builtin_amdgcn_sqrtf(mj * (2.0f - mj)) * sigmoid_of<!BF16>(widen_at<BF16, V>(ri[j], v)) *
-                         widen_at<BF16, V>(rx[j], v);
-        m[j][v] = mj;
-        hh[v] = (start ? 0.0f : __builtin_fmaf(-mj, hh[v], hh[v])) + in;
-        ha[v] = __builtin_fmaf(-mj, ha[v], ha[v]);
+        ea[v] = exp_neg<!BF16>(widen_at<BF16, V>(ra[j], v));
+        ex[v] = exp_neg<!BF16>(widen_at<BF16, V>(ri[j], v));
+        n[j][v] = exp_less_one<small()>(k[v] * rcp_fast(1.0f + ea[v]));
+        hh[v] = __builtin_fmaf(beta_of(n[j][v]) * rcp_fast(1.0f + ex[v]), widen_at<BF16, V>(rx[j], v),
+                               start ? 0.0f : __builtin_fmaf(n[j][v], hh[v], hh[v]));
+        ha[v] = __builtin_fmaf(n[j][v], ha[v], ha[v]);
+        e[v] = cut ? e[v] : __builtin_fmaf(ha[v], widen_at<BF16, V>(rd[j], v), e[v]);
         hl[j][v] = hh[v];
       }
-    }
-#pragma unroll
-    for (int j = T - 1; j >= 0; --j) {
-      if (!whole() && j >= w.n) continue;
-      const bool start = !whole() && (starts >> j & 1);
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const float g = widen_at<BF16, V>(rd[j], v) + e[v];
-        e[v] = start ? 0.0f : __builtin_fmaf(-m[j][v], g, g);
-      }
+      exp_a[j * 64] = ea;
+      exp_x[j * 64] = ex;
     }
   };
-  if (plain) {
-    if (__all(low)) local(std::true_type{}, std::true_type{});
-    else local(std::true_type{}, std::false_type{});
-  } else if (w.n > 0) {
-    local(std::false_type{}, std::false_type{});
-  }
+  if (__all(slow)) local(std::true_type{});
+  else local(std::false_type{});
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     lds_a[w.wave][lane * V + v] = ha[v];
     lds_h[w.wave][lane * V + v] = hh[v];
     lds_e[w.wave][lane * V + v] = e[v];
   }
-  if (lane == 0) lds_cut[w.wave] = starts != 0;
+  if (STARTS && lane == 0) lds_cut[w.wave] = starts != 0;
   __syncthreads();
+  const uint32_t cuts = STARTS ? cut_bits<W>(lds_cut) : 0u;
 
-  if (w.wave == 0) {
-    float first[V], carry[V], ea[V], ee[V];
-    bool cut = false;
+  float ea[V], ee[V];  // from the piece's last step to the wave's
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
+  for (int v = 0; v < V; ++v) ea[v] = 1.0f, ee[v] = 0.0f;
+  fold_waves<V, W, true>(lds_a, lds_e, cuts, w.wave + 1, W, ea, ee);
+  if (w.wave == 0) {
+    float first[V], carry[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v)
       first[v] = p.dh_last != nullptr && w.place == 0 ? p.dh_last[w.b * p.dim + w.ch + v] : 0.0f;
-      ea[v] = 1.0f, ee[v] = 0.0f;
-    }
     if (a.chain.status == nullptr) {
 #pragma unroll
       for (int v = 0; v < V; ++v) carry[v] = first[v];
     } else {
-      for (int i = W - 1; i >= 0; --i) {
-        const bool c = lds_cut[i] != 0;
-        cut |= c;
+      float pa[V], pe[V];
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const float ai = lds_a[i][lane * V + v], ei = lds_e[i][lane * V + v];
-          ee[v] = c ? ei : __builtin_fmaf(ai, ee[v], ei);
-          ea[v] *= ai;
-        }
+      for (int v = 0; v < V; ++v) {
+        pa[v] = ha[v] * ea[v];
+        pe[v] = starts != 0 ? e[v] : __builtin_fmaf(ha[v], ee[v], e[v]);
       }
-      chain_carry<V>(a.chain, w.place, w.stream, w.place + 1 == a.pieces, cut, ea, ee, first, carry);
+      chain_carry<V>(a.chain, w.place, w.stream, w.place + 1 == a.pieces, cuts != 0, pa, pe, first, carry);
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) lds_carry[lane * V + v] = carry[v];
   }
   // The states before each step, from the one that enters the piece.
-  for (int i = 0; i < w.wave; ++i) {
-    const bool c = lds_cut[i] != 0;
+  fold_waves<V, W, false>(lds_a, lds_h, cuts, 0, w.wave, ha, before);
+  float q[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) q[v] = before[v];
+#pragma unroll
+  for (int j = 0; j < T; ++j) {
+    const bool start = STARTS && (starts >> j & 1);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const float hi = lds_h[i][lane * V + v];
-      before[v] = c ? hi : __builtin_fmaf(lds_a[i][lane * V + v], before[v], hi);
+      q[v] = start ? 0.0f : __builtin_fmaf(n[j][v], q[v], q[v]);
+      hl[j][v] += q[v];
     }
   }
-  const auto enter = [&](auto whole) {
-    float q[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) q[v] = before[v];
-#pragma unroll
-    for (int j = 0; j < T; ++j) {
-      if (!whole() && j >= w.n) break;
-      const bool start = !whole() && (starts >> j & 1);
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        q[v] = start ? 0.0f : __builtin_fmaf(-m[j][v], q[v], q[v]);
-        hl[j][v] += q[v];
-      }
-    }
-  };
-  if (plain) enter(std::true_type{});
-  else if (w.n > 0) enter(std::false_type{});
   __syncthreads();
 
+  const bool apart = (cuts >> w.wave >> 1) != 0;
 #pragma unroll
-  for (int v = 0; v < V; ++v) e[v] = lds_carry[lane * V + v];
-  for (int i = W - 1; i > w.wave; --i) {
-    const bool c = lds_cut[i] != 0;
+  for (int v = 0; v < V; ++v) e[v] = apart ? ee[v] : __builtin_fmaf(ea[v], lds_carry[lane * V + v], ee[v]);
+  // Widened again from here on: values kept wide would not fit the registers.
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const float ei = lds_e[i][lane * V + v];
-      e[v] = c ? ei : __builtin_fmaf(lds_a[i][lane * V + v], e[v], ei);
-    }
-  }
+  for (int j = 0; j < T; ++j) asm volatile("" : "+v"(rx[j]), "+v"(rd[j]));
   float dlam[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) dlam[v] = 0.0f;
-  const int64_t es = BF16 ? 2 : 4;
-  char* dx = static_cast<char*>(p.dx) + (row0 + w.n) * p.dx_stride * es;
-  char* da = static_cast<char*>(p.dgate_a) + (row0 + w.n) * p.dgate_a_stride * es;
-  char* di = static_cast<char*>(p.dgate_x) + (row0 + w.n) * p.dgate_x_stride * es;
-  const auto grads = [&](auto whole) {
+  const Rows<BF16> dx(p.dx, row0, p.dx_stride, p.dim), da(p.dgate_a, row0, p.dgate_a_stride, p.dim),
+      di(p.dgate_x, row0, p.dgate_x_stride, p.dim);
 #pragma unroll
-    for (int j = T - 1; j >= 0; --j) {
-      if (!whole() && j >= w.n) continue;
-      const bool start = !whole() && (starts >> j & 1);
-      float ox[V], oa[V], oi[V];
+  for (int j = T - 1; j >= 0; --j) {
+    const bool start = STARTS && (starts >> j & 1);
+    float ox[V], oa[V], oi[V];
+    const vec ka = exp_a[j * 64], kx = exp_x[j * 64];
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        float rr, rest;
-        const float r = sigmoid_of<!BF16>(widen_at<BF16, V>(ra[j], v), rr);
-        const float i = sigmoid_of<!BF16>(widen_at<BF16, V>(ri[j], v), rest);
-        const float s = finite_decay(k[v] * r), mj = m[j][v], dec = 1.0f - mj, beta2 = mj * (2.0f - mj);
-        const float inv = __builtin_amdgcn_rsqf(beta2), beta = mj >= kLeastNormal ? beta2 * inv : mj;
-        const float g = widen_at<BF16, V>(rd[j], v) + e[v];
-        const float gi = g * i, gix = gi * widen_at<BF16, V>(rx[j], v);
-        const float from_beta = dec * dec * (mj >= kLeastNormal ? s * inv : mj) * gix;
-        const float prev = j > 0 ? hl[j > 0 ? j - 1 : 0][v] : before[v];
-        const float big = from_beta - (start ? 0.0f : s * dec * (g * prev));
-        ox[v] = gi * beta;
-        oi[v] = gix * beta * rest;
-        oa[v] = big * rr;
-        dlam[v] += big;
-        e[v] = start ? 0.0f : __builtin_fmaf(-mj, g, g);
-      }
-      dx -= p.dx_stride * es, da -= p.dgate_a_stride * es, di -= p.dgate_x_stride * es;
-      if (w.ok) {
-        store_at<BF16, V>(dx, w.ch, ox);
-        store_at<BF16, V>(da, w.ch, oa);
-        store_at<BF16, V>(di, w.ch, oi);
-      }
+    for (int v = 0; v < V; ++v) {
+      float rest_r, rest_i;
+      const float r = sigmoid_from(ka[v], rest_r), i = sigmoid_from(kx[v], rest_i);
+      const float dec = 1.0f + n[j][v], beta2 = __builtin_fmaf(-n[j][v], dec, -n[j][v]);
+      const float inv = __builtin_amdgcn_rsqf(__builtin_amdgcn_fmed3f(beta2, kLeastNormal, 2.0f));
+      const float g = widen_at<BF16, V>(rd[j], v) + e[v];
+      const float prev = j > 0 ? hl[j > 0 ? j - 1 : 0][v] : before[v];
+      ox[v] = g * i * (beta2 * inv);
+      const float wx = ox[v] * widen_at<BF16, V>(rx[j], v);
+      oi[v] = wx * rest_i;
+      const float big = k[v] * r * dec * __builtin_fmaf(dec * (inv * inv), wx, start ? 0.0f : -g * prev);
+      oa[v] = big * rest_r;
+      dlam[v] += j < w.n ? big : 0.0f;
+      e[v] = start ? 0.0f : __builtin_fmaf(n[j][v], g, g);
     }
-  };
-  if (plain) grads(std::true_type{});
-  else if (w.n > 0) grads(std::false_type{});
+    store_row<BF16, V>(dx, j, w.n, w.out, ox);
+    store_row<BF16, V>(da, j, w.n, w.out, oa);
+    store_row<BF16, V>(di, j, w.n, w.out, oi);
+    if (j % 2 == 0) __builtin_amdgcn_sched_barrier(0);  // no more than two steps at once: registers
+  }
   if (w.wave == 0 && piece == 0 && p.dh0 != nullptr && w.ok)
 #pragma unroll
     for (int v = 0; v < V; ++v) p.dh0[w.b * p.dim + w.ch + v] = e[v];
-  __syncthreads();  // lds_h has been read
+  // (lds_h was last read before the barrier above.)
 #pragma unroll
   for (int v = 0; v < V; ++v) lds_h[w.wave][lane * V + v] = dlam[v];
   __syncthreads();
@@ -586,8 +584,9 @@ __global__ void __launch_bounds__(W * 64) recurrence_bwd_kernel(BwdArgs a) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       float sum = 0.0f;
+#pragma unroll
       for (int i = 0; i < W; ++i) sum += lds_h[i][lane * V + v];
-      a.part[(w.b * a.pieces + piece) * p.dim + w.ch + v] = sum * softplus_rate(p.lam[w.ch + v], sp[v]);
+      a.part[(w.b * a.pieces + piece) * p.dim + w.ch + v] = sum * softplus_rate(lam[v], softplus_of(lam[v]));
     }
   }
 }
@@ -636,8 +635,9 @@ hipError_t launch_fwd(const RecurrenceFwdParams& p, hipStream_t stream) {
   FwdArgs a{p, {}, (int)c.blocks, c.pieces};
   const hipError_t e = start_chain(c, p.workspace, a.chain, stream);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((recurrence_fwd_kernel<BF16, V, kWaves, kFwdSteps>), dim3((unsigned)(c.streams * c.pieces)),
-                     dim3(kWaves * 64), 0, stream, a);
+  const auto kernel = p.starts != nullptr ? recurrence_fwd_kernel<BF16, V, kWaves, kFwdSteps, true>
+                                          : recurrence_fwd_kernel<BF16, V, kWaves, kFwdSteps, false>;
+  hipLaunchKernelGGL(kernel, dim3((unsigned)(c.streams * c.pieces)), dim3(kWaves * 64), 0, stream, a);
   return hipGetLastError();
 }
 
@@ -650,8 +650,10 @@ hipError_t launch_bwd(const RecurrenceBwdParams& p, hipStream_t stream) {
             c.pieces};
   hipError_t e = start_chain(c, p.workspace, a.chain, stream);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((recurrence_bwd_kernel<BF16, V, kWaves, kBwdSteps>), dim3((unsigned)(c.streams * c.pieces)),
-                     dim3(kWaves * 64), 0, stream, a);
+  const auto kernel = p.starts != nullptr ? recurrence_bwd_kernel<BF16, V, kWaves, kBwdSteps, true>
+                                          : recurrence_bwd_kernel<BF16, V, kWaves, kBwdSteps, false>;
+  hipLaunchKernelGGL(kernel, dim3((unsigned)(c.streams * c.pieces)), dim3(kWaves * 64),
+                     2 * kRecurrenceChunk * 64 * V * sizeof(float), stream, a);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   SumPartialsArgs s{};

@@ -2,16 +2,16 @@
 // gradient and its one-token step.  Per channel and step:
 //   r = sigmoid(gate_a), i = sigmoid(gate_x), s = k r with k = c softplus(lam),
 //   a = exp(-s), beta = sqrt(1 - a^2), h <- a h + beta i x.
-// The decay is kept as m = 1 - a = -expm1(-s): decays are near 1 (s is a few
-// hundredths), where a itself would hold only the leading digits of m, and m
-// gives both h - m h and beta^2 = m (2 - m) without cancellation.
+// The decay is kept as n = a - 1 = expm1(-s), in [-1, 0]: decays are near 1 (s is a
+// few hundredths), where a itself would hold only the leading digits of n, and n
+// gives both h + n h and beta^2 = -n (2 + n) without cancellation.
 #pragma once
 
 #include "common.hpp"
 
 namespace mss {
 
-// Of s, for the polynomials of one_minus_exp.
+// Of s, for the polynomials of exp_less_one.
 constexpr float kPolySmall = 0.25f, kPolyMax = 0.5f;
 
 // E = exp(-v).  EXACT (fp32 tensors): with what the rounding of the argument
@@ -31,38 +31,42 @@ __device__ __forceinline__ float exp_neg(float v) {
   }
 }
 
-// sigmoid(v), and with E also 1 - sigmoid(v) without cancellation.
+// sigmoid(v).
 template <bool EXACT>
 __device__ __forceinline__ float sigmoid_of(float v) {
   return rcp_fast(1.0f + exp_neg<EXACT>(v));
 }
-template <bool EXACT>
-__device__ __forceinline__ float sigmoid_of(float v, float& rest) {
-  const float e = exp_neg<EXACT>(v), s = rcp_fast(1.0f + e);
-  rest = e < __builtin_inff() ? e * s : 1.0f;
+// From E = exp(-v), also 1 - sigmoid(v) = E sigmoid(v), without cancellation.  Where
+// E is infinite the sigmoid is 0, and so is what its rest is multiplied by; the
+// limits, an output modifier of the product, make 0 of infinity times 0.
+__device__ __forceinline__ float sigmoid_from(float e, float& rest) {
+  const float s = rcp_fast(1.0f + e);
+  rest = __builtin_amdgcn_fmed3f(e * s, 0.0f, 1.0f);
   return s;
 }
 
-// 1 - exp(-s) for s >= 0: s times a polynomial fitted to (1 - exp(-s)) / s at
+// exp(-s) - 1 for s >= 0: s times a polynomial fitted to (exp(-s) - 1) / s at
 // Chebyshev points (off by 2.4e-9 of 1 up to 1/4, where decays of a trained layer
 // lie; by 1.2e-9 up to 1/2), beyond 1/2 the plain difference, which would lose
 // digits below.  SMALL: no s is above kPolySmall.
 template <bool SMALL>
-__device__ __forceinline__ float one_minus_exp(float s) {
+__device__ __forceinline__ float exp_less_one(float s) {
   if constexpr (SMALL) {
-    float p = __builtin_fmaf(s, 0.007514301221817732f, -0.04149100184440613f);
-    p = __builtin_fmaf(s, p, 0.16665112972259521f);
-    p = __builtin_fmaf(s, p, -0.4999995231628418f);
-    return __builtin_fmaf(s, p, 1.0f) * s;
+    float p = __builtin_fmaf(s, -0.007514301221817732f, 0.04149100184440613f);
+    p = __builtin_fmaf(s, p, -0.16665112972259521f);
+    p = __builtin_fmaf(s, p, 0.4999995231628418f);
+    return __builtin_fmaf(s, p, -1.0f) * s;
   } else {
-    float p = __builtin_fmaf(s, -0.0011237150756642222f, 0.008190003223717213f);
-    p = __builtin_fmaf(s, p, -0.04163024201989174f);
-    p = __builtin_fmaf(s, p, 0.16666245460510254f);
-    p = __builtin_fmaf(s, p, -0.4999998211860657f);
-    p = __builtin_fmaf(s, p, 1.0f) * s;
-    return s > kPolyMax ? 1.0f - exp2_fast(-s * kLog2e) : p;
+    float p = __builtin_fmaf(s, 0.0011237150756642222f, -0.008190003223717213f);
+    p = __builtin_fmaf(s, p, 0.04163024201989174f);
+    p = __builtin_fmaf(s, p, -0.16666245460510254f);
+    p = __builtin_fmaf(s, p, 0.4999998211860657f);
+    p = __builtin_fmaf(s, p, -1.0f) * s;
+    return s > kPolyMax ? exp2_fast(-s * kLog2e) - 1.0f : p;
   }
 }
+// beta = sqrt(1 - a^2).
+__device__ __forceinline__ float beta_of(float n) { return __builtin_amdgcn_sqrtf(-n * (2.0f + n)); }
 
 // softplus(lam) = max(lam, 0) + log(1 + e), e = exp(-|lam|), to a few units over
 // the whole range: log(1 + e) = 2 atanh(z), z = e / (2 + e) <= 1/3, by its series
@@ -82,8 +86,11 @@ __device__ __forceinline__ float softplus_rate(float lam, float sp) {
   return lam < -80.f ? 1.0f : sigmoid_of<true>(lam) / sp;
 }
 
-// s where only s a (and s alone nowhere) is wanted: exp(-200) is 0 in fp32, and
-// a finite s keeps s a at 0.  (A NaN stays one.)
-__device__ __forceinline__ float finite_decay(float s) { return s > 200.f ? 200.f : s; }
+// k = c softplus(lam), so that s = k r; finite, for s a has to come out as 0 where a is.
+// (A NaN stays one.)
+__device__ __forceinline__ float decay_rate(float c, float lam) {
+  const float k = c * softplus_of(lam);
+  return k > 1e30f ? 1e30f : k;
+}
 
 }  // namespace mss

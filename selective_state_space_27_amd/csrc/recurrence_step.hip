@@ -29,9 +29,9 @@ __global__ void __launch_bounds__(256) recurrence_step_kernel(RecurrenceStepPara
     ga = static_cast<const float*>(p.gate_a)[row * p.gate_a_stride + d];
     gx = static_cast<const float*>(p.gate_x)[row * p.gate_x_stride + d];
   }
-  const float k = p.c * softplus_of(p.lam[d]), h = p.h[from * p.dim + d];
-  const float m = one_minus_exp<false>(k * sigmoid_of<!BF16>(ga));
-  const float out = __builtin_fmaf(-m, h, h) + sqrtf(m * (2.0f - m)) * sigmoid_of<!BF16>(gx) * x;
+  const float k = decay_rate(p.c, p.lam[d]), h = p.h[from * p.dim + d];
+  const float n = exp_less_one<false>(k * sigmoid_of<!BF16>(ga));
+  const float out = __builtin_fmaf(n, h, h) + beta_of(n) * sigmoid_of<!BF16>(gx) * x;
   p.h_out[row * p.dim + d] = out;
   if constexpr (BF16) static_cast<uint16_t*>(p.y)[row * p.y_stride + d] = f32_to_bf16(out);
   else static_cast<float*>(p.y)[row * p.y_stride + d] = out;
