@@ -19,7 +19,8 @@ def totals(logits, scores, finished=None, eos=None):
                 out[b, k, eos] = score
             elif not np.any(np.isnan(row)) and row.max() < np.inf and row.max() > -np.inf:
                 top = row.max()
-                out[b, k] = score + (row - (top + np.log(np.sum(np.exp(row - top)))))
+                # (row - top) first: logits may be the lowest value of their type
+                out[b, k] = score + ((row - top) - np.log(np.sum(np.exp(row - top))))
     return out
 
 
