@@ -22,7 +22,7 @@ namespace mss {
 namespace {
 
 constexpr int kThreadsRow = 256, kWavesRow = kThreadsRow / 64;
-constexpr int kThreadsMerge = 512, kWavesMerge = kThreadsMerge / 64;
+constexpr int kHeld = 16;      // totals a thread of the merge holds
 constexpr int kRoom = 512;     // candidates ranked in LDS
 constexpr int kMaxOut = 64;    // n_out
 
@@ -67,11 +67,6 @@ struct Logits {
   static __device__ __forceinline__ int place(int first, int j, int e) {
     return first + (j * kThreadsRow + (int)threadIdx.x) * kVec + e;
   }
-  static __device__ __forceinline__ uint64_t key(const void* row, int place) {
-    const float v = BF16 ? bf16_to_f32(static_cast<const uint16_t*>(row)[BF16 ? place : 0])
-                         : static_cast<const float*>(row)[BF16 ? 0 : place];
-    return key_of(ordered_bits(v), (uint32_t)place);
-  }
   // Past the row's end: -infinity.
   __device__ __forceinline__ void load(const void* row, int first, int vocab) {
 #pragma unroll
@@ -105,7 +100,7 @@ __global__ void __launch_bounds__(kThreadsRow) beam_rows_kernel(BeamArgs a) {
   typedef Logits<BF16, NV> L;
   __shared__ float lds_top[kWavesRow][64], lds_sum[kWavesRow];
   __shared__ uint64_t lds_keys[kRoom];
-  __shared__ int lds_bad[kWavesRow], lds_count, lds_add[kWavesRow];
+  __shared__ int lds_count, lds_add[kWavesRow];
   const BeamSelectParams& p = a.p;
   const int64_t row = blockIdx.y;
   if (p.finished != nullptr && p.finished[row] != 0) return;  // its logits are not looked at
@@ -116,33 +111,23 @@ __global__ void __launch_bounds__(kThreadsRow) beam_rows_kernel(BeamArgs a) {
   l.load(base, first, (int)p.vocab);
 
   float top = -__builtin_inff();
-  bool fine = true;
 #pragma unroll
   for (int j = 0; j < NV; ++j)
 #pragma unroll
-    for (int e = 0; e < L::kVec; ++e) {
-      const float v = l.at(j, e);
-      fine = fine && v < __builtin_inff();
-      top = fmaxf(top, v);
-    }
+    for (int e = 0; e < L::kVec; ++e) top = fmaxf(top, l.at(j, e));
   lds_top[wave][lane] = top;
-  const bool bad = __any(!fine);
-  if (lane == 0) lds_bad[wave] = bad;
   if (threadIdx.x == 0) lds_count = 0;
   __syncthreads();
   float group = lds_top[0][lane];
-  int anybad = lds_bad[0];
 #pragma unroll
-  for (int w = 1; w < kWavesRow; ++w) {
-    group = fmaxf(group, lds_top[w][lane]);
-    anybad |= lds_bad[w];
-  }
+  for (int w = 1; w < kWavesRow; ++w) group = fmaxf(group, lds_top[w][lane]);
   float most = group;
 #pragma unroll
   for (int m = 1; m < 64; m <<= 1) most = fmaxf(most, __shfl_xor(most, m, 64));
   Slice* out = a.slices + row * a.nslices + blockIdx.x;
-  if (anybad || most == -__builtin_inff()) {
-    if (threadIdx.x == 0) *out = Slice{0.0, anybad ? __builtin_inff() : most, 0};
+  // (Where there is a NaN beside infinities the sum below shows it.)
+  if (most == __builtin_inff()) {
+    if (threadIdx.x == 0) *out = Slice{0.0, most, 0};
     return;
   }
   // Sixteen bits of the bound: for bf16 all there are, for fp32 as fine as bf16.
@@ -150,32 +135,31 @@ __global__ void __launch_bounds__(kThreadsRow) beam_rows_kernel(BeamArgs a) {
   if (bound <= kOrderedNegInf) bound = kOrderedNegInf + 1;
   const float least = value_of(bound);
 
+  // A slice of nothing but -infinity: terms of exp(-(lowest - -infinity)) = 0.
+  const float from = fmaxf(most, -3.4028235e38f);
   float sum = 0.0f;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     float part = 0.0f;
 #pragma unroll
-    for (int e = 0; e < L::kVec; ++e) part += exp_neg<true>(most - l.at(j, e));
+    for (int e = 0; e < L::kVec; ++e) part += exp_neg<!BF16>(from - l.at(j, e));
     sum += part;
   }
 #pragma unroll
   for (int m = 1; m < 64; m <<= 1) sum += __shfl_xor(sum, m, 64);
   if (lane == 0) lds_sum[wave] = sum;
 
-  // The few that pass are read again: their registers cannot be indexed.
-  auto keep = [&](uint32_t mask) {
-    for (; mask != 0; mask &= mask - 1) {
-      const int i = __builtin_ctz(mask), at = atomicAdd(&lds_count, 1);
-      if (at < kRoom) lds_keys[at] = L::key(base, L::place(first, i / L::kVec, i % L::kVec));
-    }
+  // Few pass.
+  auto keep = [&](float v, int j, int e) {
+    const int at = atomicAdd(&lds_count, 1);
+    if (at < kRoom) lds_keys[at] = key_of(ordered_bits(v), (uint32_t)L::place(first, j, e));
   };
   if (top >= least) {
-    uint32_t mask = 0;
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
-      for (int e = 0; e < L::kVec; ++e) mask |= (l.at(j, e) >= least ? 1u : 0u) << (j * L::kVec + e);
-    keep(mask);
+      for (int e = 0; e < L::kVec; ++e)
+        if (l.at(j, e) >= least) keep(l.at(j, e), j, e);
   }
   __syncthreads();
   int count = lds_count;
@@ -216,16 +200,13 @@ __global__ void __launch_bounds__(kThreadsRow) beam_rows_kernel(BeamArgs a) {
     }
     if (threadIdx.x == 0) lds_count = 0;
     __syncthreads();
-    uint32_t mask = 0;
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
       for (int e = 0; e < L::kVec; ++e) {
         const uint32_t o = ordered_bits(l.at(j, e));
-        const bool in = o > exact || (o == exact && L::place(first, j, e) <= first + until);
-        mask |= (in ? 1u : 0u) << (j * L::kVec + e);
+        if (o > exact || (o == exact && L::place(first, j, e) <= first + until)) keep(l.at(j, e), j, e);
       }
-    keep(mask);
     __syncthreads();
     count = lds_count;
   }
@@ -234,6 +215,7 @@ __global__ void __launch_bounds__(kThreadsRow) beam_rows_kernel(BeamArgs a) {
   for (int i = threadIdx.x; i < count; i += kThreadsRow) {
     const uint64_t mine = lds_keys[i];
     int rank = 0;
+#pragma unroll 8
     for (int o = 0; o < count; ++o) rank += lds_keys[o] > mine;
     if (rank < n) list[rank * across] = mine;
   }
@@ -241,18 +223,21 @@ __global__ void __launch_bounds__(kThreadsRow) beam_rows_kernel(BeamArgs a) {
     double s = 0.0;
 #pragma unroll
     for (int w = 0; w < kWavesRow; ++w) s += (double)lds_sum[w];
-    *out = Slice{s, most, count < n ? count : n};
+    *out = s == s ? Slice{s, most, count < n ? count : n} : Slice{0.0, __builtin_inff(), 0};
   }
 }
 
-__global__ void __launch_bounds__(kThreadsMerge) beam_merge_kernel(BeamArgs a) {
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) beam_merge_kernel(BeamArgs a) {
+  constexpr int WAVES = THREADS / 64;
   // A beam's totals are base + (logit - top), base = score - log sum exp(logit - top);
   // -infinity: no candidates.  (Not base - top + logit: logits may be the type's lowest.)
-  __shared__ double lds_base[64];
+  __shared__ double lds_base[64], lds_term[THREADS];
   __shared__ float lds_most[64];
-  __shared__ uint64_t lds_best[kWavesMerge][64], lds_keys[kRoom];
+  __shared__ uint32_t lds_top[64];  // ordered bits
+  __shared__ uint64_t lds_best[WAVES][64], lds_keys[kRoom];
   __shared__ uint32_t lds_places[kRoom], lds_out[kMaxOut];
-  __shared__ int lds_count, lds_add[kWavesMerge];
+  __shared__ int lds_count, lds_add[WAVES];
   const BeamSelectParams& p = a.p;
   const int64_t b = blockIdx.x;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -262,36 +247,70 @@ __global__ void __launch_bounds__(kThreadsMerge) beam_merge_kernel(BeamArgs a) {
   const Slice* slices = a.slices + b * beams * a.nslices;
   const uint64_t* lists = a.lists + b * beams * a.nslices * n;
 
-  for (int k = wave; k < beams; k += kWavesMerge) {
-    const float score = scores[k];
-    const bool over = finished != nullptr && finished[k] != 0;
-    float top = -__builtin_inff();
-    if (!over)
+  // A thread looks at one slice, at every step-th rank of its list from r0 on.  What it
+  // reads does not depend on anything read before, so it is all under way at once.
+  const int across = beams * a.nslices, items = across * n;
+  const int step = max(THREADS / across, 1), r0 = (int)threadIdx.x / across, at0 = (int)threadIdx.x - r0 * across;
+  const bool held = across <= THREADS && n <= step * kHeld;  // holds<THREADS>
+  const int k0 = at0 / a.nslices;
+  uint64_t key[kHeld];
+  Slice own{};
+  bool over0 = false;
+  if (held) {
+#pragma unroll
+    for (int j = 0; j < kHeld; ++j)
+      if (j * step < n) key[j] = lists[min(r0 + j * step, n - 1) * across + at0];
+    own = slices[at0];
+    over0 = finished != nullptr && finished[k0] != 0;
+  }
+  const float score = (int)threadIdx.x < beams ? scores[threadIdx.x] : 0.0f;
+  const bool over = (int)threadIdx.x < beams && finished != nullptr && finished[threadIdx.x] != 0;
+  if (threadIdx.x < 64) lds_top[threadIdx.x] = 0;
+  if (threadIdx.x == 0) lds_count = 0;
+  __syncthreads();
+  // Every beam's largest logit, the sum of its slices' sums, its base.
+  if (held) {
+    if (r0 == 0 && !over0) atomicMax(&lds_top[k0], ordered_bits(own.top));
+    __syncthreads();
+    const float top = value_of(lds_top[k0]);
+    if (r0 == 0)
+      lds_term[at0] = !over0 && own.count > 0 && top < __builtin_inff() ? own.sum * exp((double)own.top - (double)top) : 0.0;
+    __syncthreads();
+  } else {
+    for (int k = wave; k < beams; k += WAVES) {
+      float top = -__builtin_inff();
       for (int s = lane; s < a.nslices; s += 64) top = fmaxf(top, slices[k * a.nslices + s].top);
 #pragma unroll
-    for (int m = 1; m < 64; m <<= 1) top = fmaxf(top, __shfl_xor(top, m, 64));
-    double sum = 0.0;
-    if (!over && __builtin_fabsf(top) < __builtin_inff())
+      for (int m = 1; m < 64; m <<= 1) top = fmaxf(top, __shfl_xor(top, m, 64));
+      double sum = 0.0;
       for (int s = lane; s < a.nslices; s += 64) {
         const Slice t = slices[k * a.nslices + s];
-        if (t.count > 0) sum += t.sum * exp((double)t.top - (double)top);
+        if (t.count > 0 && top < __builtin_inff()) sum += t.sum * exp((double)t.top - (double)top);
       }
 #pragma unroll
-    for (int m = 1; m < 64; m <<= 1) sum += __shfl_xor(sum, m, 64);
+      for (int m = 1; m < 64; m <<= 1) sum += __shfl_xor(sum, m, 64);
+      if (lane == 0) lds_top[k] = ordered_bits(top), lds_base[k] = sum;
+    }
+    __syncthreads();
+  }
+  if ((int)threadIdx.x < beams) {
+    const int k = threadIdx.x;
+    double sum = 0.0;
+    if (held)
+      for (int s = 0; s < a.nslices; ++s) sum += lds_term[k * a.nslices + s];
+    else
+      sum = lds_base[k];
+    const float top = value_of(lds_top[k]);
     const bool none = !(score < __builtin_inff()) || score == -__builtin_inff() ||
                       (!over && !(__builtin_fabsf(top) < __builtin_inff()));
-    if (lane == 0) {
-      lds_base[k] = none ? -__builtin_inf() : over ? (double)score : (double)score - log(sum);
-      lds_most[k] = top;
-    }
+    lds_base[k] = none ? -__builtin_inf() : over ? (double)score : (double)score - log(sum);
+    lds_most[k] = top;
   }
-  if (threadIdx.x == 0) lds_count = 0;
   __syncthreads();
 
   // The i-th item: its total's ordered bits (kOrderedNegInf64: no candidate) and
   // place.  In the order of the lists, so that neighbouring threads, whose maxima
   // make the bound, look at the same rank of different slices.
-  const int across = beams * a.nslices, items = across * n;
   auto item = [&](int i, uint32_t& place) -> uint64_t {
     const int rank = i / across, at = i - rank * across, k = at / a.nslices;
     const double base = lds_base[k];
@@ -307,57 +326,68 @@ __global__ void __launch_bounds__(kThreadsMerge) beam_merge_kernel(BeamArgs a) {
     return ordered_bits(base + ((double)value_of((uint32_t)(key >> 32)) - (double)lds_most[k]));
   };
   uint32_t place;
-  uint64_t best = kOrderedNegInf64;
-  for (int i = threadIdx.x; i < items; i += kThreadsMerge) {
-    const uint64_t o = item(i, place);
-    best = o > best ? o : best;
-  }
-  lds_best[wave][lane] = best;
-  __syncthreads();
+  auto keep = [&](uint64_t o, uint32_t at) {
+    const int to = atomicAdd(&lds_count, 1);
+    if (to < kRoom) lds_keys[to] = o, lds_places[to] = at;
+  };
+  if (held) {
+    const double base = lds_base[k0], most = (double)lds_most[k0];
+    const bool none = r0 >= step || base == -__builtin_inf();
+    uint64_t o[kHeld], best = kOrderedNegInf64;
 #pragma unroll
-  for (int w = 0; w < kWavesMerge; ++w) best = lds_best[w][lane] > best ? lds_best[w][lane] : best;
-  uint64_t bound = wave_threshold<32>(best, n);
-  if (bound <= kOrderedNegInf64) bound = kOrderedNegInf64 + 1;
-  for (int i = threadIdx.x; i < items; i += kThreadsMerge) {
-    const uint64_t o = item(i, place);
-    if (o >= bound) {
-      const int at = atomicAdd(&lds_count, 1);
-      if (at < kRoom) lds_keys[at] = o, lds_places[at] = place;
+    for (int j = 0; j < kHeld; ++j) {
+      o[j] = kOrderedNegInf64;
+      if (j * step >= n) continue;
+      const int r = r0 + j * step;
+      if (over0) key[j] = key_of(0, (uint32_t)p.eos);
+      const double total = over0 ? base : base + ((double)value_of((uint32_t)(key[j] >> 32)) - most);
+      if (!none && (over0 ? r == 0 && at0 == k0 * a.nslices : r < own.count && r < n)) o[j] = ordered_bits(total);
+      best = o[j] > best ? o[j] : best;
     }
+    lds_best[wave][lane] = best;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) best = lds_best[w][lane] > best ? lds_best[w][lane] : best;
+    uint64_t bound = (uint64_t)wave_threshold<32>((uint32_t)(best >> 32), n) << 32;
+    if (bound <= kOrderedNegInf64) bound = kOrderedNegInf64 + 1;
+#pragma unroll
+    for (int j = 0; j < kHeld; ++j)
+      if (o[j] >= bound) keep(o[j], (uint32_t)k0 * vocab + place_of(key[j]));
+  } else if (threadIdx.x == 0) {
+    lds_count = kRoom + 1;
   }
   __syncthreads();
   int count = lds_count;
-  if (count > kRoom) {  // as above
+  if (count > kRoom) {  // as above, reading the lists each time
     uint64_t exact = 0;
     bool tied = true;
     for (int bit = 63; bit >= 0 && tied; --bit) {
       const uint64_t with = exact | 1ull << bit;
       int c = 0;
-      for (int i = threadIdx.x; i < items; i += kThreadsMerge) c += item(i, place) >= with;
-      c = block_sum<kWavesMerge>(c, lds_add);
+      for (int i = threadIdx.x; i < items; i += THREADS) c += item(i, place) >= with;
+      c = block_sum<WAVES>(c, lds_add);
       if (c >= n) exact = with, tied = c > kRoom;
     }
+    // (Fewer than n candidates: all of them, and none of what is not one.)
+    if (exact <= kOrderedNegInf64) exact = kOrderedNegInf64 + 1, tied = false;
     uint32_t until = ~0u;
     if (tied) {
       int above = 0;
-      for (int i = threadIdx.x; i < items; i += kThreadsMerge) above += item(i, place) > exact;
-      above = block_sum<kWavesMerge>(above, lds_add);
+      for (int i = threadIdx.x; i < items; i += THREADS) above += item(i, place) > exact;
+      above = block_sum<WAVES>(above, lds_add);
       until = 0;
       for (int bit = 30; bit >= 0; --bit) {
         const uint32_t with = until | 1u << bit;
         int c = 0;
-        for (int i = threadIdx.x; i < items; i += kThreadsMerge) c += item(i, place) == exact && place < with;
-        if (block_sum<kWavesMerge>(c, lds_add) < n - above) until = with;
+        for (int i = threadIdx.x; i < items; i += THREADS) c += item(i, place) == exact && place < with;
+        if (block_sum<WAVES>(c, lds_add) < n - above) until = with;
       }
     }
     if (threadIdx.x == 0) lds_count = 0;
     __syncthreads();
-    for (int i = threadIdx.x; i < items; i += kThreadsMerge) {
+    for (int i = threadIdx.x; i < items; i += THREADS) {
       const uint64_t o = item(i, place);
-      if (o > exact || (o == exact && place <= until)) {
-        const int at = atomicAdd(&lds_count, 1);
-        if (at < kRoom) lds_keys[at] = o, lds_places[at] = place;
-      }
+      if (o > exact || (o == exact && place <= until)) keep(o, place);
     }
     __syncthreads();
     count = lds_count;
@@ -371,13 +401,17 @@ __global__ void __launch_bounds__(kThreadsMerge) beam_merge_kernel(BeamArgs a) {
     if (p.out_finished != nullptr) p.out_finished[o] = token == p.eos || (finished != nullptr && finished[parent] != 0);
   };
   const int found = count < n ? count : n;
-  for (int i = threadIdx.x; i < count; i += kThreadsMerge) {
+  for (int i = threadIdx.x; i < count; i += THREADS) {
     const uint64_t mine = lds_keys[i];
     const uint32_t at = lds_places[i];
     int rank = 0;
-    for (int o = 0; o < count; ++o) rank += lds_keys[o] > mine || (lds_keys[o] == mine && lds_places[o] < at);
-    if (rank < n) put(rank, (float)value_of(mine), at);
-    if (rank < n) lds_out[rank] = at;
+#pragma unroll 8
+    for (int o = 0; o < count; ++o) {
+      const uint64_t other = lds_keys[o];
+      const uint32_t where = lds_places[o];
+      rank += (other > mine) | ((other == mine) & (where < at));
+    }
+    if (rank < n) put(rank, (float)value_of(mine), at), lds_out[rank] = at;
   }
   if (found == n) return;
   // Fewer candidates than asked for: all are listed, the others follow in order of place.
@@ -393,6 +427,10 @@ __global__ void __launch_bounds__(kThreadsMerge) beam_merge_kernel(BeamArgs a) {
     if (!taken && rank < n - found) put(found + rank, -__builtin_inff(), threadIdx.x);
   }
 }
+
+// 256 threads where they hold the lists, whose barriers take less time.
+template <int THREADS>
+bool holds(int64_t across, int64_t n) { return across <= THREADS && n <= THREADS / across * kHeld; }
 
 // Slices of 8192 logits where they fill the card twice; else of 2048, for the time
 // that a workgroup takes for its slice.
@@ -428,7 +466,10 @@ hipError_t launch_beam_select(const BeamSelectParams& p, hipStream_t stream) {
   else wide ? launch_rows<false, 8>(a, stream) : launch_rows<false, 2>(a, stream);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(beam_merge_kernel, dim3((unsigned)p.batch), dim3(kThreadsMerge), 0, stream, a);
+  if (holds<256>(p.beams * a.nslices, p.n_out))
+    hipLaunchKernelGGL(beam_merge_kernel<256>, dim3((unsigned)p.batch), dim3(256), 0, stream, a);
+  else
+    hipLaunchKernelGGL(beam_merge_kernel<1024>, dim3((unsigned)p.batch), dim3(1024), 0, stream, a);
   return hipGetLastError();
 }
 

@@ -620,7 +620,7 @@ hipError_t start_chain(const Cut& c, void* workspace, Chain& chain, hipStream_t 
   chain.ticket = chain.status + 1;
   chain.own = reinterpret_cast<uint64_t*>(base + c.own);
   chain.end = reinterpret_cast<float*>(base + c.end);
-  const int64_t n = (int64_t)(c.bytes / 16), groups = (n + 1023) / 1024;
+  const int64_t n = (int64_t)(c.bytes / 16), groups = (n + 255) / 256;
   hipLaunchKernelGGL(chain_clear_kernel, dim3((unsigned)(groups < 2048 ? groups : 2048)), dim3(256), 0, stream,
                      reinterpret_cast<u32x4*>(base), n);
   return hipGetLastError();
@@ -646,8 +646,10 @@ size_t bwd_part_offset(const Cut& c) { return (c.bytes + 255) / 256 * 256; }
 template <bool BF16, int V>
 hipError_t launch_bwd(const RecurrenceBwdParams& p, hipStream_t stream) {
   const Cut c = cut_of(p.batch, p.seqlen, p.dim, V, kRecurrenceChunk);
-  BwdArgs a{p, {}, reinterpret_cast<float*>(static_cast<char*>(p.workspace) + bwd_part_offset(c)), (int)c.blocks,
-            c.pieces};
+  // One piece of one row writes dlam itself.
+  const int64_t parts = p.batch * c.pieces;
+  float* part = reinterpret_cast<float*>(static_cast<char*>(p.workspace) + bwd_part_offset(c));
+  BwdArgs a{p, {}, parts > 1 ? part : p.dlam, (int)c.blocks, c.pieces};
   hipError_t e = start_chain(c, p.workspace, a.chain, stream);
   if (e != hipSuccess) return e;
   const auto kernel = p.starts != nullptr ? recurrence_bwd_kernel<BF16, V, kWaves, kBwdSteps, true>
@@ -655,11 +657,11 @@ hipError_t launch_bwd(const RecurrenceBwdParams& p, hipStream_t stream) {
   hipLaunchKernelGGL(kernel, dim3((unsigned)(c.streams * c.pieces)), dim3(kWaves * 64),
                      2 * kRecurrenceChunk * 64 * V * sizeof(float), stream, a);
   e = hipGetLastError();
-  if (e != hipSuccess) return e;
+  if (e != hipSuccess || parts == 1) return e;
   SumPartialsArgs s{};
   s.part = a.part;
   s.dweight = p.dlam;
-  s.nparts = p.batch * c.pieces;
+  s.nparts = parts;
   s.cols = p.dim;
   s.nout = 1;
   return launch_sum_partials(s, stream);
