@@ -11,6 +11,7 @@ import torch
 import selective_state_space_27_amd as _mss
 
 from .norms import _code, _on, _rows, _workspace_size
+from .recurrence import _address, _state
 
 
 def beam_select(logits, scores, n_out=None, *, finished=None, eos=None, stream=None):
@@ -36,7 +37,7 @@ def beam_select(logits, scores, n_out=None, *, finished=None, eos=None, stream=N
     lp, ls = _rows(logits, "logits", logits.shape, logits.dtype, dev)
     if scores is None:
         raise TypeError("scores must be a torch.Tensor")
-    _mss._check(scores, "scores", (batch, beams), torch.float32, dev)
+    sp = _state(scores, "scores", (batch, beams), dev)
     if finished is not None:
         _mss._check(finished, "finished", (batch, beams),
                     torch.uint8 if finished.dtype == torch.uint8 else torch.bool, dev)
@@ -54,8 +55,8 @@ def beam_select(logits, scores, n_out=None, *, finished=None, eos=None, stream=N
         tokens = torch.empty_like(parents)
         done = torch.empty((batch, n), dtype=torch.bool, device=dev) if eos is not None else None
         ws = torch.empty(need, dtype=torch.uint8, device=dev)
-        st = _mss.lib().mss_beam_select(lp, ls, scores.data_ptr(), _mss._ptr(finished), -1 if eos is None else eos,
-                                        best.data_ptr(), parents.data_ptr(), tokens.data_ptr(), _mss._ptr(done), batch,
+        st = _mss.lib().mss_beam_select(lp, ls, sp, _address(finished), -1 if eos is None else eos,
+                                        best.data_ptr(), parents.data_ptr(), tokens.data_ptr(), _address(done), batch,
                                         beams, vocab, n, io, 0, ws.data_ptr(), need, handle)
     _mss._raise(st, "mss_beam_select")
     return (best, parents, tokens) if done is None else (best, parents, tokens, done)

@@ -29,17 +29,34 @@ constexpr uint64_t kOrderedNegInf64 = 0x000fffffffffffffull;
 __device__ __forceinline__ uint64_t key_of(uint32_t ordered, uint32_t place) { return (uint64_t)ordered << 32 | ~place; }
 __device__ __forceinline__ uint32_t place_of(uint64_t key) { return ~(uint32_t)key; }
 
-// The largest prefix of BITS bits such that at least `want` of the wave's 64 lanes
-// hold a value not below it (0 where fewer hold one above 0).
-template <int BITS, typename T>
-__device__ __forceinline__ T wave_threshold(T mine, int want) {
-  T t = 0;
+// The largest prefix of BITS bits such that at least `want` of the values that the
+// wave's lanes hold, G each, are not below it (0 where fewer are above 0).
+template <int BITS, int G>
+__device__ __forceinline__ uint32_t wave_threshold(const uint32_t (&mine)[G], int want) {
+  uint32_t t = 0;
+  for (int b = 31; b >= 32 - BITS; --b) {
+    const uint32_t with = t | 1u << b;
+    int c = 0;
 #pragma unroll
-  for (int b = 8 * (int)sizeof(T) - 1; b >= 8 * (int)sizeof(T) - BITS; --b) {
-    const T with = t | ((T)1 << b);
-    if (__popcll(__ballot(mine >= with)) >= want) t = with;
+    for (int g = 0; g < G; ++g) c += (int)__popcll(__ballot(mine[g] >= with));
+    if (c >= want) t = with;
   }
   return t;
 }
+// The same of the values v[W][64] in LDS, each lane's largest alone where that is
+// enough: of 64 values the want-th largest is a good bound for up to 32, the least of
+// them a poor one for 64.
+template <int BITS, int W>
+__device__ __forceinline__ uint32_t lds_threshold(const uint32_t (*v)[64], bool all, int want) {
+  uint32_t mine[W], most[1];
+#pragma unroll
+  for (int w = 0; w < W; ++w) mine[w] = v[w][threadIdx.x & 63];
+  if (all) return wave_threshold<BITS, W>(mine, want);
+  most[0] = mine[0];
+#pragma unroll
+  for (int w = 1; w < W; ++w) most[0] = max(most[0], mine[w]);
+  return wave_threshold<BITS, 1>(most, want);
+}
+constexpr int kLanesEnough = 32;
 
 }  // namespace mss

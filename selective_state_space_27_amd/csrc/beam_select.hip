@@ -7,8 +7,8 @@
 // beam can differ by one unit of a logit near zero while their totals are tens)
 // and takes the best.
 //
-// The best n of many, in either launch: the threads' maxima, the 64 lanes' over
-// all waves, give a bound that at least n candidates are not below, and few
+// The best n of many, in either launch: the threads' maxima (for n up to 32 the 64
+// lanes' over all waves) give a bound that at least n candidates are not below, and few
 // others (with 8192 logits and n = 16 some 20); those go to LDS and are ranked
 // there, each by counting what comes before it.  Where more pass than there is room
 // for (ties, a sorted row), the bound is raised by bisection first, and among equals
@@ -23,7 +23,9 @@ namespace {
 
 constexpr int kThreadsRow = 256, kWavesRow = kThreadsRow / 64;
 constexpr int kHeld = 16;      // totals a thread of the merge holds
-constexpr int kRoom = 512;     // candidates ranked in LDS
+// Candidates ranked in LDS; more are narrowed down first (which takes as long as
+// ranking about as many).
+constexpr int kRoom = 512, kRoomMerge = 1024;
 constexpr int kMaxOut = 64;    // n_out
 
 struct Slice {
@@ -38,6 +40,18 @@ struct BeamArgs {
   uint64_t* lists;  // [batch][n_out][beams][nslices]: every slice's best, every slice's second, ..
   int nslices;
 };
+
+// Maximum over the wave's lanes, which every one of them gets.
+__device__ __forceinline__ float lanes_max(float v) {
+  v = fmaxf(v, dpp_f32<kDppXor1>(v));
+  v = fmaxf(v, dpp_f32<kDppXor2>(v));
+  v = fmaxf(v, dpp_f32<kDppHalfMirror>(v));
+  v = fmaxf(v, dpp_f32<kDppMirror>(v));
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  const auto q = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(q[0]), __uint_as_float(q[1]));
+}
 
 // Sum over the workgroup, in a fixed order; every thread gets it.  `lds` is free
 // to be written when the call begins, and again after the next barrier.
@@ -98,7 +112,8 @@ struct Logits {
 template <bool BF16, int NV>
 __global__ void __launch_bounds__(kThreadsRow) beam_rows_kernel(BeamArgs a) {
   typedef Logits<BF16, NV> L;
-  __shared__ float lds_top[kWavesRow][64], lds_sum[kWavesRow];
+  __shared__ uint32_t lds_top[kWavesRow][64];  // ordered bits
+  __shared__ float lds_sum[kWavesRow];
   __shared__ uint64_t lds_keys[kRoom];
   __shared__ int lds_count, lds_add[kWavesRow];
   const BeamSelectParams& p = a.p;
@@ -115,15 +130,13 @@ __global__ void __launch_bounds__(kThreadsRow) beam_rows_kernel(BeamArgs a) {
   for (int j = 0; j < NV; ++j)
 #pragma unroll
     for (int e = 0; e < L::kVec; ++e) top = fmaxf(top, l.at(j, e));
-  lds_top[wave][lane] = top;
+  lds_top[wave][lane] = ordered_bits(top);
   if (threadIdx.x == 0) lds_count = 0;
   __syncthreads();
-  float group = lds_top[0][lane];
+  uint32_t group = lds_top[0][lane];
 #pragma unroll
-  for (int w = 1; w < kWavesRow; ++w) group = fmaxf(group, lds_top[w][lane]);
-  float most = group;
-#pragma unroll
-  for (int m = 1; m < 64; m <<= 1) most = fmaxf(most, __shfl_xor(most, m, 64));
+  for (int w = 1; w < kWavesRow; ++w) group = max(group, lds_top[w][lane]);
+  const float most = lanes_max(value_of(group));
   Slice* out = a.slices + row * a.nslices + blockIdx.x;
   // (Where there is a NaN beside infinities the sum below shows it.)
   if (most == __builtin_inff()) {
@@ -131,7 +144,7 @@ __global__ void __launch_bounds__(kThreadsRow) beam_rows_kernel(BeamArgs a) {
     return;
   }
   // Sixteen bits of the bound: for bf16 all there are, for fp32 as fine as bf16.
-  uint32_t bound = wave_threshold<16>(ordered_bits(group), n);
+  uint32_t bound = lds_threshold<16, kWavesRow>(lds_top, n > kLanesEnough, n);
   if (bound <= kOrderedNegInf) bound = kOrderedNegInf + 1;
   const float least = value_of(bound);
 
@@ -145,8 +158,7 @@ __global__ void __launch_bounds__(kThreadsRow) beam_rows_kernel(BeamArgs a) {
     for (int e = 0; e < L::kVec; ++e) part += exp_neg<!BF16>(from - l.at(j, e));
     sum += part;
   }
-#pragma unroll
-  for (int m = 1; m < 64; m <<= 1) sum += __shfl_xor(sum, m, 64);
+  sum = lanes_sum<64>(sum);
   if (lane == 0) lds_sum[wave] = sum;
 
   // Few pass.
@@ -235,8 +247,10 @@ __global__ void __launch_bounds__(THREADS) beam_merge_kernel(BeamArgs a) {
   __shared__ double lds_base[64], lds_term[THREADS];
   __shared__ float lds_most[64];
   __shared__ uint32_t lds_top[64];  // ordered bits
-  __shared__ uint64_t lds_best[WAVES][64], lds_keys[kRoom];
-  __shared__ uint32_t lds_places[kRoom], lds_out[kMaxOut];
+  __shared__ int lds_over[64];
+  __shared__ uint64_t lds_keys[kRoomMerge];
+  __shared__ uint32_t lds_best[WAVES][64];  // the upper halves
+  __shared__ uint32_t lds_places[kRoomMerge], lds_out[kMaxOut];
   __shared__ int lds_count, lds_add[WAVES];
   const BeamSelectParams& p = a.p;
   const int64_t b = blockIdx.x;
@@ -280,8 +294,7 @@ __global__ void __launch_bounds__(THREADS) beam_merge_kernel(BeamArgs a) {
     for (int k = wave; k < beams; k += WAVES) {
       float top = -__builtin_inff();
       for (int s = lane; s < a.nslices; s += 64) top = fmaxf(top, slices[k * a.nslices + s].top);
-#pragma unroll
-      for (int m = 1; m < 64; m <<= 1) top = fmaxf(top, __shfl_xor(top, m, 64));
+      top = lanes_max(top);
       double sum = 0.0;
       for (int s = lane; s < a.nslices; s += 64) {
         const Slice t = slices[k * a.nslices + s];
@@ -305,6 +318,7 @@ __global__ void __launch_bounds__(THREADS) beam_merge_kernel(BeamArgs a) {
                       (!over && !(__builtin_fabsf(top) < __builtin_inff()));
     lds_base[k] = none ? -__builtin_inf() : over ? (double)score : (double)score - log(sum);
     lds_most[k] = top;
+    lds_over[k] = over;
   }
   __syncthreads();
 
@@ -313,27 +327,24 @@ __global__ void __launch_bounds__(THREADS) beam_merge_kernel(BeamArgs a) {
   // make the bound, look at the same rank of different slices.
   auto item = [&](int i, uint32_t& place) -> uint64_t {
     const int rank = i / across, at = i - rank * across, k = at / a.nslices;
-    const double base = lds_base[k];
-    place = 0;
-    if (base == -__builtin_inf()) return kOrderedNegInf64;
-    if (finished != nullptr && finished[k] != 0) {
-      place = (uint32_t)k * vocab + (uint32_t)p.eos;
-      return rank == 0 && at == k * a.nslices ? ordered_bits(base) : kOrderedNegInf64;
-    }
-    if (rank >= slices[at].count) return kOrderedNegInf64;
     const uint64_t key = lists[i];
-    place = (uint32_t)k * vocab + place_of(key);
-    return ordered_bits(base + ((double)value_of((uint32_t)(key >> 32)) - (double)lds_most[k]));
+    const int listed = slices[at].count;
+    const double base = lds_base[k];
+    const bool over = lds_over[k] != 0;
+    place = (uint32_t)k * vocab + (over ? (uint32_t)p.eos : place_of(key));
+    const bool is = base != -__builtin_inf() && (over ? rank == 0 && at == k * a.nslices : rank < listed);
+    const double total = over ? base : base + ((double)value_of((uint32_t)(key >> 32)) - (double)lds_most[k]);
+    return is ? ordered_bits(total) : kOrderedNegInf64;
   };
   uint32_t place;
   auto keep = [&](uint64_t o, uint32_t at) {
     const int to = atomicAdd(&lds_count, 1);
-    if (to < kRoom) lds_keys[to] = o, lds_places[to] = at;
+    if (to < kRoomMerge) lds_keys[to] = o, lds_places[to] = at;
   };
+  uint64_t o[kHeld], best = kOrderedNegInf64;
   if (held) {
     const double base = lds_base[k0], most = (double)lds_most[k0];
     const bool none = r0 >= step || base == -__builtin_inf();
-    uint64_t o[kHeld], best = kOrderedNegInf64;
 #pragma unroll
     for (int j = 0; j < kHeld; ++j) {
       o[j] = kOrderedNegInf64;
@@ -344,21 +355,31 @@ __global__ void __launch_bounds__(THREADS) beam_merge_kernel(BeamArgs a) {
       if (!none && (over0 ? r == 0 && at0 == k0 * a.nslices : r < own.count && r < n)) o[j] = ordered_bits(total);
       best = o[j] > best ? o[j] : best;
     }
-    lds_best[wave][lane] = best;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < WAVES; ++w) best = lds_best[w][lane] > best ? lds_best[w][lane] : best;
-    uint64_t bound = (uint64_t)wave_threshold<32>((uint32_t)(best >> 32), n) << 32;
-    if (bound <= kOrderedNegInf64) bound = kOrderedNegInf64 + 1;
+  } else {
+#pragma unroll 4
+    for (int i = threadIdx.x; i < items; i += THREADS) {
+      const uint64_t t = item(i, place);
+      best = t > best ? t : best;
+    }
+  }
+  lds_best[wave][lane] = (uint32_t)(best >> 32);
+  __syncthreads();
+  uint64_t bound = (uint64_t)lds_threshold<32, WAVES>(lds_best, !held || n > kLanesEnough, n) << 32;
+  if (bound <= kOrderedNegInf64) bound = kOrderedNegInf64 + 1;
+  if (held) {
 #pragma unroll
     for (int j = 0; j < kHeld; ++j)
       if (o[j] >= bound) keep(o[j], (uint32_t)k0 * vocab + place_of(key[j]));
-  } else if (threadIdx.x == 0) {
-    lds_count = kRoom + 1;
+  } else {
+#pragma unroll 4
+    for (int i = threadIdx.x; i < items; i += THREADS) {
+      const uint64_t t = item(i, place);
+      if (t >= bound) keep(t, place);
+    }
   }
   __syncthreads();
   int count = lds_count;
-  if (count > kRoom) {  // as above, reading the lists each time
+  if (count > kRoomMerge) {  // as for a row, reading the lists each time
     uint64_t exact = 0;
     bool tied = true;
     for (int bit = 63; bit >= 0 && tied; --bit) {
@@ -366,7 +387,7 @@ __global__ void __launch_bounds__(THREADS) beam_merge_kernel(BeamArgs a) {
       int c = 0;
       for (int i = threadIdx.x; i < items; i += THREADS) c += item(i, place) >= with;
       c = block_sum<WAVES>(c, lds_add);
-      if (c >= n) exact = with, tied = c > kRoom;
+      if (c >= n) exact = with, tied = c > kRoomMerge;
     }
     // (Fewer than n candidates: all of them, and none of what is not one.)
     if (exact <= kOrderedNegInf64) exact = kOrderedNegInf64 + 1, tied = false;

@@ -31,7 +31,15 @@ def _sequences(x, name):
 
 def _state(t, name, shape, device):
     """Pointer of a dense float32 tensor, or None."""
-    _mss._check(t, name, shape, torch.float32, device)
+    if t is None:
+        return None
+    if not (isinstance(t, torch.Tensor) and t.dtype == torch.float32 and t.shape == shape and t.device == device and
+            t.is_contiguous()):
+        _mss._check(t, name, shape, torch.float32, device)
+    return t.data_ptr()
+
+
+def _address(t):
     return None if t is None else t.data_ptr()
 
 
@@ -76,8 +84,8 @@ def gated_recurrence_fwd(x, gate_a, gate_x, lam, *, c=8.0, h0=None, starts=None,
         if need == 0:
             _mss._raise(2, "gated_recurrence_fwd")
         ws = torch.empty(need, dtype=torch.uint8, device=dev)
-        st = _mss.lib().mss_gated_recurrence_fwd(xp, xs, ap, as_, ip, is_, lp, c, hp, sp, op, os, _mss._ptr(last),
-                                                 _mss._ptr(states), b, length, dim, io, 0, ws.data_ptr(), need, handle)
+        st = _mss.lib().mss_gated_recurrence_fwd(xp, xs, ap, as_, ip, is_, lp, c, hp, sp, op, os, _address(last),
+                                                 _address(states), b, length, dim, io, 0, ws.data_ptr(), need, handle)
         _mss._raise(st, "mss_gated_recurrence_fwd")
         if check_waits:
             _mss._check_waits(ws, stream, "mss_gated_recurrence_fwd")
@@ -117,7 +125,7 @@ def gated_recurrence_bwd(dy, x, gate_a, gate_x, lam, states, *, c=8.0, starts=No
             _mss._raise(2, "gated_recurrence_bwd")
         ws = torch.empty(need, dtype=torch.uint8, device=dev)
         st = _mss.lib().mss_gated_recurrence_bwd(dp, ds, xp, xs, ap, as_, ip, is_, lp, c, sp, tp, hp, dxp, dxs, dap, das,
-                                                 dip, dis, dlam.data_ptr(), _mss._ptr(dh0), b, length, dim, io, 0,
+                                                 dip, dis, dlam.data_ptr(), _address(dh0), b, length, dim, io, 0,
                                                  ws.data_ptr(), need, handle)
         _mss._raise(st, "mss_gated_recurrence_bwd")
         if check_waits:
