@@ -222,7 +222,9 @@ struct WavePlace {
   uint32_t in, out;  // its offset in a row for loads, and for stores
 };
 
-// `piece` in order along time; a lane past the last channel repeats it.
+// `piece` in order along time.  A lane past the last channel repeats it, and so does
+// one with half a pair, as the second of the last two: what two lanes write there is
+// the same.
 template <bool BF16, int V, int W, int T>
 __device__ __forceinline__ WavePlace<V, W, T> wave_place(int64_t id, int streams, int blocks, int64_t pieces,
                                                          bool reversed, int64_t seqlen, int64_t dim) {
@@ -237,18 +239,17 @@ __device__ __forceinline__ WavePlace<V, W, T> wave_place(int64_t id, int streams
   w.n = left < 0 ? 0 : left < T ? __builtin_amdgcn_readfirstlane((int)left) : T;
   const int64_t c = (int64_t)(w.stream - (int)w.b * blocks) * (64 * V) + (threadIdx.x & 63) * V;
   w.ok = c < dim;
-  w.ch = (uint32_t)(w.ok ? c : dim - V);
+  w.ch = (uint32_t)(c + V <= dim ? c : dim - V);
   w.in = w.ch * (BF16 ? 2u : 4u);
   w.out = w.ok ? w.in : kOffNone;
   return w;
 }
 
-// Bit j: a sequence starts at the wave's step j.
-template <int T>
-__device__ __forceinline__ uint64_t start_bits(const uint8_t* starts, int64_t row, int n) {
-  if (starts == nullptr) return 0;
+// Whether a sequence starts at the wave's step `lane` (the load comes before the
+// rows', so that it is not waited for behind them); bit j of the wave's: at step j.
+__device__ __forceinline__ uint32_t start_mark(const uint8_t* starts, int64_t row, int n) {
   const int lane = threadIdx.x & 63;
-  return __ballot(lane < n && starts[row + (lane < n ? lane : 0)] != 0);
+  return lane < n ? starts[row + lane] : 0u;
 }
 
 // Bit i: a sequence starts in wave i's steps.
@@ -313,6 +314,7 @@ __global__ void __launch_bounds__(W * 64) __attribute__((amdgpu_waves_per_eu(4))
   const int lane = threadIdx.x & 63;
   const int64_t row0 = w.b * p.seqlen + w.t0;
 
+  const uint32_t mark = STARTS ? start_mark(p.starts, row0, w.n) : 0u;
   float lam[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) lam[v] = p.lam[w.ch + v];
@@ -320,7 +322,7 @@ __global__ void __launch_bounds__(W * 64) __attribute__((amdgpu_waves_per_eu(4))
   load_rows<BF16, V, T>(Rows<BF16>(p.gate_a, row0, p.gate_a_stride, p.dim), w.in, w.n, kClosed<BF16>, ra);
   load_rows<BF16, V, T>(Rows<BF16>(p.gate_x, row0, p.gate_x_stride, p.dim), w.in, w.n, kClosed<BF16>, ri);
   load_rows<BF16, V, T>(Rows<BF16>(p.x, row0, p.x_stride, p.dim), w.in, w.n, 0u, rx);
-  const uint64_t starts = STARTS ? start_bits<T>(p.starts, row0, w.n) : 0;
+  const uint64_t starts = STARTS ? __ballot(mark != 0) : 0;
   float k[V];
   bool slow = true;
 #pragma unroll
@@ -436,6 +438,7 @@ __global__ void __launch_bounds__(W * 64) __attribute__((amdgpu_waves_per_eu(4))
   const int lane = threadIdx.x & 63;
   const int64_t row0 = w.b * p.seqlen + w.t0, piece = a.pieces - 1 - w.place;
 
+  const uint32_t mark = STARTS ? start_mark(p.starts, row0, w.n) : 0u;
   float lam[V], before[V];  // before: the state entering the piece, then this wave's steps
 #pragma unroll
   for (int v = 0; v < V; ++v) {
@@ -447,7 +450,7 @@ __global__ void __launch_bounds__(W * 64) __attribute__((amdgpu_waves_per_eu(4))
   load_rows<BF16, V, T>(Rows<BF16>(p.gate_x, row0, p.gate_x_stride, p.dim), w.in, w.n, kClosed<BF16>, ri);
   load_rows<BF16, V, T>(Rows<BF16>(p.x, row0, p.x_stride, p.dim), w.in, w.n, 0u, rx);
   load_rows<BF16, V, T>(Rows<BF16>(p.dy, row0, p.dy_stride, p.dim), w.in, w.n, 0u, rd);
-  const uint64_t starts = STARTS ? start_bits<T>(p.starts, row0, w.n) : 0;
+  const uint64_t starts = STARTS ? __ballot(mark != 0) : 0;
   float k[V];
   bool slow = true;
 #pragma unroll
@@ -626,8 +629,10 @@ hipError_t start_chain(const Cut& c, void* workspace, Chain& chain, hipStream_t 
   return hipGetLastError();
 }
 
-// Two bf16 channels a lane need rows of whole words.
-bool pairs(const void* p, int64_t stride) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0 && stride % 2 == 0; }
+// bf16 channels go in pairs, a word a lane, which the hardware reads and writes at any
+// alignment (at odd ones, 3 x 4099 x 1001, 39 us forward and 61 us backward, against 43
+// and 70 with one channel a lane); a row of one channel has none.
+bool in_pairs(int64_t dim, bool bf16) { return bf16 && dim > 1; }
 
 template <bool BF16, int V>
 hipError_t launch_fwd(const RecurrenceFwdParams& p, hipStream_t stream) {
@@ -669,32 +674,23 @@ hipError_t launch_bwd(const RecurrenceBwdParams& p, hipStream_t stream) {
 
 }  // namespace
 
-// Whether channels go in pairs depends on the call's addresses: room for either.
 size_t recurrence_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, bool bf16) {
-  const size_t one = cut_of(batch, seqlen, dim, 1, kWaves * kFwdSteps).bytes;
-  const size_t two = bf16 ? cut_of(batch, seqlen, dim, 2, kWaves * kFwdSteps).bytes : 0;
-  return one > two ? one : two;
+  return cut_of(batch, seqlen, dim, in_pairs(dim, bf16) ? 2 : 1, kWaves * kFwdSteps).bytes;
 }
 
 hipError_t launch_recurrence_fwd(const RecurrenceFwdParams& p, hipStream_t stream) {
   if (!p.bf16) return launch_fwd<false, 1>(p, stream);
-  const bool two = p.dim % 2 == 0 && pairs(p.x, p.x_stride) && pairs(p.gate_a, p.gate_a_stride) &&
-                   pairs(p.gate_x, p.gate_x_stride) && pairs(p.y, p.y_stride);
-  return two ? launch_fwd<true, 2>(p, stream) : launch_fwd<true, 1>(p, stream);
+  return in_pairs(p.dim, true) ? launch_fwd<true, 2>(p, stream) : launch_fwd<true, 1>(p, stream);
 }
 
 size_t recurrence_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, bool bf16) {
-  const Cut one = cut_of(batch, seqlen, dim, 1, kRecurrenceChunk), two = cut_of(batch, seqlen, dim, 2, kRecurrenceChunk);
-  const size_t a = bwd_part_offset(one), b = bf16 ? bwd_part_offset(two) : 0;
-  return (a > b ? a : b) + (size_t)(batch * one.pieces * dim) * sizeof(float);
+  const Cut c = cut_of(batch, seqlen, dim, in_pairs(dim, bf16) ? 2 : 1, kRecurrenceChunk);
+  return bwd_part_offset(c) + (size_t)(batch * c.pieces * dim) * sizeof(float);
 }
 
 hipError_t launch_recurrence_bwd(const RecurrenceBwdParams& p, hipStream_t stream) {
   if (!p.bf16) return launch_bwd<false, 1>(p, stream);
-  const bool two = p.dim % 2 == 0 && pairs(p.dy, p.dy_stride) && pairs(p.x, p.x_stride) &&
-                   pairs(p.gate_a, p.gate_a_stride) && pairs(p.gate_x, p.gate_x_stride) && pairs(p.dx, p.dx_stride) &&
-                   pairs(p.dgate_a, p.dgate_a_stride) && pairs(p.dgate_x, p.dgate_x_stride);
-  return two ? launch_bwd<true, 2>(p, stream) : launch_bwd<true, 1>(p, stream);
+  return in_pairs(p.dim, true) ? launch_bwd<true, 2>(p, stream) : launch_bwd<true, 1>(p, stream);
 }
 
 }  // namespace mss
