@@ -741,7 +741,8 @@ mss_status mss_gated_recurrence_step(const float* h, const int64_t* parents, con
 /* with finished and out_finished (else MSS_ERR_UNSUPPORTED).                */
 /* Supported: beams and n_out up to 64, n_out at most beams * vocab, eos     */
 /* below vocab (else MSS_ERR_UNSUPPORTED); vocab up to 2^24, batch up to     */
-/* 65535, rows * stride below 2^47 (else MSS_ERR_SHAPE).  `flags` must be 0. */
+/* 65535, batch * beams * ceil(vocab / 8192) below 2^24, rows * stride below */
+/* 2^47 (else MSS_ERR_SHAPE).  `flags` must be 0.                            */
 /* Outputs must not overlap inputs or each other.  The workspace (16-byte    */
 /* aligned, the size of the query) need not be zeroed.                       */
 /* ------------------------------------------------------------------------ */

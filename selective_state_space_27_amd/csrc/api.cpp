@@ -1289,7 +1289,9 @@ mss_status mss_gated_recurrence_step(const float* h, const int64_t* parents, con
 // ------------------------------------------------- beam search
 static mss_status beam_shape(int64_t batch, int64_t beams, int64_t vocab, int64_t n_out) {
   if (batch <= 0 || beams <= 0 || vocab <= 0 || n_out <= 0 || batch > 65535 || vocab > (1LL << 24)) return MSS_ERR_SHAPE;
-  return beams > 64 || n_out > 64 || n_out > beams * vocab ? MSS_ERR_UNSUPPORTED : MSS_OK;
+  if (beams > 64 || n_out > 64 || n_out > beams * vocab) return MSS_ERR_UNSUPPORTED;
+  // Workgroups of 256 threads: fewer than 2^32 threads.
+  return mss::beam_select_workgroups(batch, beams, vocab) < (1LL << 24) ? MSS_OK : MSS_ERR_SHAPE;
 }
 
 size_t mss_beam_select_workspace_size(int64_t batch, int64_t beams, int64_t vocab, int64_t n_out) {

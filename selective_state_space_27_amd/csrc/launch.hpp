@@ -382,6 +382,7 @@ struct BeamSelectParams {
   bool bf16;
   void* workspace;
 };
+int64_t beam_select_workgroups(int64_t batch, int64_t beams, int64_t vocab);
 size_t beam_select_workspace_bytes(int64_t batch, int64_t beams, int64_t vocab, int64_t n_out);
 hipError_t launch_beam_select(const BeamSelectParams& p, hipStream_t stream);
 

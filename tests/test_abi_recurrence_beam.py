@@ -143,7 +143,8 @@ def test_select_refusals():
     for k in ("logits", "scores", "best", "parents", "tokens"):
         assert select(**{k: None}) == NULL, k
     for kw in (dict(batch=0), dict(beams=0), dict(vocab=0), dict(n=0), dict(batch=65536),
-               dict(vocab=(1 << 24) + 1, ls=1 << 25), dict(ls=999), dict(ls=1 << 46)):
+               dict(vocab=(1 << 24) + 1, ls=1 << 25), dict(ls=999), dict(ls=1 << 46),
+               dict(batch=65535, beams=64, vocab=1 << 16, ls=1 << 16)):
         assert select(**kw) == SHAPE, kw
     assert select(io=3) == DTYPE
     for kw in (dict(beams=65), dict(n=65), dict(vocab=1, eos=0, n=5), dict(flags=1), dict(eos=1000), dict(eos=-2),
