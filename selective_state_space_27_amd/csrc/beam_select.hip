@@ -251,6 +251,7 @@ __global__ void __launch_bounds__(THREADS) beam_merge_kernel(BeamArgs a) {
   __shared__ float lds_most[64];
   __shared__ uint32_t lds_top[64];  // ordered bits
   __shared__ int lds_over[64];
+  __shared__ uint32_t lds_bound;
   __shared__ uint64_t lds_keys[kRoomMerge];
   __shared__ uint32_t lds_best[WAVES][64];  // the upper halves
   __shared__ uint32_t lds_places[kRoomMerge], lds_out[kMaxOut];
@@ -367,12 +368,18 @@ __global__ void __launch_bounds__(THREADS) beam_merge_kernel(BeamArgs a) {
   }
   lds_best[wave][lane] = (uint32_t)(best >> 32);
   __syncthreads();
-  uint64_t bound = (uint64_t)lds_threshold<32, WAVES>(lds_best, !held || n > kLanesEnough, n) << 32;
+  if (wave == 0) {
+    const uint32_t t = lds_threshold<32, WAVES>(lds_best, !held || n > kLanesEnough, n);
+    if (lane == 0) lds_bound = t;
+  }
+  __syncthreads();
+  uint64_t bound = (uint64_t)lds_bound << 32;
   if (bound <= kOrderedNegInf64) bound = kOrderedNegInf64 + 1;
   if (held) {
+    if (best >= bound)
 #pragma unroll
-    for (int j = 0; j < kHeld; ++j)
-      if (o[j] >= bound) keep(o[j], (uint32_t)k0 * vocab + place_of(key[j]));
+      for (int j = 0; j < kHeld; ++j)
+        if (o[j] >= bound) keep(o[j], (uint32_t)k0 * vocab + place_of(key[j]));
   } else {
 #pragma unroll 4
     for (int i = threadIdx.x; i < items; i += THREADS) {
