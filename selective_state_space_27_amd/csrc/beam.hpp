@@ -43,18 +43,21 @@ __device__ __forceinline__ uint32_t wave_threshold(const uint32_t (&mine)[G], in
   }
   return t;
 }
-// The same of the values v[W][64] in LDS, each lane's largest alone where that is
-// enough: of 64 values the want-th largest is a good bound for up to 32, the least of
-// them a poor one for 64.
+// The same of the values v[W][64] in LDS, of which the largest of every lane count
+// (`fine`: of every lane and quarter of the rows).  The want-th of 64 is a good bound
+// while the best lie in different lanes: not for 64 of them, nor where they lie in one
+// beam's few slices.
 template <int BITS, int W>
-__device__ __forceinline__ uint32_t lds_threshold(const uint32_t (*v)[64], bool all, int want) {
-  uint32_t mine[W], most[1];
+__device__ __forceinline__ uint32_t lds_threshold(const uint32_t (*v)[64], bool fine, int want) {
+  uint32_t mine[4], most[1];
 #pragma unroll
-  for (int w = 0; w < W; ++w) mine[w] = v[w][threadIdx.x & 63];
-  if (all) return wave_threshold<BITS, W>(mine, want);
-  most[0] = mine[0];
+  for (int g = 0; g < 4; ++g) {
+    mine[g] = v[g * (W / 4)][threadIdx.x & 63];
 #pragma unroll
-  for (int w = 1; w < W; ++w) most[0] = max(most[0], mine[w]);
+    for (int w = 1; w < W / 4; ++w) mine[g] = max(mine[g], v[g * (W / 4) + w][threadIdx.x & 63]);
+  }
+  if (fine) return wave_threshold<BITS, 4>(mine, want);
+  most[0] = max(max(mine[0], mine[1]), max(mine[2], mine[3]));
   return wave_threshold<BITS, 1>(most, want);
 }
 constexpr int kLanesEnough = 32;

@@ -7,12 +7,15 @@
 // beam can differ by one unit of a logit near zero while their totals are tens)
 // and takes the best.
 //
-// The best n of many, in either launch: the threads' maxima (for n up to 32 the 64
-// lanes' over all waves) give a bound that at least n candidates are not below, and few
-// others (with 8192 logits and n = 16 some 20); those go to LDS and are ranked
-// there, each by counting what comes before it.  Where more pass than there is room
-// for (ties, a sorted row), the bound is raised by bisection first, and among equals
-// the place.
+// The best n of many, in either launch: the maxima of groups of threads give a bound
+// that at least n candidates are not below, and few others (with 8192 logits and n =
+// 16 some 20); those go to LDS and are ranked there, each by counting what comes
+// before it.  Where more pass than there is room for (ties, a sorted row), the bound is
+// raised by bisection first, and among equals the place.
+//
+// 32 x 8 x 50277 bf16 (25.7 MB): 11 us the slices, 5 us the merge; 8 x 16 x 250001 fp32
+// (128 MB), n = 32: 30 us and 10 us.  The first is bound by memory where logits are many
+// (4.3 TB/s), else by the latency of its steps, as the second always is.
 #include "beam.hpp"
 #include "launch.hpp"
 #include "recurrence.hpp"
@@ -369,7 +372,7 @@ __global__ void __launch_bounds__(THREADS) beam_merge_kernel(BeamArgs a) {
   lds_best[wave][lane] = (uint32_t)(best >> 32);
   __syncthreads();
   if (wave == 0) {
-    const uint32_t t = lds_threshold<32, WAVES>(lds_best, !held || n > kLanesEnough, n);
+    const uint32_t t = lds_threshold<24, WAVES>(lds_best, n > 8, n);
     if (lane == 0) lds_bound = t;
   }
   __syncthreads();
