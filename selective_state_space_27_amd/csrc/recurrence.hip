@@ -640,8 +640,11 @@ hipError_t start_chain(const Cut& c, void* workspace, Chain& chain, hipStream_t 
 
 // bf16 channels go in pairs, a word a lane, which the hardware reads and writes at any
 // alignment (at odd ones, 3 x 4099 x 1001, 39 us forward and 61 us backward, against 43
-// and 70 with one channel a lane); a row of one channel has none.
-bool in_pairs(int64_t dim, bool bf16) { return bf16 && dim > 1; }
+// and 70 with one channel a lane).  Not where the last channel would be alone in a
+// workgroup: the one before it, repeated to make a pair, would belong to two
+// workgroups, which may take different polynomials for the decay, and what is stored
+// would be either's.
+bool in_pairs(int64_t dim, bool bf16) { return bf16 && dim % 128 != 1; }
 
 template <bool BF16, int V>
 hipError_t launch_fwd(const RecurrenceFwdParams& p, hipStream_t stream) {

@@ -236,6 +236,22 @@ def test_same_call_same_bits():
         assert all(torch.equal(a, b) for a, b in zip(first, once()))
 
 
+@pytest.mark.parametrize("dim", [129, 257, 385])
+def test_a_last_channel_by_itself(dim):
+    """Channels next to the last one decay fast, the last two slowly: each has one value, whoever computes it."""
+    d = make(2, 700, dim, "bf16", dim)
+    d["lam"] = torch.full((dim,), 2.0, device="cuda:0")
+    d["lam"][-2:] = -6.0
+    check(d, "bf16")
+    first = None
+    for _ in range(20):
+        y, states = mss.gated_recurrence_fwd(*(d[k] for k in FWD), h0=d["h0"], keep_states=True)
+        g = mss.gated_recurrence_bwd(d["dy"], *(d[k] for k in FWD), states)
+        got = [y, states] + [g[k] for k in GRADS[:4]]
+        first = first or got
+        assert all(torch.equal(a, b) for a, b in zip(first, got))
+
+
 def test_two_streams_at_once():
     a, b = make(1, 8000, 200, "bf16", 31), make(2, 5000, 130, "fp32", 32)
     want = [mss.gated_recurrence_fwd(*(d[k] for k in FWD), h0=d["h0"]) for d in (a, b)]
