@@ -632,7 +632,9 @@ size_t mss_wgrad8_workspace_size(const void* dy, int64_t dy_stride, int64_t toke
 /* with h before the first step h0 (NULL: zero).  sqrt(1 - a^2) keeps the    */
 /* state's size whatever the decay.  Where starts[b, t] is not zero, a       */
 /* sequence packed into the row begins: h_{t-1} counts as zero there,        */
-/* whatever it holds.                                                         */
+/* whatever it holds.  A step with gate_a = -infinity (a = 1) and a finite x */
+/* leaves the state as it is: padding behind a sequence's end.  A state past */
+/* fp32's range stays without a value (infinity or NaN) up to the next start. */
 /*                                                                          */
 /* Layouts: x, gate_a, gate_x, y [batch, seqlen, dim] io_dtype, rows         */
 /*   (b * seqlen + t) with a row stride each (elements, at least dim) and    */
@@ -775,12 +777,12 @@ mss_status mss_reorder_states(void* const* states, const int64_t* row_bytes, int
 /* Status of a call that used `workspace`.                                   */
 /*                                                                          */
 /* The selective scan (forward, fused, backward) and the gated recurrence    */
-/* (forward, backward) hand states between                                    */
-/* workgroups through flags in their workspace; each wait for such a flag is */
-/* bounded, and a wait that gives up (never expected) leaves the call's      */
-/* outputs invalid and sets the status word, the workspace's first 4 bytes, */
-/* which every call of the library clears in its first kernel (the SSD      */
-/* workspace has the word too and never sets it).  This waits for           */
+/* (forward, backward) hand states between workgroups through flags in their */
+/* workspace; each wait for such a flag is bounded, and a wait that gives up */
+/* (never expected) leaves the call's outputs invalid and sets the status    */
+/* word, the workspace's first 4 bytes, which every call of the library      */
+/* clears in its first kernel (the SSD and beam selection workspaces have    */
+/* the word too and never set it).  This waits for                           */
 /* `hip_stream` (NULL = the default stream) to finish, reads the word and    */
 /* returns MSS_OK, or MSS_ERR_WAIT when the last call that used the         */
 /* workspace gave up a wait; MSS_ERR_NULL for a NULL workspace, MSS_ERR_HIP  */

@@ -37,6 +37,8 @@ struct Slice {
   int count;   // of candidates listed
 };
 
+constexpr size_t kHeader = 16;  // of the workspace: the status word, which nothing sets
+
 struct BeamArgs {
   BeamSelectParams p;
   Slice* slices;    // [rows][nslices]
@@ -124,6 +126,7 @@ __global__ void __launch_bounds__(kThreadsRow) beam_rows_kernel(BeamArgs a) {
   // us instead of 16.1).
   const uint32_t slice = blockIdx.x % (uint32_t)a.nslices;
   const int64_t row = blockIdx.x / (uint32_t)a.nslices;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *static_cast<int*>(a.p.workspace) = 0;
   if (p.finished != nullptr && p.finished[row] != 0) return;  // its logits are not looked at
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, first = (int)slice * L::kSlice;
   const int n = (int)p.n_out;
@@ -491,12 +494,12 @@ int64_t beam_select_workgroups(int64_t batch, int64_t beams, int64_t vocab) {
 
 size_t beam_select_workspace_bytes(int64_t batch, int64_t beams, int64_t vocab, int64_t n_out) {
   const int64_t rows = batch * beams;
-  return lists_offset(rows, vocab) + (size_t)(rows * slices_of(rows, vocab) * n_out) * sizeof(uint64_t);
+  return kHeader + lists_offset(rows, vocab) + (size_t)(rows * slices_of(rows, vocab) * n_out) * sizeof(uint64_t);
 }
 
 hipError_t launch_beam_select(const BeamSelectParams& p, hipStream_t stream) {
   const int64_t rows = p.batch * p.beams;
-  char* ws = static_cast<char*>(p.workspace);
+  char* ws = static_cast<char*>(p.workspace) + kHeader;
   const BeamArgs a{p, reinterpret_cast<Slice*>(ws), reinterpret_cast<uint64_t*>(ws + lists_offset(rows, p.vocab)),
                    (int)slices_of(rows, p.vocab)};
   const bool wide = wide_slices(rows, p.vocab);

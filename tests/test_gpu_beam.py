@@ -1,9 +1,10 @@
 """GPU parity of beam search's selection and of the states' reordering.
 
 Parents, tokens and finished marks have to be equal.  Scores: a total is formed
-in 64 bits from the log of a sum whose terms are within 4 units of 2^-24 and whose
-fp32 partial sums have at most 128 terms: 140 units at most, and its own rounding
-to fp32."""
+in 64 bits from the log of a sum whose terms exp(-d) are within 4 units of 2^-24
+(for bf16 logits 4 + 2 d, of a term that is exp(-d) of the largest: under 5 units of
+that) and whose fp32 partial sums have at most 128 terms: 140 units at most, and its
+own rounding to fp32."""
 import numpy as np
 import pytest
 import torch
@@ -127,6 +128,24 @@ def test_beams_without_candidates():
 
 
 @pytest.mark.parametrize("io", ["bf16", "fp32"])
+def test_more_lists_than_the_merge_holds(io):
+    """Ordinary rows; ties beyond what is ranked; finished beams and beams without candidates."""
+    for beams, vocab, n_out in ((64, 10001, 64), (32, 70001, 48), (3, 1000003, 64)):
+        logits, scores = make(2, beams, vocab, io, vocab)
+        check(logits, scores, n_out)
+        finished = torch.arange(beams, device="cuda:0").expand(2, beams).contiguous() % 3 == 1
+        logits[:, 1] = float("nan")  # finished: not looked at
+        logits[0, 2, 17], scores[1, 0] = float("inf"), -float("inf")
+        scores[:, 1] = -1.0
+        check(logits, scores, n_out, finished, vocab - 1)
+        check(torch.zeros(2, beams, vocab, dtype=DT[io], device="cuda:0"), torch.zeros(2, beams, device="cuda:0"), n_out,
+              finished, 5)
+        few = torch.full((1, beams, vocab), -float("inf"), dtype=DT[io], device="cuda:0")
+        few[0, -1, vocab // 2], few[0, 0, vocab - 1] = 3.0, -7.0
+        check(few, torch.zeros(1, beams, device="cuda:0"), n_out)
+
+
+@pytest.mark.parametrize("io", ["bf16", "fp32"])
 def test_finished_beams(io):
     for eos, n_out in ((0, 8), (2, 16), (699, 40)):
         logits, scores = make(4, 4, 700, io, eos, 3)
@@ -185,6 +204,20 @@ def test_two_streams_at_once():
     for pair in got:
         for g, w in zip(pair, want):
             assert all(torch.equal(x, y) for x, y in zip(g, w))
+
+
+def test_workspace_status():
+    """The workspace's status word is cleared like every call's, and a finished first beam does not keep it from that."""
+    logits, scores = make(1, 2, 100, "fp32", 13)
+    finished = torch.ones(1, 2, dtype=torch.uint8, device="cuda:0")
+    need = mss.lib().mss_beam_select_workspace_size(1, 2, 100, 2)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda:0")
+    out, at = torch.empty(1, 2, device="cuda:0"), torch.empty(2, 1, 2, dtype=torch.int64, device="cuda:0")
+    torch.cuda.synchronize()
+    st = mss.lib().mss_beam_select(logits.data_ptr(), 100, scores.data_ptr(), finished.data_ptr(), 3, out.data_ptr(),
+                                   at[0].data_ptr(), at[1].data_ptr(), None, 1, 2, 100, 2, 0, 0, ws.data_ptr(), need, None)
+    assert st == 0 and mss.lib().mss_workspace_status(ws.data_ptr(), None) == 0
+    assert at[1].tolist() == [[3, 3]] and sorted(at[0][0].tolist()) == [0, 1]
 
 
 def test_select_refusals():
