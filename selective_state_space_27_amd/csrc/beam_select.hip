@@ -465,19 +465,25 @@ __global__ void __launch_bounds__(THREADS) beam_merge_kernel(BeamArgs a) {
   }
 }
 
-// 256 threads where they hold the lists, whose barriers take less time.
+// 256 threads where they hold the lists, whose barriers take less time (16 x 8 x 32000
+// bf16, n = 16: 13.2 us, with 1024 14.3; 64 x 4 x 32000 fp32: 15.1 and 15.7).
 template <int THREADS>
 bool holds(int64_t across, int64_t n) { return across <= THREADS && n <= THREADS / across * kHeld; }
 
-// Slices of 8192 logits where they fill the card twice; else of 2048, for the time
-// that a workgroup takes for its slice.
+// Slices of 8192 logits where there is much to do or to merge (16 x 8 x 32000 bf16:
+// 13.2 us, with slices of 2048 15.1; 4 x 16 x 32000: 13.4 and 16.3), else of 2048, for
+// the time that a workgroup takes for its slice (1 x 5 x 50277: 10.8 and 10.0) or
+// for rows that are no longer (256 x 16 x 1500: 25.6 and 18.6).  16 x 4 x 32000 and 64 x 8
+// x 5000 take the same time either way.
 constexpr int64_t kWideSlice = 8192, kNarrowSlice = 2048;
-bool wide_slices(int64_t rows, int64_t vocab) { return rows * ((vocab + kWideSlice - 1) / kWideSlice) >= 512; }
-int64_t slices_of(int64_t rows, int64_t vocab) {
-  const int64_t s = wide_slices(rows, vocab) ? kWideSlice : kNarrowSlice;
-  return (vocab + s - 1) / s;
+constexpr int64_t kManySlices = 1280, kManyLists = 128;  // narrow ones: of the call, of a sequence
+int64_t slices_of(int64_t batch, int64_t beams, int64_t vocab, bool& wide) {
+  const int64_t narrow = (vocab + kNarrowSlice - 1) / kNarrowSlice;
+  wide = narrow > 1 && (batch * beams * narrow > kManySlices || beams * narrow > kManyLists);
+  return wide ? (vocab + kWideSlice - 1) / kWideSlice : narrow;
 }
-size_t lists_offset(int64_t rows, int64_t vocab) { return (size_t)(rows * slices_of(rows, vocab)) * sizeof(Slice); }
+
+size_t lists_offset(int64_t slices) { return kHeader + (size_t)slices * sizeof(Slice); }
 
 template <bool BF16, int NV>
 void launch_rows(const BeamArgs& a, hipStream_t stream) {
@@ -489,20 +495,21 @@ void launch_rows(const BeamArgs& a, hipStream_t stream) {
 }  // namespace
 
 int64_t beam_select_workgroups(int64_t batch, int64_t beams, int64_t vocab) {
-  return batch * beams * slices_of(batch * beams, vocab);
+  bool wide;
+  return batch * beams * slices_of(batch, beams, vocab, wide);
 }
 
 size_t beam_select_workspace_bytes(int64_t batch, int64_t beams, int64_t vocab, int64_t n_out) {
-  const int64_t rows = batch * beams;
-  return kHeader + lists_offset(rows, vocab) + (size_t)(rows * slices_of(rows, vocab) * n_out) * sizeof(uint64_t);
+  const int64_t slices = beam_select_workgroups(batch, beams, vocab);
+  return lists_offset(slices) + (size_t)(slices * n_out) * sizeof(uint64_t);
 }
 
 hipError_t launch_beam_select(const BeamSelectParams& p, hipStream_t stream) {
-  const int64_t rows = p.batch * p.beams;
-  char* ws = static_cast<char*>(p.workspace) + kHeader;
-  const BeamArgs a{p, reinterpret_cast<Slice*>(ws), reinterpret_cast<uint64_t*>(ws + lists_offset(rows, p.vocab)),
-                   (int)slices_of(rows, p.vocab)};
-  const bool wide = wide_slices(rows, p.vocab);
+  bool wide;
+  const int64_t nslices = slices_of(p.batch, p.beams, p.vocab, wide);
+  char* ws = static_cast<char*>(p.workspace);
+  const BeamArgs a{p, reinterpret_cast<Slice*>(ws + kHeader),
+                   reinterpret_cast<uint64_t*>(ws + lists_offset(p.batch * p.beams * nslices)), (int)nslices};
   if (p.bf16) wide ? launch_rows<true, 4>(a, stream) : launch_rows<true, 1>(a, stream);
   else wide ? launch_rows<false, 8>(a, stream) : launch_rows<false, 2>(a, stream);
   const hipError_t e = hipGetLastError();
