@@ -725,8 +725,9 @@ mss_status mss_gated_recurrence_step(const float* h, const int64_t* parents, con
 /*   total[k, v] = scores[b, k] + logits[b, k, v]                            */
 /*                 - log sum_v' exp(logits[b, k, v'])                        */
 /* and the n_out largest over k and v are taken, in descending order, ties   */
-/* by the lower k * vocab + v: out_scores (rounded to fp32), parents (k) and */
-/* tokens (v), [batch, n_out] each.  Totals are compared in 64 bits.         */
+/* by the lower k, then the larger logit, then the lower v: out_scores       */
+/* (rounded to fp32), parents (k) and tokens (v), [batch, n_out] each.       */
+/* Totals are compared in 64 bits.                                           */
 /*   A logit of -infinity (a banned token) has total -infinity.              */
 /*   finished[b, k] not zero: the beam's only candidate is the token eos,    */
 /*     with total scores[b, k]; its other totals are -infinity and its       */

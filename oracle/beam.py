@@ -25,11 +25,16 @@ def totals(logits, scores, finished=None, eos=None):
 
 
 def select(logits, scores, n_out, finished=None, eos=None):
-    """(scores, parents, tokens, finished) in fp64 and integers."""
+    """(scores, parents, tokens, finished) in fp64 and integers; ties by the lower beam,
+    the larger logit, the lower token."""
     t = totals(logits, scores, finished, eos)
     batch, _, vocab = t.shape
     flat = t.reshape(batch, -1)
-    at = np.argsort(-flat, axis=1, kind="stable")[:, :n_out]
+    logit = np.where(flat == -np.inf, 0.0, np.asarray(logits, np.float64).reshape(batch, -1))
+    if finished is not None:
+        logit[np.repeat(np.asarray(finished) != 0, vocab, 1)] = 0.0
+    beam = np.arange(flat.shape[1]) // vocab
+    at = np.stack([np.lexsort((-logit[b], beam, -flat[b]))[:n_out] for b in range(batch)])  # stable: then the place
     parents, tokens = at // vocab, at % vocab
     done = tokens == (-1 if eos is None else eos)
     if finished is not None:

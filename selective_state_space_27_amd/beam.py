@@ -18,7 +18,8 @@ def beam_select(logits, scores, n_out=None, *, finished=None, eos=None, stream=N
     """The ``n_out`` (default: beams) best continuations of every sequence.
 
     total = scores + log_softmax(logits), over beams and vocabulary; in
-    descending order, ties by the lower beam * vocab + token.  logits: [batch,
+    descending order, ties by the lower beam, then the larger logit (where 64 bits
+    of a total do not tell them apart), then the lower token.  logits: [batch,
     beams, vocab] float32 or bfloat16 (rows may have a stride); scores: [batch,
     beams] float32, the beams' totals so far (-inf: not in use); finished:
     [batch, beams] bool or uint8, beams whose only candidate is the token

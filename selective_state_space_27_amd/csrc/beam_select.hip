@@ -5,7 +5,8 @@
 // exponentials and its n_out best candidates.  The second, a workgroup per
 // sequence, forms the beams' totals from those (in 64 bits: candidates of one
 // beam can differ by one unit of a logit near zero while their totals are tens)
-// and takes the best.
+// and takes the best; of equal totals the lower beam's, in a beam the larger logit's
+// (tiny logits may differ where 64 bits of a total do not), then the lower token's.
 //
 // The best n of many, in either launch: the maxima of groups of threads give a bound
 // that at least n candidates are not below, and few others (with 8192 logits and n =
@@ -30,6 +31,15 @@ constexpr int kHeld = 16;      // totals a thread of the merge holds
 // ranking about as many).
 constexpr int kRoom = 512, kRoomMerge = 1024;
 constexpr int kMaxOut = 64;    // n_out
+
+// What decides between equal totals, larger first: 6 bits of the beam, the logit, 24 of
+// the token.
+__device__ __forceinline__ uint64_t second_of(int beam, uint64_t key) {
+  return (uint64_t)(63 - beam) << 56 | (key >> 32) << 24 | (0xffffffu - place_of(key));
+}
+__device__ __forceinline__ uint32_t place_of_second(uint64_t second, int vocab) {
+  return (63 - (uint32_t)(second >> 56)) * (uint32_t)vocab + (0xffffffu - ((uint32_t)second & 0xffffffu));
+}
 
 struct Slice {
   double sum;  // of exp(logit - top)
@@ -73,43 +83,76 @@ __device__ __forceinline__ int block_sum(int v, int* lds) {
   return s;
 }
 
+// Sum over the threads before this one, and over all; `lds` as there.
+template <int WAVES>
+__device__ __forceinline__ int block_before(int v, int* lds, int& total) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int s = v;
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) {
+    const int t = __shfl_up(s, m, 64);
+    s += lane >= m ? t : 0;
+  }
+  if (lane == 63) lds[wave] = s;
+  __syncthreads();
+  int before = 0;
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) {
+    before += w < wave ? lds[w] : 0;
+    total += lds[w];
+  }
+  __syncthreads();
+  return before + s - v;
+}
+
 // VE logits at `at` as loaded; NV vectors a thread.
 template <bool BF16, int NV>
 struct Logits {
   static constexpr int kVec = BF16 ? 8 : 4;
   static constexpr int kSlice = kThreadsRow * NV * kVec;
   u32x4 raw[NV];
-  __device__ __forceinline__ float at(int j, int e) const {
-    if constexpr (BF16) return e & 1 ? bf16_hi(raw[j][e >> 1]) : bf16_lo(raw[j][e >> 1]);
-    else return __uint_as_float(raw[j][e]);
+  static __device__ __forceinline__ float value(u32x4 v, int e) {
+    if constexpr (BF16) return e & 1 ? bf16_hi(v[e >> 1]) : bf16_lo(v[e >> 1]);
+    else return __uint_as_float(v[e]);
   }
+  __device__ __forceinline__ float at(int j, int e) const { return value(raw[j], e); }
   static __device__ __forceinline__ int place(int first, int j, int e) {
     return first + (j * kThreadsRow + (int)threadIdx.x) * kVec + e;
   }
-  // Past the row's end: -infinity.
-  __device__ __forceinline__ void load(const void* row, int first, int vocab) {
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int at = place(first, j, 0), n = vocab - at;
-      if constexpr (BF16) {
-        const uint16_t* p = static_cast<const uint16_t*>(row) + at;
-        if (n >= kVec) {
-          raw[j] = *reinterpret_cast<const u32x4_a2*>(p);
-        } else {
-          raw[j] = u32x4{0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u};
-#pragma unroll
-          for (int e = 0; e < kVec - 1; ++e)
-            if (e < n) raw[j][e >> 1] = (raw[j][e >> 1] & (e & 1 ? 0xffffu : 0xffff0000u)) | (uint32_t)p[e] << (16 * (e & 1));
-        }
+  // From `at` on; past the row's end: -infinity.
+  static __device__ __forceinline__ u32x4 load(const void* row, int at, int vocab) {
+    const int n = vocab - at;
+    u32x4 v;
+    if constexpr (BF16) {
+      const uint16_t* p = static_cast<const uint16_t*>(row) + at;
+      if (n >= kVec) {
+        v = *reinterpret_cast<const u32x4_a2*>(p);
       } else {
-        const uint32_t* p = static_cast<const uint32_t*>(row) + at;
-        if (n >= kVec) {
-          raw[j] = *reinterpret_cast<const u32x4_a4*>(p);
-        } else {
+        v = u32x4{0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u};
 #pragma unroll
-          for (int e = 0; e < kVec; ++e) raw[j][e] = e < n ? p[e] : 0xff800000u;
-        }
+        for (int e = 0; e < kVec - 1; ++e)
+          if (e < n) v[e >> 1] = (v[e >> 1] & (e & 1 ? 0xffffu : 0xffff0000u)) | (uint32_t)p[e] << (16 * (e & 1));
       }
+    } else {
+      const uint32_t* p = static_cast<const uint32_t*>(row) + at;
+      if (n >= kVec) {
+        v = *reinterpret_cast<const u32x4_a4*>(p);
+      } else {
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) v[e] = e < n ? p[e] : 0xff800000u;
+      }
+    }
+    return v;
+  }
+  // f(ordered bits) of every logit of the thread, read again.
+  template <class F>
+  static __device__ __forceinline__ void again(const void* row, int first, int vocab, F f) {
+#pragma unroll 1
+    for (int j = 0; j < NV; ++j) {
+      const u32x4 v = load(row, place(first, j, 0), vocab);
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) f(ordered_bits(value(v, e)));
     }
   }
 };
@@ -132,7 +175,8 @@ __global__ void __launch_bounds__(kThreadsRow) beam_rows_kernel(BeamArgs a) {
   const int n = (int)p.n_out;
   const void* base = static_cast<const char*>(p.logits) + row * p.stride * (BF16 ? 2 : 4);
   L l;
-  l.load(base, first, (int)p.vocab);
+#pragma unroll
+  for (int j = 0; j < NV; ++j) l.raw[j] = L::load(base, L::place(first, j, 0), (int)p.vocab);
 
   float top = -__builtin_inff();
 #pragma unroll
@@ -171,63 +215,66 @@ __global__ void __launch_bounds__(kThreadsRow) beam_rows_kernel(BeamArgs a) {
   if (lane == 0) lds_sum[wave] = sum;
 
   // Few pass.
-  auto keep = [&](float v, int j, int e) {
+  auto keep = [&](uint32_t ordered, int place) {
     const int at = atomicAdd(&lds_count, 1);
-    if (at < kRoom) lds_keys[at] = key_of(ordered_bits(v), (uint32_t)L::place(first, j, e));
+    if (at < kRoom) lds_keys[at] = key_of(ordered, (uint32_t)place);
   };
   if (top >= least) {
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
       for (int e = 0; e < L::kVec; ++e)
-        if (l.at(j, e) >= least) keep(l.at(j, e), j, e);
+        if (l.at(j, e) >= least) keep(ordered_bits(l.at(j, e)), L::place(first, j, e));
   }
   __syncthreads();
   int count = lds_count;
   if (count > kRoom) {
-    // A bound that n to kRoom candidates are not below; where equals allow none, the
-    // n-th largest value and the place up to which its equals are taken.
-    uint32_t exact = 0;
-    bool tied = true;
-    for (int b = 31; b >= 0 && tied; --b) {
-      const uint32_t with = exact | 1u << b;
+    // Mostly many equal the bound, and fewer than n are above it: it is the n-th largest.
+    // Else a bound that n to kRoom candidates are not below, or, where equals allow
+    // none, the n-th largest.  Of its equals the first are taken.  The logits are read
+    // again, from the caches: kept in registers for this they would take half of the
+    // waves' room (8 x 16 x 250001 fp32: 40.2 us, so 38.2).
+    const auto all = [&](auto f) { L::again(base, first, (int)p.vocab, f); };
+    const auto number = [&](auto f) {
       int c = 0;
-#pragma unroll
-      for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int e = 0; e < L::kVec; ++e) c += ordered_bits(l.at(j, e)) >= with;
-      c = block_sum<kWavesRow>(c, lds_add);
-      if (c >= n) exact = with, tied = c > kRoom;
-    }
-    int until = L::kSlice;  // past the first place, of what is taken of the equals
-    if (tied) {
-      int above = 0;
-#pragma unroll
-      for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int e = 0; e < L::kVec; ++e) above += ordered_bits(l.at(j, e)) > exact;
-      above = block_sum<kWavesRow>(above, lds_add);
-      until = 0;
-      for (int b = 13; b >= 0; --b) {
-        const int with = until | 1 << b;
-        int c = 0;
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-#pragma unroll
-          for (int e = 0; e < L::kVec; ++e)
-            c += ordered_bits(l.at(j, e)) == exact && L::place(first, j, e) < first + with;
-        if (block_sum<kWavesRow>(c, lds_add) < n - above) until = with;
+      all([&](uint32_t o) { c += f(o); });
+      return block_sum<kWavesRow>(c, lds_add);
+    };
+    // (A negative bf16's ordered bits end in ones.)
+    const auto whole = [](uint32_t o) { return BF16 && !(o >> 31) ? o | 0xffffu : o; };
+    uint32_t exact = whole(bound);
+    int above = number([&](uint32_t o) { return o > exact; });
+    if (above >= n) {
+      const bool high = BF16 || number([&](uint32_t o) { return o > (bound | 0xffffu); }) >= n;
+      if (high) exact = 0;
+      bool tied = true;
+      for (int b = high ? 31 : 15; b >= (BF16 ? 16 : 0) && tied; --b) {
+        const uint32_t with = exact | 1u << b;
+        const int c = number([&](uint32_t o) { return o >= with; });
+        if (c >= n) exact = with, tied = c > kRoom;
       }
+      exact = whole(exact);
+      if (tied) above = number([&](uint32_t o) { return o > exact; });
+      else exact -= 1, above = n;  // none of its equals apart from the others
     }
     if (threadIdx.x == 0) lds_count = 0;
     __syncthreads();
+    int left = n - above;  // of the equals
+#pragma unroll 1
+    for (int j = 0; j < NV; ++j) {
+      const u32x4 v = L::load(base, L::place(first, j, 0), (int)p.vocab);
+      int equals = 0, total;
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
+      for (int e = 0; e < L::kVec; ++e) equals += ordered_bits(L::value(v, e)) == exact;
+      int before = block_before<kWavesRow>(equals, lds_add, total);
 #pragma unroll
       for (int e = 0; e < L::kVec; ++e) {
-        const uint32_t o = ordered_bits(l.at(j, e));
-        if (o > exact || (o == exact && L::place(first, j, e) <= first + until)) keep(l.at(j, e), j, e);
+        const uint32_t o = ordered_bits(L::value(v, e));
+        if (o > exact || (o == exact && before < left)) keep(o, L::place(first, j, e));
+        before += o == exact;
       }
+      left -= total;
+    }
     __syncthreads();
     count = lds_count;
   }
@@ -260,7 +307,8 @@ __global__ void __launch_bounds__(THREADS) beam_merge_kernel(BeamArgs a) {
   __shared__ uint32_t lds_bound;
   __shared__ uint64_t lds_keys[kRoomMerge];
   __shared__ uint32_t lds_best[WAVES][64];  // the upper halves
-  __shared__ uint32_t lds_places[kRoomMerge], lds_out[kMaxOut];
+  __shared__ uint64_t lds_seconds[kRoomMerge];
+  __shared__ uint32_t lds_out[kMaxOut];
   __shared__ int lds_count, lds_add[WAVES];
   const BeamSelectParams& p = a.p;
   const int64_t b = blockIdx.x;
@@ -332,24 +380,24 @@ __global__ void __launch_bounds__(THREADS) beam_merge_kernel(BeamArgs a) {
   }
   __syncthreads();
 
-  // The i-th item: its total's ordered bits (kOrderedNegInf64: no candidate) and
-  // place.  In the order of the lists, so that neighbouring threads, whose maxima
+  // The i-th item: its total's ordered bits (kOrderedNegInf64: no candidate) and what
+  // decides between equal ones.  In the order of the lists, so that neighbouring threads, whose maxima
   // make the bound, look at the same rank of different slices.
-  auto item = [&](int i, uint32_t& place) -> uint64_t {
+  auto item = [&](int i, uint64_t& second) -> uint64_t {
     const int rank = i / across, at = i - rank * across, k = at / a.nslices;
     const uint64_t key = lists[i];
     const int listed = slices[at].count;
     const double base = lds_base[k];
     const bool over = lds_over[k] != 0;
-    place = (uint32_t)k * vocab + (over ? (uint32_t)p.eos : place_of(key));
+    second = second_of(k, over ? key_of(0, (uint32_t)p.eos) : key);
     const bool is = base != -__builtin_inf() && (over ? rank == 0 && at == k * a.nslices : rank < listed);
     const double total = over ? base : base + ((double)value_of((uint32_t)(key >> 32)) - (double)lds_most[k]);
     return is ? ordered_bits(total) : kOrderedNegInf64;
   };
-  uint32_t place;
-  auto keep = [&](uint64_t o, uint32_t at) {
+  uint64_t second;
+  auto keep = [&](uint64_t o, uint64_t then) {
     const int to = atomicAdd(&lds_count, 1);
-    if (to < kRoomMerge) lds_keys[to] = o, lds_places[to] = at;
+    if (to < kRoomMerge) lds_keys[to] = o, lds_seconds[to] = then;
   };
   uint64_t o[kHeld], best = kOrderedNegInf64;
   if (held) {
@@ -368,7 +416,7 @@ __global__ void __launch_bounds__(THREADS) beam_merge_kernel(BeamArgs a) {
   } else {
 #pragma unroll 4
     for (int i = threadIdx.x; i < items; i += THREADS) {
-      const uint64_t t = item(i, place);
+      const uint64_t t = item(i, second);
       best = t > best ? t : best;
     }
   }
@@ -385,46 +433,48 @@ __global__ void __launch_bounds__(THREADS) beam_merge_kernel(BeamArgs a) {
     if (best >= bound)
 #pragma unroll
       for (int j = 0; j < kHeld; ++j)
-        if (o[j] >= bound) keep(o[j], (uint32_t)k0 * vocab + place_of(key[j]));
+        if (o[j] >= bound) keep(o[j], second_of(k0, key[j]));
   } else {
 #pragma unroll 4
     for (int i = threadIdx.x; i < items; i += THREADS) {
-      const uint64_t t = item(i, place);
-      if (t >= bound) keep(t, place);
+      const uint64_t t = item(i, second);
+      if (t >= bound) keep(t, second);
     }
   }
   __syncthreads();
   int count = lds_count;
   if (count > kRoomMerge) {  // as for a row, reading the lists each time
-    uint64_t exact = 0;
+    int past = 0;  // of other prefixes than the bound's
+    for (int i = threadIdx.x; i < items; i += THREADS) past += item(i, second) > (bound | 0xffffffffffull);
+    const bool high = block_sum<WAVES>(past, lds_add) >= n;
+    uint64_t exact = high ? 0 : bound;
     bool tied = true;
-    for (int bit = 63; bit >= 0 && tied; --bit) {
+    for (int bit = high ? 63 : 39; bit >= 0 && tied; --bit) {
       const uint64_t with = exact | 1ull << bit;
       int c = 0;
-      for (int i = threadIdx.x; i < items; i += THREADS) c += item(i, place) >= with;
+      for (int i = threadIdx.x; i < items; i += THREADS) c += item(i, second) >= with;
       c = block_sum<WAVES>(c, lds_add);
       if (c >= n) exact = with, tied = c > kRoomMerge;
     }
     // (Fewer than n candidates: all of them, and none of what is not one.)
     if (exact <= kOrderedNegInf64) exact = kOrderedNegInf64 + 1, tied = false;
-    uint32_t until = ~0u;
+    uint64_t least = 0;  // of the equals' second keys
     if (tied) {
       int above = 0;
-      for (int i = threadIdx.x; i < items; i += THREADS) above += item(i, place) > exact;
+      for (int i = threadIdx.x; i < items; i += THREADS) above += item(i, second) > exact;
       above = block_sum<WAVES>(above, lds_add);
-      until = 0;
-      for (int bit = 30; bit >= 0; --bit) {
-        const uint32_t with = until | 1u << bit;
+      for (int bit = 61; bit >= 0; --bit) {
+        const uint64_t with = least | 1ull << bit;
         int c = 0;
-        for (int i = threadIdx.x; i < items; i += THREADS) c += item(i, place) == exact && place < with;
-        if (block_sum<WAVES>(c, lds_add) < n - above) until = with;
+        for (int i = threadIdx.x; i < items; i += THREADS) c += item(i, second) == exact && second >= with;
+        if (block_sum<WAVES>(c, lds_add) >= n - above) least = with;
       }
     }
     if (threadIdx.x == 0) lds_count = 0;
     __syncthreads();
     for (int i = threadIdx.x; i < items; i += THREADS) {
-      const uint64_t o = item(i, place);
-      if (o > exact || (o == exact && place <= until)) keep(o, place);
+      const uint64_t o = item(i, second);
+      if (o > exact || (o == exact && second >= least)) keep(o, second);
     }
     __syncthreads();
     count = lds_count;
@@ -440,15 +490,18 @@ __global__ void __launch_bounds__(THREADS) beam_merge_kernel(BeamArgs a) {
   const int found = count < n ? count : n;
   for (int i = threadIdx.x; i < count; i += THREADS) {
     const uint64_t mine = lds_keys[i];
-    const uint32_t at = lds_places[i];
+    const uint64_t then = lds_seconds[i];
     int rank = 0;
 #pragma unroll 8
     for (int o = 0; o < count; ++o) {
       const uint64_t other = lds_keys[o];
-      const uint32_t where = lds_places[o];
-      rank += (other > mine) | ((other == mine) & (where < at));
+      rank += (other > mine) | ((other == mine) & (lds_seconds[o] > then));
     }
-    if (rank < n) put(rank, (float)value_of(mine), at), lds_out[rank] = at;
+    if (rank < n) {
+      const uint32_t at = place_of_second(then, vocab);
+      put(rank, (float)value_of(mine), at);
+      lds_out[rank] = at;
+    }
   }
   if (found == n) return;
   // Fewer candidates than asked for: all are listed, the others follow in order of place.

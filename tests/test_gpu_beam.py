@@ -1,10 +1,10 @@
 """GPU parity of beam search's selection and of the states' reordering.
 
 Parents, tokens and finished marks have to be equal.  Scores: a total is formed
-in 64 bits from the log of a sum whose terms exp(-d) are within 4 units of 2^-24
-(for bf16 logits 4 + 2 d, of a term that is exp(-d) of the largest: under 5 units of
-that) and whose fp32 partial sums have at most 128 terms: 140 units at most, and its
-own rounding to fp32."""
+in 64 bits from the log of a sum of terms exp(-d).  A term is within 4 units of 2^-24
+(bf16 logits: 4 + 2 d, and on the softmax's own average d is below the log of the
+vocabulary, 17), and has gone through at most 24 additions in fp32: under 140 units
+in all, and its own rounding to fp32."""
 import numpy as np
 import pytest
 import torch
@@ -85,6 +85,23 @@ def test_ties_go_to_the_lowest_place(io, vocab):
     zeros = torch.zeros(1, 2, vocab, dtype=DT[io], device="cuda:0")
     zeros[0, :, ::2] = -0.0  # equal to +0
     check(zeros, torch.zeros(1, 2, device="cuda:0"), 16)
+
+
+@pytest.mark.parametrize("io", ["bf16", "fp32"])
+@pytest.mark.parametrize("n_out", [1, 7, 64])
+def test_many_nearly_equal_logits(io, n_out):
+    """More candidates near the best than are ranked: equal ones of either sign, ones that differ in their last bits
+    only, and ones a little above many equals."""
+    vocab, g = 20011, gen(n_out)
+    some = torch.rand(vocab, generator=g, device="cuda:0")
+    negative = torch.full((vocab,), -1.1, device="cuda:0")
+    above = torch.where(torch.arange(vocab, device="cuda:0") % 2500 == 77, 2.0 + some, 0.7)
+    half = torch.where(some < 0.5, 3.3, -3.3)
+    few = torch.where(some < 0.002, 5.0, -5.0)
+    for row in (negative, above, -above, half, few, 1 + some / 128, -1 - some / 128, some * 1e-30, 100 + some,
+                torch.where(some < 0.1, 1 + some / 128, negative)):
+        check(row.expand(1, 2, vocab).to(DT[io]).contiguous(), torch.tensor([[-0.5, -40.0]], device="cuda:0"), n_out,
+              apart=False)
 
 
 @pytest.mark.parametrize("io", ["bf16", "fp32"])
