@@ -12,11 +12,12 @@
 // that at least n candidates are not below, and few others (with 8192 logits and n =
 // 16 some 20); those go to LDS and are ranked there, each by counting what comes
 // before it.  Where more pass than there is room for (ties, a sorted row), the bound is
-// raised by bisection first, and among equals the place.
+// raised first, bit by bit where need be.
 //
-// 32 x 8 x 50277 bf16 (25.7 MB): 11 us the slices, 5 us the merge; 8 x 16 x 250001 fp32
-// (128 MB), n = 32: 30 us and 10 us.  The first is bound by memory where logits are many
-// (4.3 TB/s), else by the latency of its steps, as the second always is.
+// 32 x 8 x 50277 bf16 (25.7 MB): 11 us the slices, 5 us the merge (all logits equal: 33
+// in all); 8 x 16 x 250001 fp32 (128 MB), n = 32: 28 us and 10 us (110).  The first is
+// bound by memory where logits are many (4.6 TB/s), else by the latency of its steps,
+// as the second always is.
 #include "beam.hpp"
 #include "launch.hpp"
 #include "recurrence.hpp"
@@ -233,7 +234,7 @@ __global__ void __launch_bounds__(kThreadsRow) beam_rows_kernel(BeamArgs a) {
     // Else a bound that n to kRoom candidates are not below, or, where equals allow
     // none, the n-th largest.  Of its equals the first are taken.  The logits are read
     // again, from the caches: kept in registers for this they would take half of the
-    // waves' room (8 x 16 x 250001 fp32: 40.2 us, so 38.2).
+    // waves' room (8 x 16 x 250001 fp32: 40.3 us, so 38.2).
     const auto all = [&](auto f) { L::again(base, first, (int)p.vocab, f); };
     const auto number = [&](auto f) {
       int c = 0;

@@ -150,3 +150,19 @@ def test_search_captured():
         s.step()
         trail.append((s.parents.tolist(), s.tokens.tolist()))
     check(found, s, trail)
+
+
+def test_search_on_a_side_stream():
+    """Every call follows the current stream: nothing waits for the other one, which is kept busy."""
+    w = weights(SEED)
+    found, busy, side = reference(w), torch.randn(4096, 4096, device="cuda"), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        s, trail = Search(w), []
+    for _ in range(STEPS):
+        busy @ busy
+        with torch.cuda.stream(side):
+            s.step()
+            trail.append((s.parents.clone(), s.tokens.clone()))
+    torch.cuda.synchronize()
+    check(found, s, [(p.tolist(), t.tolist()) for p, t in trail])
