@@ -44,17 +44,19 @@ namespace {
 // for the stores, one load more for each look and two more for each hand-over.
 constexpr int kMaxSpinsChain = 1 << 20;
 constexpr uint32_t kUnset = 0xffffffffu;
-constexpr int kChainHeader = 64;  // bytes before the values: status word, ticket
+constexpr int kChainHeader = 64;  // bytes before the values: status word, tickets
 
 struct Chain {
   int* status;    // null: one piece a stream, nothing is handed on
-  int* ticket;
+  int* ticket;    // one for each share of the streams
   uint64_t* own;  // [place][stream][64 V]: A, H
   float* end;     // [place][stream][64 V]
-  int streams;
+  uint32_t streams;
+  uint32_t shares;      // of the streams: 1, or one for each die
+  uint32_t each, more;  // streams of a share, and how many shares have one more
 };
 
-// Status word and ticket to 0, the rest (n times 16 bytes) to unset.
+// Status word and tickets to 0, the rest (n times 16 bytes) to unset.
 __global__ void __launch_bounds__(256) chain_clear_kernel(u32x4* p, int64_t n) {
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
     const uint32_t v = i < kChainHeader / 16 ? 0u : kUnset;
@@ -167,6 +169,35 @@ __device__ __forceinline__ void chain_carry(const Chain& c, int place, int strea
   put_end<V>(c.end + off, h);
 }
 
+// Which piece a workgroup works on.  Neighbouring workgroups start on different dies,
+// each with a cache of its own, while a row's neighbouring channels have lines in common
+// where rows are not whole lines.  So each die has a share of neighbouring streams, and
+// takes from another's when its own has run out (there are as many pieces as
+// workgroups: each finds one).  Only the speed depends on which die a workgroup runs on.
+struct Turn {
+  int place, stream;
+};
+constexpr uint32_t kDies = 8;
+__device__ __forceinline__ Turn take_turn(const Chain& c, uint32_t pieces, Turn* lds) {
+  const auto first = [&](uint32_t g) { return g * c.each + (g < c.more ? g : c.more); };
+  const uint32_t mask = c.shares - 1, own = blockIdx.x & mask;
+  if (c.status == nullptr) return Turn{0, (int)(first(own) + (blockIdx.x >> __popc(mask)))};
+  if (threadIdx.x == 0) {
+    for (uint32_t i = 0; i < c.shares; ++i) {
+      const uint32_t g = (own + i) & mask, n = c.each + (g < c.more);
+      if (n == 0) continue;
+      const uint32_t t = (uint32_t)atomicAdd(c.ticket + g, 1);
+      if (t < n * pieces) {
+        const uint32_t place = t / n;
+        *lds = Turn{(int)place, (int)(first(g) + t - place * n)};
+        break;
+      }
+    }
+  }
+  __syncthreads();
+  return Turn{__builtin_amdgcn_readfirstlane(lds->place), __builtin_amdgcn_readfirstlane(lds->stream)};
+}
+
 // ------------------------------------------------------------ rows
 // Rows r0, r0 + 1, .. of a tensor, one descriptor each (its base in scalar
 // registers, a lane's channel as the offset: no address arithmetic in the vector
@@ -208,11 +239,12 @@ __device__ __forceinline__ float widen_at(uint32_t w, int v) {
   if constexpr (!BF16) return __uint_as_float(w);
   else return v == 0 ? bf16_lo(w) : bf16_hi(w);
 }
-// Not to take the place of what is read next in the caches (backward of 8 x 2048 x
-// 1536: 93 -> 80 us, 4 x 8192 x 5120: 507 -> 502).
+// Stores that do not take the place of what is read next in the caches (backward of 8 x
+// 2048 x 1536: 93 -> 80 us, 4 x 8192 x 5120: 507 -> 502), for whole lines; parts of lines
+// go to memory one by one then.
 constexpr int kNonTemporal = 2;
 // Rows past the n-th are not stored, nor what a lane without channels has.
-template <bool BF16, int V>
+template <bool BF16, int V, int AUX>
 __device__ __forceinline__ void store_row(const Rows<BF16>& r, int j, int n, uint32_t off, const float (&o)[V]) {
   const rsrc_t d = make_rsrc(r.at + j * r.step, j < n ? r.bytes : 0u);
   if constexpr (BF16 && V == 1) {
@@ -221,7 +253,7 @@ __device__ __forceinline__ void store_row(const Rows<BF16>& r, int j, int n, uin
     uint32_t v;
     if constexpr (BF16) v = pack_bf16x2(o[0], o[1]);
     else v = __float_as_uint(o[0]);
-    __builtin_amdgcn_raw_buffer_store_b32(v, d, (int)off, 0, kNonTemporal);
+    __builtin_amdgcn_raw_buffer_store_b32(v, d, (int)off, 0, AUX);
   }
 }
 
@@ -240,11 +272,11 @@ struct WavePlace {
 // one with half a pair, as the second of the last two: what two lanes write there is
 // the same.
 template <bool BF16, int V, int W, int T>
-__device__ __forceinline__ WavePlace<V, W, T> wave_place(int64_t id, int streams, int blocks, int64_t pieces,
-                                                         bool reversed, int64_t seqlen, int64_t dim) {
+__device__ __forceinline__ WavePlace<V, W, T> wave_place(Turn turn, int blocks, int64_t pieces, bool reversed,
+                                                         int64_t seqlen, int64_t dim) {
   WavePlace<V, W, T> w;
-  w.place = (int)(id / streams);
-  w.stream = (int)(id - (int64_t)w.place * streams);
+  w.place = turn.place;
+  w.stream = turn.stream;
   w.wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   w.b = w.stream / blocks;
   const int64_t piece = reversed ? pieces - 1 - w.place : w.place;
@@ -314,17 +346,13 @@ struct FwdArgs {
 template <bool BF16, int V, int W, int T, bool STARTS>
 __global__ void __launch_bounds__(W * 64) __attribute__((amdgpu_waves_per_eu(4))) recurrence_fwd_kernel(FwdArgs a) {
   __shared__ float lds_a[W][64 * V], lds_h[W][64 * V], lds_carry[64 * V];
-  __shared__ int lds_cut[W], lds_id;
+  __shared__ int lds_cut[W];
+  __shared__ Turn lds_turn;
   const RecurrenceFwdParams& p = a.p;
-  int64_t id = blockIdx.x;
-  if (a.chain.status != nullptr) {
-    if (threadIdx.x == 0) lds_id = atomicAdd(a.chain.ticket, 1);
-    __syncthreads();
-    id = __builtin_amdgcn_readfirstlane(lds_id);
-  } else if (id == 0 && threadIdx.x == 0) {
+  const Turn turn = take_turn(a.chain, (uint32_t)a.pieces, &lds_turn);
+  if (a.chain.status == nullptr && blockIdx.x == 0 && threadIdx.x == 0)
     *static_cast<int*>(p.workspace) = 0;  // the status word: nothing waits
-  }
-  const auto w = wave_place<BF16, V, W, T>(id, a.chain.streams, a.blocks, a.pieces, false, p.seqlen, p.dim);
+  const auto w = wave_place<BF16, V, W, T>(turn, a.blocks, a.pieces, false, p.seqlen, p.dim);
   const int lane = threadIdx.x & 63;
   const int64_t row0 = w.b * p.seqlen + w.t0;
 
@@ -410,7 +438,7 @@ __global__ void __launch_bounds__(W * 64) __attribute__((amdgpu_waves_per_eu(4))
     float o[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) o[v] = cut ? hl[j][v] : __builtin_fmaf(pr[j][v], q[v], hl[j][v]);
-    store_row<BF16, V>(y, j, w.n, w.out, o);
+    store_row<BF16, V, kNonTemporal>(y, j, w.n, w.out, o);
     if (p.h_last != nullptr && w.ok && w.t0 + j == p.seqlen - 1)
 #pragma unroll
       for (int v = 0; v < V; ++v) p.h_last[w.b * p.dim + w.ch + v] = o[v];
@@ -434,22 +462,18 @@ constexpr float kLeastNormal = 1.1754944e-38f;
 // registers until the gradients, the gates' exponentials in LDS (each lane its
 // own).  With w = dx x:
 //   dx = g i beta,  dgate_x = w (1 - i),  G = s a (a w / beta^2 - g h_{t-1}).
-template <bool BF16, int V, int W, int T, bool STARTS>
+template <bool BF16, int V, int W, int T, bool STARTS, int AUX>
 __global__ void __launch_bounds__(W * 64) __attribute__((amdgpu_waves_per_eu(4))) recurrence_bwd_kernel(BwdArgs a) {
   static_assert(W * T == kRecurrenceChunk, "");
   extern __shared__ __align__(16) float lds_kept[];  // [2][W][T][64 V]
   __shared__ float lds_a[W][64 * V], lds_h[W][64 * V], lds_e[W][64 * V], lds_carry[64 * V];
-  __shared__ int lds_cut[W], lds_id;
+  __shared__ int lds_cut[W];
+  __shared__ Turn lds_turn;
   const RecurrenceBwdParams& p = a.p;
-  int64_t id = blockIdx.x;
-  if (a.chain.status != nullptr) {
-    if (threadIdx.x == 0) lds_id = atomicAdd(a.chain.ticket, 1);
-    __syncthreads();
-    id = __builtin_amdgcn_readfirstlane(lds_id);
-  } else if (id == 0 && threadIdx.x == 0) {
+  const Turn turn = take_turn(a.chain, (uint32_t)a.pieces, &lds_turn);
+  if (a.chain.status == nullptr && blockIdx.x == 0 && threadIdx.x == 0)
     *static_cast<int*>(p.workspace) = 0;  // the status word: nothing waits
-  }
-  const auto w = wave_place<BF16, V, W, T>(id, a.chain.streams, a.blocks, a.pieces, true, p.seqlen, p.dim);
+  const auto w = wave_place<BF16, V, W, T>(turn, a.blocks, a.pieces, true, p.seqlen, p.dim);
   const int lane = threadIdx.x & 63;
   const int64_t row0 = w.b * p.seqlen + w.t0, piece = a.pieces - 1 - w.place;
 
@@ -586,9 +610,9 @@ __global__ void __launch_bounds__(W * 64) __attribute__((amdgpu_waves_per_eu(4))
       dlam[v] += j < w.n ? big : 0.0f;
       e[v] = start ? 0.0f : __builtin_fmaf(n[j][v], g, g);
     }
-    store_row<BF16, V>(dx, j, w.n, w.out, ox);
-    store_row<BF16, V>(da, j, w.n, w.out, oa);
-    store_row<BF16, V>(di, j, w.n, w.out, oi);
+    store_row<BF16, V, AUX>(dx, j, w.n, w.out, ox);
+    store_row<BF16, V, AUX>(da, j, w.n, w.out, oa);
+    store_row<BF16, V, AUX>(di, j, w.n, w.out, oi);
     if (j % 2 == 0) __builtin_amdgcn_sched_barrier(0);  // no more than two steps at once: registers
   }
   if (w.wave == 0 && piece == 0 && p.dh0 != nullptr && w.ok)
@@ -633,9 +657,12 @@ Cut cut_of(int64_t batch, int64_t seqlen, int64_t dim, int v, int steps) {
   return c;
 }
 
-hipError_t start_chain(const Cut& c, void* workspace, Chain& chain, hipStream_t stream) {
+hipError_t start_chain(const Cut& c, uint32_t shares, void* workspace, Chain& chain, hipStream_t stream) {
   char* base = static_cast<char*>(workspace);
-  chain.streams = (int)c.streams;
+  chain.streams = (uint32_t)c.streams;
+  chain.shares = c.pieces == 1 ? kDies : shares;
+  chain.each = chain.streams / chain.shares;
+  chain.more = chain.streams % chain.shares;
   chain.status = nullptr;
   if (c.pieces == 1) return hipSuccess;
   chain.status = reinterpret_cast<int*>(base);
@@ -660,13 +687,25 @@ template <bool BF16, int V>
 hipError_t launch_fwd(const RecurrenceFwdParams& p, hipStream_t stream) {
   const Cut c = cut_of(p.batch, p.seqlen, p.dim, V, kWaves * kFwdSteps);
   FwdArgs a{p, {}, (int)c.blocks, c.pieces};
-  const hipError_t e = start_chain(c, p.workspace, a.chain, stream);
+  const hipError_t e = start_chain(c, 1, p.workspace, a.chain, stream);
   if (e != hipSuccess) return e;
   const auto kernel = p.starts != nullptr ? recurrence_fwd_kernel<BF16, V, kWaves, kFwdSteps, true>
                                           : recurrence_fwd_kernel<BF16, V, kWaves, kFwdSteps, false>;
   hipLaunchKernelGGL(kernel, dim3((unsigned)(c.streams * c.pieces)), dim3(kWaves * 64), 0, stream, a);
   return hipGetLastError();
 }
+
+// Rows of which the 64 channels of a wave are whole half lines.
+template <bool BF16>
+bool whole_lines(const void* p, int64_t stride) {
+  return ((reinterpret_cast<uintptr_t>(p) | (uint64_t)stride * (BF16 ? 2 : 4)) & 63u) == 0;
+}
+// Gradients of other rows: a share of the streams for each die where there are many
+// (4 x 8192 x 2561 fp32 586 -> 532 us, 8 x 2048 x 1537 192 -> 165; few wait for each other,
+// 32768 x 770 bf16 139 -> 167), and plain stores once the tensors together are beyond the
+// last-level cache (706 -> 586 us, 6 x 11725 x 2099 1274 -> 1034; but 3 x 4099 x 1001 90 -> 99).
+// The forward, with one output beside three inputs, gains from neither.
+constexpr int64_t kManyStreams = 48, kNearBytes = 64ll << 20;
 
 size_t bwd_part_offset(const Cut& c) { return (c.bytes + 255) / 256 * 256; }
 
@@ -677,10 +716,16 @@ hipError_t launch_bwd(const RecurrenceBwdParams& p, hipStream_t stream) {
   const int64_t parts = p.batch * c.pieces;
   float* part = reinterpret_cast<float*>(static_cast<char*>(p.workspace) + bwd_part_offset(c));
   BwdArgs a{p, {}, parts > 1 ? part : p.dlam, (int)c.blocks, c.pieces};
-  hipError_t e = start_chain(c, p.workspace, a.chain, stream);
+  const bool whole = whole_lines<BF16>(p.dx, p.dx_stride) && whole_lines<BF16>(p.dgate_a, p.dgate_a_stride) &&
+                     whole_lines<BF16>(p.dgate_x, p.dgate_x_stride);
+  hipError_t e = start_chain(c, !whole && c.streams >= kManyStreams ? kDies : 1, p.workspace, a.chain, stream);
   if (e != hipSuccess) return e;
-  const auto kernel = p.starts != nullptr ? recurrence_bwd_kernel<BF16, V, kWaves, kBwdSteps, true>
-                                          : recurrence_bwd_kernel<BF16, V, kWaves, kBwdSteps, false>;
+  const bool past = whole || p.batch * p.seqlen * p.dim * (BF16 ? 2 : 4) <= kNearBytes;
+  const auto kernel = p.starts != nullptr
+                          ? past ? recurrence_bwd_kernel<BF16, V, kWaves, kBwdSteps, true, kNonTemporal>
+                                 : recurrence_bwd_kernel<BF16, V, kWaves, kBwdSteps, true, 0>
+                          : past ? recurrence_bwd_kernel<BF16, V, kWaves, kBwdSteps, false, kNonTemporal>
+                                 : recurrence_bwd_kernel<BF16, V, kWaves, kBwdSteps, false, 0>;
   hipLaunchKernelGGL(kernel, dim3((unsigned)(c.streams * c.pieces)), dim3(kWaves * 64),
                      2 * kRecurrenceChunk * 64 * V * sizeof(float), stream, a);
   e = hipGetLastError();

@@ -46,6 +46,28 @@ def test_recurrence_past_32_bit_offsets(batch, length, dim):
     assert torch.equal(small["dh0"], grads["dh0"][rows, cols])
 
 
+@pytest.mark.parametrize("io,batch,length,dim", [("fp32", 40, 3001, 161), ("bf16", 40, 6001, 161), ("fp32", 25, 130, 6011),
+                                                 ("fp32", 60, 700, 33), ("bf16", 9, 200, 901), ("fp32", 70, 20, 515)])
+def test_many_streams_of_rows_that_are_no_whole_lines(io, batch, length, dim):
+    """Below and beyond the last-level cache, several pieces or one: the last batch rows against a call of their own."""
+    g = gen(5)
+    dtype = torch.float32 if io == "fp32" else torch.bfloat16
+    x, a, i, dy = (torch.randn(batch, length, dim, generator=g, device="cuda:0").to(dtype) for _ in range(4))
+    starts = torch.rand(batch, length, generator=g, device="cuda:0") < 0.002
+    lam = torch.randn(dim, generator=g, device="cuda:0") - 3
+    y, last, states = mss.gated_recurrence_fwd(x, a, i, lam, starts=starts, return_last_state=True, keep_states=True,
+                                               check_waits=True)
+    grads = mss.gated_recurrence_bwd(dy, x, a, i, lam, states, starts=starts, want_dh0=True, check_waits=True)
+    for rows in (slice(0, 1), slice(batch // 2, batch // 2 + 2), slice(batch - 1, batch)):
+        z, zlast, zstates = mss.gated_recurrence_fwd(x[rows], a[rows], i[rows], lam, starts=starts[rows],
+                                                     return_last_state=True, keep_states=True)
+        assert torch.equal(z, y[rows]) and torch.equal(zlast, last[rows]) and torch.equal(zstates, states[rows])
+        small = mss.gated_recurrence_bwd(dy[rows], x[rows], a[rows], i[rows], lam, zstates, starts=starts[rows],
+                                         want_dh0=True)
+        for k in ("dx", "dgate_a", "dgate_x", "dh0"):
+            assert torch.equal(small[k], grads[k][rows]), (k, rows)
+
+
 @pytest.mark.parametrize("batch,length,dim", [(70001, 1, 1), (70001, 3, 2), (66000, 70, 3)])
 def test_recurrence_of_many_rows(batch, length, dim):
     g = gen(2)
