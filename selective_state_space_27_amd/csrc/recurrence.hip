@@ -30,7 +30,7 @@ namespace {
 // ------------------------------------------------------------ pieces in order
 // A piece is one workgroup's steps of one stream (64 V channels of a batch row).
 // Pieces take their place in order of start (a ticket): s-th in its stream, all
-// streams' s-th before any (s+1)-th.  A piece that has its own A and H publishes
+// s-th of a share of the streams before any (s+1)-th of it.  A piece that has its own A and H publishes
 // them, looks back for the nearest piece whose end state is known, folds what
 // lies between from there on, and publishes its own end state.  The fold is the
 // same sequence of operations wherever it begins, so results do not depend on
@@ -704,7 +704,7 @@ bool whole_lines(const void* p, int64_t stride) {
 // (4 x 8192 x 2561 fp32 586 -> 532 us, 8 x 2048 x 1537 192 -> 165; few wait for each other,
 // 32768 x 770 bf16 139 -> 167), and plain stores once the tensors together are beyond the
 // last-level cache (706 -> 586 us, 6 x 11725 x 2099 1274 -> 1034; but 3 x 4099 x 1001 90 -> 99).
-// The forward, with one output beside three inputs, gains from neither.
+// The forward, with one output beside three inputs, gains little or loses.
 constexpr int64_t kManyStreams = 48, kNearBytes = 64ll << 20;
 
 size_t bwd_part_offset(const Cut& c) { return (c.bytes + 255) / 256 * 256; }
