@@ -265,12 +265,14 @@ struct WavePlace {
   int n;             // steps that exist
   uint32_t ch;       // first channel, kept inside the row
   bool ok;           // whether it exists
+  bool any_rate;     // the workgroup takes the polynomial for all decays whatever its channels'
   uint32_t in, out;  // its offset in a row for loads, and for stores
 };
 
 // `piece` in order along time.  A lane past the last channel repeats it, and so does
 // one with half a pair, as the second of the last two: what two lanes write there is
-// the same.
+// the same.  Where that one is alone in its workgroup the other of the two belongs to
+// the workgroup before as well, and both have to take the same polynomial.
 template <bool BF16, int V, int W, int T>
 __device__ __forceinline__ WavePlace<V, W, T> wave_place(Turn turn, int blocks, int64_t pieces, bool reversed,
                                                          int64_t seqlen, int64_t dim) {
@@ -288,6 +290,7 @@ __device__ __forceinline__ WavePlace<V, W, T> wave_place(Turn turn, int blocks, 
   w.ch = (uint32_t)(c + V <= dim ? c : dim - V);
   w.in = w.ch * (BF16 ? 2u : 4u);
   w.out = w.ok ? w.in : kOffNone;
+  w.any_rate = V == 2 && dim % (64 * V) == 1 && w.stream - (int)w.b * blocks >= blocks - 2;
   return w;
 }
 
@@ -366,7 +369,7 @@ __global__ void __launch_bounds__(W * 64) __attribute__((amdgpu_waves_per_eu(4))
   load_rows<BF16, V, T>(Rows<BF16>(p.x, row0, p.x_stride, p.dim), w.in, w.n, 0u, rx);
   const uint64_t starts = STARTS ? __ballot(mark != 0) : 0;
   float k[V];
-  bool slow = true;
+  bool slow = !w.any_rate;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     k[v] = decay_rate(p.c, lam[v]);
@@ -491,7 +494,7 @@ __global__ void __launch_bounds__(W * 64) __attribute__((amdgpu_waves_per_eu(4))
   load_rows<BF16, V, T>(Rows<BF16>(p.dy, row0, p.dy_stride, p.dim), w.in, w.n, 0u, rd);
   const uint64_t starts = STARTS ? __ballot(mark != 0) : 0;
   float k[V];
-  bool slow = true;
+  bool slow = !w.any_rate;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     k[v] = decay_rate(p.c, lam[v]);
@@ -677,11 +680,8 @@ hipError_t start_chain(const Cut& c, uint32_t shares, void* workspace, Chain& ch
 
 // bf16 channels go in pairs, a word a lane, which the hardware reads and writes at any
 // alignment (at odd ones, 3 x 4099 x 1001, 39 us forward and 61 us backward, against 43
-// and 70 with one channel a lane).  Not where the last channel would be alone in a
-// workgroup: the one before it, repeated to make a pair, would belong to two
-// workgroups, which may take different polynomials for the decay, and what is stored
-// would be either's.
-bool in_pairs(int64_t dim, bool bf16) { return bf16 && dim % 128 != 1; }
+// and 70 with one channel a lane); a row of one channel has none.
+bool in_pairs(int64_t dim, bool bf16) { return bf16 && dim > 1; }
 
 template <bool BF16, int V>
 hipError_t launch_fwd(const RecurrenceFwdParams& p, hipStream_t stream) {
