@@ -43,7 +43,8 @@ namespace {
 // whether a value is there and what it is; flags beside the values took a wait
 // for the stores, one load more for each look and two more for each hand-over.
 constexpr int kMaxSpinsChain = 1 << 20;
-constexpr uint32_t kUnset = 0xffffffffu;
+constexpr uint32_t kUnset = 0xffffffffu, kNaN = 0x7fc00000u, kCutMark = 0x7fc0c0c0u;
+constexpr int kGroup = 8;  // pieces
 constexpr int kChainHeader = 64;  // bytes before the values: status word, tickets
 
 struct Chain {
@@ -51,6 +52,8 @@ struct Chain {
   int* ticket;    // one for each share of the streams
   uint64_t* own;  // [place][stream][64 V]: A, H
   float* end;     // [place][stream][64 V]
+  uint64_t* group_own;  // [group][stream][64 V], or null: no groups
+  float* group_end;
   uint32_t streams;
   uint32_t shares;      // of the streams: 1, or one for each die
   uint32_t each, more;  // streams of a share, and how many shares have one more
@@ -66,7 +69,7 @@ __global__ void __launch_bounds__(256) chain_clear_kernel(u32x4* p, int64_t n) {
 
 __device__ __forceinline__ uint32_t set_bits(float v) {
   const uint32_t u = __float_as_uint(v);
-  return u == kUnset ? 0x7fc00000u : u;
+  return u == kUnset ? kNaN : u;
 }
 template <int V>
 __device__ __forceinline__ void put_end(float* p, const float (&h)[V]) {
@@ -135,6 +138,28 @@ __device__ __forceinline__ bool chain_look(const Chain& c, int place, int stream
   return true;
 }
 
+// Never expected; keeps every wait finite, reported through the status word.
+__device__ __forceinline__ bool gives_up(const Chain& c, int spins) {
+  if (spins <= kMaxSpinsChain) return false;
+  if ((threadIdx.x & 63) == 0) __hip_atomic_store(c.status, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  return true;
+}
+
+// Mostly the piece before has ended (a first look at four places: 2 x 16384 x 5120
+// backward 556 us, with one at one place 523; with 20 streams or fewer the same).
+template <int V>
+__device__ __forceinline__ void chain_wait(const Chain& c, int place, int stream, float (&carry)[V]) {
+  bool found = chain_look<V, 1>(c, place, stream, carry);
+  for (int spins = 0; !found; ++spins) {
+    found = chain_look<V, 4>(c, place, stream, carry);
+    if (!found && gives_up(c, spins)) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) carry[v] = 0.0f;
+      break;
+    }
+  }
+}
+
 // What enters the piece at `place` of `stream` (wave 0's lanes; `first` at place
 // 0), given its own A and H; publishes what later pieces need.  `cut`: a sequence
 // starts inside, so its end state does not depend on what enters.
@@ -149,24 +174,100 @@ __device__ __forceinline__ void chain_carry(const Chain& c, int place, int strea
     for (int v = 0; v < V; ++v) carry[v] = first[v];
   } else {
     if (!cut && !last) put_own<V>(c.own + off, own_a, own_h);
-    // Mostly the piece before has ended (a first look at four places: 2 x 16384 x 5120
-    // backward 556 us, with one at one place 523; with 20 streams or fewer the same).
-    bool found = chain_look<V, 1>(c, place, stream, carry);
-    for (int spins = 0; !found; ++spins) {
-      found = chain_look<V, 4>(c, place, stream, carry);
-      if (!found && spins > kMaxSpinsChain) {  // never expected; keeps every wait finite, reported through the status word
-        if ((threadIdx.x & 63) == 0) __hip_atomic_store(c.status, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-#pragma unroll
-        for (int v = 0; v < V; ++v) carry[v] = 0.0f;
-        break;
-      }
-    }
+    chain_wait<V>(c, place, stream, carry);
   }
   if (cut || last) return;
   float h[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) h[v] = __builtin_fmaf(own_a[v], carry[v], own_h[v]);
   put_end<V>(c.end + off, h);
+}
+
+// The same with few streams, where the way of a state from piece to piece is what
+// takes the time (a look is a trip to memory, and one brings it four pieces on).  Eight
+// pieces are a group, whose A and H its last piece forms and hands on as above, so a
+// look brings a state four groups on; inside its group a piece folds what is before it.
+// Each of these folds, too, is always the same.  A piece in which a sequence starts has
+// a mark for its A.
+template <int V>
+__device__ __forceinline__ void group_fold(const Chain& c, int from, int n, int stream, float (&a)[V], float (&x)[V],
+                                           bool& cut) {
+  uint64_t own[4][V];
+  for (int spins = 0;; ++spins) {
+    bool there = true;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int64_t off = ((int64_t)(from + (q < n ? q : 0)) * c.streams + stream) * (64 * V);
+        own[q][v] = __hip_atomic_load(c.own + off + (threadIdx.x & 63) * V + v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        there = there && is_set(own[q][v]);
+      }
+    if (__all(there) || gives_up(c, spins)) break;
+  }
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    if (q >= n) continue;
+    const bool mark = __any((uint32_t)own[q][0] == kCutMark);
+    cut = cut || mark;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const float pa = __uint_as_float((uint32_t)own[q][v]), px = __uint_as_float((uint32_t)(own[q][v] >> 32));
+      x[v] = mark ? px : __builtin_fmaf(pa, x[v], px);
+      a[v] *= pa;
+    }
+  }
+}
+template <int V>
+__device__ __forceinline__ void group_carry(const Chain& c, int place, int stream, bool last, bool cut,
+                                            const float (&own_a)[V], const float (&own_h)[V], const float (&first)[V],
+                                            float (&carry)[V]) {
+  const int group = place / kGroup, before = place % kGroup;
+  const int64_t lane = (threadIdx.x & 63) * V;
+  if (!last) {
+    const float mark = __uint_as_float(kCutMark);
+    float pa[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) pa[v] = cut ? mark : __float_as_uint(own_a[v]) == kCutMark ? __uint_as_float(kNaN) : own_a[v];
+    put_own<V>(c.own + ((int64_t)place * c.streams + stream) * (64 * V) + lane, pa, own_h);
+  }
+  float a[V], x[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) a[v] = 1.0f, x[v] = 0.0f;
+  bool apart = false;  // a sequence starts in the group, before this piece
+  for (int q = 0; q < before; q += 4)
+    group_fold<V>(c, group * kGroup + q, before - q < 4 ? before - q : 4, stream, a, x, apart);
+  const bool hands = before == kGroup - 1 && !last;
+  const int64_t off = ((int64_t)group * c.streams + stream) * (64 * V) + lane;
+  float ga[V], gx[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    ga[v] = a[v] * own_a[v];
+    gx[v] = cut ? own_h[v] : __builtin_fmaf(own_a[v], x[v], own_h[v]);
+  }
+  if (hands && (apart || cut)) put_end<V>(c.group_end + off, gx);
+  else if (hands && group > 0) put_own<V>(c.group_own + off, ga, gx);
+  if (apart) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) carry[v] = x[v];
+    return;
+  }
+  float enters[V];
+  if (group == 0) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) enters[v] = first[v];
+  } else {
+    Chain g = c;
+    g.own = c.group_own;
+    g.end = c.group_end;
+    chain_wait<V>(g, group, stream, enters);
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    carry[v] = __builtin_fmaf(a[v], enters[v], x[v]);
+    gx[v] = __builtin_fmaf(ga[v], enters[v], gx[v]);
+  }
+  if (hands && !cut) put_end<V>(c.group_end + off, gx);
 }
 
 // Which piece a workgroup works on.  Neighbouring workgroups start on different dies,
@@ -407,13 +508,16 @@ __global__ void __launch_bounds__(W * 64) __attribute__((amdgpu_waves_per_eu(4))
   if (w.wave == 0) {
     float first[V], carry[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) first[v] = p.h0 != nullptr && w.place == 0 ? p.h0[w.b * p.dim + w.ch + v] : 0.0f;
+    for (int v = 0; v < V; ++v) first[v] = p.h0 != nullptr && w.place < kGroup ? p.h0[w.b * p.dim + w.ch + v] : 0.0f;
     if (a.chain.status == nullptr) {
 #pragma unroll
       for (int v = 0; v < V; ++v) carry[v] = first[v];
     } else {
       fold_waves<V, W, false>(lds_a, lds_h, cuts, 1, W, ha, hh);
-      chain_carry<V>(a.chain, w.place, w.stream, w.place + 1 == a.pieces, cuts != 0, ha, hh, first, carry);
+      if (a.chain.group_own == nullptr)
+        chain_carry<V>(a.chain, w.place, w.stream, w.place + 1 == a.pieces, cuts != 0, ha, hh, first, carry);
+      else
+        group_carry<V>(a.chain, w.place, w.stream, w.place + 1 == a.pieces, cuts != 0, ha, hh, first, carry);
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) lds_carry[lane * V + v] = carry[v], ha[v] = 1.0f, hh[v] = 0.0f;
@@ -549,7 +653,7 @@ __global__ void __launch_bounds__(W * 64) __attribute__((amdgpu_waves_per_eu(4))
     float first[V], carry[V];
 #pragma unroll
     for (int v = 0; v < V; ++v)
-      first[v] = p.dh_last != nullptr && w.place == 0 ? p.dh_last[w.b * p.dim + w.ch + v] : 0.0f;
+      first[v] = p.dh_last != nullptr && w.place < kGroup ? p.dh_last[w.b * p.dim + w.ch + v] : 0.0f;
     if (a.chain.status == nullptr) {
 #pragma unroll
       for (int v = 0; v < V; ++v) carry[v] = first[v];
@@ -560,7 +664,10 @@ __global__ void __launch_bounds__(W * 64) __attribute__((amdgpu_waves_per_eu(4))
         pa[v] = ha[v] * ea[v];
         pe[v] = starts != 0 ? e[v] : __builtin_fmaf(ha[v], ee[v], e[v]);
       }
-      chain_carry<V>(a.chain, w.place, w.stream, w.place + 1 == a.pieces, cuts != 0, pa, pe, first, carry);
+      if (a.chain.group_own == nullptr)
+        chain_carry<V>(a.chain, w.place, w.stream, w.place + 1 == a.pieces, cuts != 0, pa, pe, first, carry);
+      else
+        group_carry<V>(a.chain, w.place, w.stream, w.place + 1 == a.pieces, cuts != 0, pa, pe, first, carry);
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) lds_carry[lane * V + v] = carry[v];
@@ -660,6 +767,11 @@ Cut cut_of(int64_t batch, int64_t seqlen, int64_t dim, int v, int steps) {
   return c;
 }
 
+// 131072 x 512 bf16 (4 streams) 238 us forward and 467 backward, with groups 135 and 266; 65536
+// x 1001 fp32 (16) 242 and 471, 234 and 466; with 20 to 160 streams groups take up to 6% longer
+// (4 x 8192 x 5120: 257 and 507, 269 and 539).
+constexpr int64_t kFewStreams = 16, kManyPieces = 32;
+
 hipError_t start_chain(const Cut& c, uint32_t shares, void* workspace, Chain& chain, hipStream_t stream) {
   char* base = static_cast<char*>(workspace);
   chain.streams = (uint32_t)c.streams;
@@ -672,6 +784,11 @@ hipError_t start_chain(const Cut& c, uint32_t shares, void* workspace, Chain& ch
   chain.ticket = chain.status + 1;
   chain.own = reinterpret_cast<uint64_t*>(base + c.own);
   chain.end = reinterpret_cast<float*>(base + c.end);
+  // Groups: their words take the place of the pieces' end states, of which there are none.
+  const bool grouped = c.streams <= kFewStreams && c.pieces >= kManyPieces;
+  const int64_t half = (int64_t)(c.bytes - c.end) / 2;
+  chain.group_end = grouped ? chain.end : nullptr;
+  chain.group_own = grouped ? reinterpret_cast<uint64_t*>(base + c.end + half) : nullptr;
   const int64_t n = (int64_t)(c.bytes / 16), groups = (n + 255) / 256;
   hipLaunchKernelGGL(chain_clear_kernel, dim3((unsigned)(groups < 2048 ? groups : 2048)), dim3(256), 0, stream,
                      reinterpret_cast<u32x4*>(base), n);

@@ -236,6 +236,38 @@ def test_same_call_same_bits():
         assert all(torch.equal(a, b) for a, b in zip(first, once()))
 
 
+@pytest.mark.parametrize("io", ["bf16", "fp32"])
+@pytest.mark.parametrize("length,starts", [(4096, 0.0), (4097, 0.0005), (7301, 0.0), (7301, 0.003), (9000, 0.0002)])
+def test_few_long_streams(io, length, starts):
+    """States handed on by groups of pieces: whole and part groups, starts in some of them, results that repeat."""
+    d = make(2, length, 70, io, length, starts=starts, lam=-6.0)
+    check(d, io)
+    first = None
+    for _ in range(5):
+        y, last, states = mss.gated_recurrence_fwd(*(d[k] for k in FWD), h0=d["h0"], starts=d["starts"],
+                                                   return_last_state=True, keep_states=True)
+        g = mss.gated_recurrence_bwd(d["dy"], *(d[k] for k in FWD), states, starts=d["starts"], dh_last=d["dh_last"],
+                                     want_dh0=True)
+        got = [y, last, states] + [g[k] for k in GRADS]
+        first = first or got
+        assert all(torch.equal(a, b) for a, b in zip(first, got))
+
+
+@pytest.mark.parametrize("at", [1000, 1024, 3000, 4095])
+def test_a_start_forgets_whatever_was_before_in_groups(at):
+    d = make(1, 6000, 40, "fp32", at, starts=1e-9)
+    d["starts"][:] = False
+    d["starts"][0, at] = True
+    clean = [mss.gated_recurrence_fwd(*(d[k] for k in FWD), h0=d["h0"], starts=d["starts"], keep_states=True)]
+    clean.append(mss.gated_recurrence_bwd(d["dy"], *(d[k] for k in FWD), clean[0][1], starts=d["starts"]))
+    d["x"][0, :at] = float("nan")
+    y, states = mss.gated_recurrence_fwd(*(d[k] for k in FWD), h0=d["h0"], starts=d["starts"], keep_states=True)
+    g = mss.gated_recurrence_bwd(d["dy"], *(d[k] for k in FWD), states, starts=d["starts"])
+    assert y[0, :at].isnan().all() and torch.equal(y[0, at:], clean[0][0][0, at:])
+    for k in ("dx", "dgate_a", "dgate_x"):
+        assert torch.equal(g[k][0, at:], clean[1][k][0, at:]), k
+
+
 @pytest.mark.parametrize("dim", [129, 257, 385])
 def test_a_last_channel_by_itself(dim):
     """Channels next to the last one decay fast, the last two slowly: each has one value, whoever computes it."""

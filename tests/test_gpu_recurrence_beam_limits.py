@@ -1,7 +1,9 @@
 """Largest sizes of the gated recurrence and of beam search: offsets past 32 bits,
 more rows than a grid's second axis holds.  A large call is compared bit for bit
 with a small one on a part of its data (a channel's arithmetic does not depend on
-where the channel lies), or with what was planted."""
+where the channel lies), or with what was planted.  Long sequences of few streams
+hand their states on by groups, with other roundings: the part's rows are repeated to
+as many as are not few."""
 import pytest
 import torch
 
@@ -35,15 +37,16 @@ def test_recurrence_past_32_bit_offsets(batch, length, dim):
     y, last, states = mss.gated_recurrence_fwd(x, a, i, lam, return_last_state=True, keep_states=True, check_waits=True)
     grads = mss.gated_recurrence_bwd(dy, x, a, i, lam, states, want_dh0=True, check_waits=True)
     rows, cols = slice(max(0, batch - 2), batch), slice(dim - 64, dim)
-    part = [t[rows, :, cols].contiguous() for t in (x, a, i, dy)]
+    n = min(2, batch)
+    part = [t[rows, :, cols].repeat(17, 1, 1) for t in (x, a, i, dy)]
     z, zlast, zstates = mss.gated_recurrence_fwd(*part[:3], lam[cols].contiguous(), return_last_state=True,
                                                  keep_states=True)
-    assert torch.equal(z, y[rows, :, cols]) and torch.equal(zlast, last[rows, cols])
-    assert torch.equal(zstates, states[rows, :, cols])
+    assert torch.equal(z[:n], y[rows, :, cols]) and torch.equal(zlast[-n:], last[rows, cols])
+    assert torch.equal(zstates[:n], states[rows, :, cols])
     small = mss.gated_recurrence_bwd(part[3], *part[:3], lam[cols].contiguous(), zstates, want_dh0=True)
     for k in ("dx", "dgate_a", "dgate_x"):
-        assert torch.equal(small[k], grads[k][rows, :, cols]), k
-    assert torch.equal(small["dh0"], grads["dh0"][rows, cols])
+        assert torch.equal(small[k][:n], grads[k][rows, :, cols]), k
+    assert torch.equal(small["dh0"][-n:], grads["dh0"][rows, cols])
 
 
 @pytest.mark.parametrize("io,batch,length,dim", [("fp32", 40, 3001, 161), ("bf16", 40, 6001, 161), ("fp32", 25, 130, 6011),
@@ -59,13 +62,15 @@ def test_many_streams_of_rows_that_are_no_whole_lines(io, batch, length, dim):
                                                check_waits=True)
     grads = mss.gated_recurrence_bwd(dy, x, a, i, lam, states, starts=starts, want_dh0=True, check_waits=True)
     for rows in (slice(0, 1), slice(batch // 2, batch // 2 + 2), slice(batch - 1, batch)):
-        z, zlast, zstates = mss.gated_recurrence_fwd(x[rows], a[rows], i[rows], lam, starts=starts[rows],
-                                                     return_last_state=True, keep_states=True)
-        assert torch.equal(z, y[rows]) and torch.equal(zlast, last[rows]) and torch.equal(zstates, states[rows])
-        small = mss.gated_recurrence_bwd(dy[rows], x[rows], a[rows], i[rows], lam, zstates, starts=starts[rows],
-                                         want_dh0=True)
+        n, many = rows.stop - rows.start, lambda t: t[rows].repeat(17, *[1] * (t.dim() - 1))  # noqa: E731
+        sx, sa, si, sdy, sstarts = (many(t) for t in (x, a, i, dy, starts))
+        z, zlast, zstates = mss.gated_recurrence_fwd(sx, sa, si, lam, starts=sstarts, return_last_state=True,
+                                                     keep_states=True)
+        assert torch.equal(z[:n], y[rows]) and torch.equal(zlast[-n:], last[rows])
+        assert torch.equal(zstates[:n], states[rows])
+        small = mss.gated_recurrence_bwd(sdy, sx, sa, si, lam, zstates, starts=sstarts, want_dh0=True)
         for k in ("dx", "dgate_a", "dgate_x", "dh0"):
-            assert torch.equal(small[k], grads[k][rows]), (k, rows)
+            assert torch.equal(small[k][-n:], grads[k][rows]), (k, rows)
 
 
 @pytest.mark.parametrize("batch,length,dim", [(70001, 1, 1), (70001, 3, 2), (66000, 70, 3)])
