@@ -160,8 +160,8 @@ __device__ __forceinline__ void chain_wait(const Chain& c, int place, int stream
   }
 }
 
-// What enters the piece at `place` of `stream` (wave 0's lanes; `first` at place
-// 0), given its own A and H; publishes what later pieces need.  `cut`: a sequence
+// What enters the piece at `place` of `stream` (wave 0's lanes; `first` the stream),
+// given its own A and H; publishes what later pieces need.  `cut`: a sequence
 // starts inside, so its end state does not depend on what enters.
 template <int V>
 __device__ __forceinline__ void chain_carry(const Chain& c, int place, int stream, bool last, bool cut,
@@ -447,7 +447,9 @@ struct FwdArgs {
   int64_t pieces;  // of a stream
 };
 
-template <bool BF16, int V, int W, int T, bool STARTS>
+// GROUPS apart: in one kernel each would cost the other registers (131072 x 512 bf16
+// backward 266 us, so 258).
+template <bool BF16, int V, int W, int T, bool STARTS, bool GROUPS>
 __global__ void __launch_bounds__(W * 64) __attribute__((amdgpu_waves_per_eu(4))) recurrence_fwd_kernel(FwdArgs a) {
   __shared__ float lds_a[W][64 * V], lds_h[W][64 * V], lds_carry[64 * V];
   __shared__ int lds_cut[W];
@@ -514,7 +516,7 @@ __global__ void __launch_bounds__(W * 64) __attribute__((amdgpu_waves_per_eu(4))
       for (int v = 0; v < V; ++v) carry[v] = first[v];
     } else {
       fold_waves<V, W, false>(lds_a, lds_h, cuts, 1, W, ha, hh);
-      if (a.chain.group_own == nullptr)
+      if constexpr (!GROUPS)
         chain_carry<V>(a.chain, w.place, w.stream, w.place + 1 == a.pieces, cuts != 0, ha, hh, first, carry);
       else
         group_carry<V>(a.chain, w.place, w.stream, w.place + 1 == a.pieces, cuts != 0, ha, hh, first, carry);
@@ -569,7 +571,7 @@ constexpr float kLeastNormal = 1.1754944e-38f;
 // registers until the gradients, the gates' exponentials in LDS (each lane its
 // own).  With w = dx x:
 //   dx = g i beta,  dgate_x = w (1 - i),  G = s a (a w / beta^2 - g h_{t-1}).
-template <bool BF16, int V, int W, int T, bool STARTS, int AUX>
+template <bool BF16, int V, int W, int T, bool STARTS, int AUX, bool GROUPS>
 __global__ void __launch_bounds__(W * 64) __attribute__((amdgpu_waves_per_eu(4))) recurrence_bwd_kernel(BwdArgs a) {
   static_assert(W * T == kRecurrenceChunk, "");
   extern __shared__ __align__(16) float lds_kept[];  // [2][W][T][64 V]
@@ -664,7 +666,7 @@ __global__ void __launch_bounds__(W * 64) __attribute__((amdgpu_waves_per_eu(4))
         pa[v] = ha[v] * ea[v];
         pe[v] = starts != 0 ? e[v] : __builtin_fmaf(ha[v], ee[v], e[v]);
       }
-      if (a.chain.group_own == nullptr)
+      if constexpr (!GROUPS)
         chain_carry<V>(a.chain, w.place, w.stream, w.place + 1 == a.pieces, cuts != 0, pa, pe, first, carry);
       else
         group_carry<V>(a.chain, w.place, w.stream, w.place + 1 == a.pieces, cuts != 0, pa, pe, first, carry);
@@ -767,7 +769,7 @@ Cut cut_of(int64_t batch, int64_t seqlen, int64_t dim, int v, int steps) {
   return c;
 }
 
-// 131072 x 512 bf16 (4 streams) 238 us forward and 467 backward, with groups 135 and 266; 65536
+// 131072 x 512 bf16 (4 streams) 238 us forward and 467 backward, with groups 133 and 258; 65536
 // x 1001 fp32 (16) 242 and 471, 234 and 466; with 20 to 160 streams groups take up to 6% longer
 // (4 x 8192 x 5120: 257 and 507, 269 and 539).
 constexpr int64_t kFewStreams = 16, kManyPieces = 32;
@@ -775,6 +777,7 @@ constexpr int64_t kFewStreams = 16, kManyPieces = 32;
 hipError_t start_chain(const Cut& c, uint32_t shares, void* workspace, Chain& chain, hipStream_t stream) {
   char* base = static_cast<char*>(workspace);
   chain.streams = (uint32_t)c.streams;
+  chain.group_own = nullptr;
   chain.shares = c.pieces == 1 ? kDies : shares;
   chain.each = chain.streams / chain.shares;
   chain.more = chain.streams % chain.shares;
@@ -806,8 +809,11 @@ hipError_t launch_fwd(const RecurrenceFwdParams& p, hipStream_t stream) {
   FwdArgs a{p, {}, (int)c.blocks, c.pieces};
   const hipError_t e = start_chain(c, 1, p.workspace, a.chain, stream);
   if (e != hipSuccess) return e;
-  const auto kernel = p.starts != nullptr ? recurrence_fwd_kernel<BF16, V, kWaves, kFwdSteps, true>
-                                          : recurrence_fwd_kernel<BF16, V, kWaves, kFwdSteps, false>;
+  const auto kernel = a.chain.group_own != nullptr
+                          ? p.starts != nullptr ? recurrence_fwd_kernel<BF16, V, kWaves, kFwdSteps, true, true>
+                                                : recurrence_fwd_kernel<BF16, V, kWaves, kFwdSteps, false, true>
+                          : p.starts != nullptr ? recurrence_fwd_kernel<BF16, V, kWaves, kFwdSteps, true, false>
+                                                : recurrence_fwd_kernel<BF16, V, kWaves, kFwdSteps, false, false>;
   hipLaunchKernelGGL(kernel, dim3((unsigned)(c.streams * c.pieces)), dim3(kWaves * 64), 0, stream, a);
   return hipGetLastError();
 }
@@ -838,11 +844,15 @@ hipError_t launch_bwd(const RecurrenceBwdParams& p, hipStream_t stream) {
   hipError_t e = start_chain(c, !whole && c.streams >= kManyStreams ? kDies : 1, p.workspace, a.chain, stream);
   if (e != hipSuccess) return e;
   const bool past = whole || p.batch * p.seqlen * p.dim * (BF16 ? 2 : 4) <= kNearBytes;
-  const auto kernel = p.starts != nullptr
-                          ? past ? recurrence_bwd_kernel<BF16, V, kWaves, kBwdSteps, true, kNonTemporal>
-                                 : recurrence_bwd_kernel<BF16, V, kWaves, kBwdSteps, true, 0>
-                          : past ? recurrence_bwd_kernel<BF16, V, kWaves, kBwdSteps, false, kNonTemporal>
-                                 : recurrence_bwd_kernel<BF16, V, kWaves, kBwdSteps, false, 0>;
+  constexpr int kNT = kNonTemporal;
+  const auto kernel = a.chain.group_own != nullptr
+                          ? p.starts != nullptr ? recurrence_bwd_kernel<BF16, V, kWaves, kBwdSteps, true, kNT, true>
+                                                : recurrence_bwd_kernel<BF16, V, kWaves, kBwdSteps, false, kNT, true>
+                      : past
+                          ? p.starts != nullptr ? recurrence_bwd_kernel<BF16, V, kWaves, kBwdSteps, true, kNT, false>
+                                                : recurrence_bwd_kernel<BF16, V, kWaves, kBwdSteps, false, kNT, false>
+                          : p.starts != nullptr ? recurrence_bwd_kernel<BF16, V, kWaves, kBwdSteps, true, 0, false>
+                                                : recurrence_bwd_kernel<BF16, V, kWaves, kBwdSteps, false, 0, false>;
   hipLaunchKernelGGL(kernel, dim3((unsigned)(c.streams * c.pieces)), dim3(kWaves * 64),
                      2 * kRecurrenceChunk * 64 * V * sizeof(float), stream, a);
   e = hipGetLastError();
