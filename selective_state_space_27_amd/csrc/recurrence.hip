@@ -13,9 +13,9 @@
 // NaN: A is not multiplied in but skipped (a start is the same for all channels,
 // so the choice is a scalar one).
 //
-// Bound by memory where there is enough to do: 4 x 8192 x 5120 bf16 forward 270 us (1.34
-// GB at 5.0 TB/s; a 1 GiB copy reaches 5.13), backward 502 us (2.35 GB, 4.7 TB/s);
-// 131072 x 2560 forward 521 us (5.1); 4 x 8192 x 2560 fp32 237 and 408 us (5.7).  The
+// Bound by memory where there is enough to do: 4 x 8192 x 5120 bf16 forward 257 us (1.34
+// GB at 5.2 TB/s; a 1 GiB copy reaches 5.13), backward 507 us (2.35 GB, 4.6 TB/s);
+// 131072 x 2560 forward 521 us (5.1); 4 x 8192 x 2560 fp32 235 and 431 us (5.7, 5.5).  The
 // vector unit follows: busy 60% of the forward and 71% of the backward (31 and 71
 // instructions for 64 values, five and eight of them transcendental, at a quarter of the
 // rate).  Odd rows of fp32 with starts (3 x 4099 x 1001) run at 4 TB/s.  With
