@@ -12,8 +12,13 @@ u = 2^-24:
   m = 1 - exp(-s): the relative error of s is not amplified, 8 u for the
     polynomial or the exponential and the difference;
   sqrt(m (2 - m)): half of m's, 4 u;
-  a step h + (b - m h): m's error on m |h|, 4 u of the sum of magnitudes (the
-    part of the state from before a piece of the sequence and the part from
+  a = exp(-s): up to s = 1/2 as 1 - m, off by m's error; beyond it is the
+    exponential itself, whose relative error is s times that of s, the rounding of
+    the argument (2 s u, or left out as for the sigmoid) and 4 u.  (At s = 1/2 the
+    first is the larger of the two whatever the gate, so it does not matter on
+    which side a rounding of s falls.)  Below 2^-126 the exponential is 0;
+  a step h + (b - m h) or a h + b: a's error on |h|, 4 u of the sum of magnitudes
+    (the part of the state from before a piece of the sequence and the part from
     inside it are formed apart and added).
 """
 from __future__ import annotations
@@ -50,6 +55,8 @@ class Parts:
         self.e_r, self.e_i = (8 + arg * np.abs(gate_a)) * U, (8 + arg * np.abs(gate_x)) * U
         self.e_s = self.e_r + 8 * U
         self.e_m = self.e_s + 8 * U
+        beyond = self.a * (self.s * (self.e_s + arg * U) + 4 * U) + 2.0 ** -126
+        self.d_a = np.where(self.s > 0.5001, beyond, self.e_m * self.m)  # of a, absolute
         self.rate = np.exp(-np.logaddexp(0.0, -lam) - np.log(softplus(lam)))  # sigmoid / softplus
 
 
@@ -65,7 +72,7 @@ def forward(x, gate_a, gate_x, lam, c=8.0, h0=None, starts=None, exact=True):
     for t in range(x.shape[1]):
         keep = np.ones((x.shape[0], 1)) if starts is None else (np.asarray(starts)[:, t, None] == 0).astype(float)
         a = keep * p.a[:, t]
-        err = a * err + p.e_m[:, t] * keep * p.m[:, t] * size
+        err = a * err + p.d_a[:, t] * keep * size
         size = a * size + np.abs(b[:, t])
         err = err + 4 * U * size + e_b[:, t]
         h = a * h + b[:, t]
@@ -93,9 +100,9 @@ def backward(dy, x, gate_a, gate_x, lam, c=8.0, h0=None, starts=None, dh_last=No
         k = keep[:, t, None]
         carry = k * p.a[:, t] * g[:, t]
         size = k * p.a[:, t] * gs[:, t]
-        err = k * (p.a[:, t] * ge[:, t] + p.e_m[:, t] * p.m[:, t] * gs[:, t] + 4 * U * size)
+        err = k * (p.a[:, t] * ge[:, t] + p.d_a[:, t] * gs[:, t] + 4 * U * size)
     bi = p.beta * p.i
-    e_a = p.e_m * p.m + 2 * U  # of a, absolute
+    e_a = p.d_a + 2 * U * p.a
     with np.errstate(divide="ignore", invalid="ignore"):
         ratio = np.where(p.m > 0, p.s / p.beta, 0.0)
     ix, kb = np.abs(p.i * x), keep[:, :, None] * np.abs(before)

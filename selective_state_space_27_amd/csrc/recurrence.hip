@@ -489,10 +489,10 @@ __global__ void __launch_bounds__(W * 64) __attribute__((amdgpu_waves_per_eu(4))
       const bool start = STARTS && (starts >> j & 1);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const float n = exp_less_one<small()>(k[v] * sigmoid_of<!BF16>(widen_at<BF16, V>(ra[j], v)));
-        const float u = beta_of(n) * sigmoid_of<!BF16>(widen_at<BF16, V>(ri[j], v));
-        hh[v] = __builtin_fmaf(u, widen_at<BF16, V>(rx[j], v), start ? 0.0f : __builtin_fmaf(n, hh[v], hh[v]));
-        ha[v] = __builtin_fmaf(n, ha[v], ha[v]);
+        const float m = decay_of<small(), !BF16>(k[v] * sigmoid_of<!BF16>(widen_at<BF16, V>(ra[j], v)));
+        const float u = beta_of(rest_of<small()>(m)) * sigmoid_of<!BF16>(widen_at<BF16, V>(ri[j], v));
+        hh[v] = __builtin_fmaf(u, widen_at<BF16, V>(rx[j], v), start ? 0.0f : decayed<small()>(m, hh[v]));
+        ha[v] = decayed<small()>(m, ha[v]);
         hl[j][v] = hh[v];
         pr[j][v] = ha[v];
       }
@@ -567,7 +567,7 @@ struct BwdArgs {
 // nothing or 0, which must not meet an infinity.
 constexpr float kLeastNormal = 1.1754944e-38f;
 
-// One piece is one chunk: W T = kRecurrenceChunk.  Of a step, n and h_{t-1} stay in
+// One piece is one chunk: W T = kRecurrenceChunk.  Of a step, m and h_{t-1} stay in
 // registers until the gradients, the gates' exponentials in LDS (each lane its
 // own).  With w = dx x:
 //   dx = g i beta,  dgate_x = w (1 - i),  G = s a (a w / beta^2 - g h_{t-1}).
@@ -612,7 +612,7 @@ __global__ void __launch_bounds__(W * 64) __attribute__((amdgpu_waves_per_eu(4))
   typedef float vec __attribute__((ext_vector_type(V)));
   vec* const exp_a = reinterpret_cast<vec*>(lds_kept) + w.wave * (T * 64) + lane;
   vec* const exp_x = exp_a + W * T * 64;
-  float n[T][V], hl[T][V], ha[V], hh[V], e[V];
+  float m[T][V], hl[T][V], ha[V], hh[V], e[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) ha[v] = 1.0f, hh[v] = 0.0f, e[v] = 0.0f;
   const auto local = [&](auto small) {
@@ -624,10 +624,10 @@ __global__ void __launch_bounds__(W * 64) __attribute__((amdgpu_waves_per_eu(4))
       for (int v = 0; v < V; ++v) {
         ea[v] = exp_neg<!BF16>(widen_at<BF16, V>(ra[j], v));
         ex[v] = exp_neg<!BF16>(widen_at<BF16, V>(ri[j], v));
-        n[j][v] = exp_less_one<small()>(k[v] * rcp_fast(1.0f + ea[v]));
-        hh[v] = __builtin_fmaf(beta_of(n[j][v]) * rcp_fast(1.0f + ex[v]), widen_at<BF16, V>(rx[j], v),
-                               start ? 0.0f : __builtin_fmaf(n[j][v], hh[v], hh[v]));
-        ha[v] = __builtin_fmaf(n[j][v], ha[v], ha[v]);
+        m[j][v] = decay_of<small(), !BF16>(k[v] * rcp_fast(1.0f + ea[v]));
+        hh[v] = __builtin_fmaf(beta_of(rest_of<small()>(m[j][v])) * rcp_fast(1.0f + ex[v]), widen_at<BF16, V>(rx[j], v),
+                               start ? 0.0f : decayed<small()>(m[j][v], hh[v]));
+        ha[v] = decayed<small()>(m[j][v], ha[v]);
         e[v] = cut ? e[v] : __builtin_fmaf(ha[v], widen_at<BF16, V>(rd[j], v), e[v]);
         hl[j][v] = hh[v];
       }
@@ -679,15 +679,19 @@ __global__ void __launch_bounds__(W * 64) __attribute__((amdgpu_waves_per_eu(4))
   float q[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) q[v] = before[v];
+  const auto states = [&](auto small) {
 #pragma unroll
-  for (int j = 0; j < T; ++j) {
-    const bool start = STARTS && (starts >> j & 1);
+    for (int j = 0; j < T; ++j) {
+      const bool start = STARTS && (starts >> j & 1);
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      q[v] = start ? 0.0f : __builtin_fmaf(n[j][v], q[v], q[v]);
-      hl[j][v] += q[v];
+      for (int v = 0; v < V; ++v) {
+        q[v] = start ? 0.0f : decayed<small()>(m[j][v], q[v]);
+        hl[j][v] += q[v];
+      }
     }
-  }
+  };
+  if (__all(slow)) states(std::true_type{});
+  else states(std::false_type{});
   __syncthreads();
 
   const bool apart = (cuts >> w.wave >> 1) != 0;
@@ -701,32 +705,36 @@ __global__ void __launch_bounds__(W * 64) __attribute__((amdgpu_waves_per_eu(4))
   for (int v = 0; v < V; ++v) dlam[v] = 0.0f;
   const Rows<BF16> dx(p.dx, row0, p.dx_stride, p.dim), da(p.dgate_a, row0, p.dgate_a_stride, p.dim),
       di(p.dgate_x, row0, p.dgate_x_stride, p.dim);
+  const auto gradients = [&](auto small) {
 #pragma unroll
-  for (int j = T - 1; j >= 0; --j) {
-    const bool start = STARTS && (starts >> j & 1);
-    float ox[V], oa[V], oi[V];
-    const vec ka = exp_a[j * 64], kx = exp_x[j * 64];
+    for (int j = T - 1; j >= 0; --j) {
+      const bool start = STARTS && (starts >> j & 1);
+      float ox[V], oa[V], oi[V];
+      const vec ka = exp_a[j * 64], kx = exp_x[j * 64];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      float rest_r, rest_i;
-      const float r = sigmoid_from(ka[v], rest_r), i = sigmoid_from(kx[v], rest_i);
-      const float dec = 1.0f + n[j][v], beta2 = __builtin_fmaf(-n[j][v], dec, -n[j][v]);
-      const float inv = __builtin_amdgcn_rsqf(__builtin_amdgcn_fmed3f(beta2, kLeastNormal, 2.0f));
-      const float g = widen_at<BF16, V>(rd[j], v) + e[v];
-      const float prev = j > 0 ? hl[j > 0 ? j - 1 : 0][v] : before[v];
-      ox[v] = g * i * (beta2 * inv);
-      const float wx = ox[v] * widen_at<BF16, V>(rx[j], v);
-      oi[v] = wx * rest_i;
-      const float big = k[v] * r * dec * __builtin_fmaf(dec * (inv * inv), wx, start ? 0.0f : -g * prev);
-      oa[v] = big * rest_r;
-      dlam[v] += j < w.n ? big : 0.0f;
-      e[v] = start ? 0.0f : __builtin_fmaf(n[j][v], g, g);
+      for (int v = 0; v < V; ++v) {
+        float rest_r, rest_i;
+        const float r = sigmoid_from(ka[v], rest_r), i = sigmoid_from(kx[v], rest_i);
+        const float n = rest_of<small()>(m[j][v]), dec = factor_of<small()>(m[j][v]), beta2 = __builtin_fmaf(-n, dec, -n);
+        const float inv = __builtin_amdgcn_rsqf(__builtin_amdgcn_fmed3f(beta2, kLeastNormal, 2.0f));
+        const float g = widen_at<BF16, V>(rd[j], v) + e[v];
+        const float prev = j > 0 ? hl[j > 0 ? j - 1 : 0][v] : before[v];
+        ox[v] = g * i * (beta2 * inv);
+        const float wx = ox[v] * widen_at<BF16, V>(rx[j], v);
+        oi[v] = wx * rest_i;
+        const float big = k[v] * r * dec * __builtin_fmaf(dec * (inv * inv), wx, start ? 0.0f : -g * prev);
+        oa[v] = big * rest_r;
+        dlam[v] += j < w.n ? big : 0.0f;
+        e[v] = start ? 0.0f : decayed<small()>(m[j][v], g);
+      }
+      store_row<BF16, V, AUX>(dx, j, w.n, w.out, ox);
+      store_row<BF16, V, AUX>(da, j, w.n, w.out, oa);
+      store_row<BF16, V, AUX>(di, j, w.n, w.out, oi);
+      if (j % 2 == 0) __builtin_amdgcn_sched_barrier(0);  // no more than two steps at once: registers
     }
-    store_row<BF16, V, AUX>(dx, j, w.n, w.out, ox);
-    store_row<BF16, V, AUX>(da, j, w.n, w.out, oa);
-    store_row<BF16, V, AUX>(di, j, w.n, w.out, oi);
-    if (j % 2 == 0) __builtin_amdgcn_sched_barrier(0);  // no more than two steps at once: registers
-  }
+  };
+  if (__all(slow)) gradients(std::true_type{});
+  else gradients(std::false_type{});
   if (w.wave == 0 && piece == 0 && p.dh0 != nullptr && w.ok)
 #pragma unroll
     for (int v = 0; v < V; ++v) p.dh0[w.b * p.dim + w.ch + v] = e[v];

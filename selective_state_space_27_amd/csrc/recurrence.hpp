@@ -2,16 +2,19 @@
 // gradient and its one-token step.  Per channel and step:
 //   r = sigmoid(gate_a), i = sigmoid(gate_x), s = k r with k = c softplus(lam),
 //   a = exp(-s), beta = sqrt(1 - a^2), h <- a h + beta i x.
-// The decay is kept as n = a - 1 = expm1(-s), in [-1, 0]: decays are near 1 (s is a
-// few hundredths), where a itself would hold only the leading digits of n, and n
-// gives both h + n h and beta^2 = -n (2 + n) without cancellation.
+// The decay is kept as one number m, whose sign tells which:
+//   n = a - 1 = expm1(-s), -1/2 < n <= -0, while s <= 1/2: most decays are near 1 (s is a
+//     few hundredths), where a itself would hold only the leading digits of n, and n
+//     gives both h + n h and beta^2 = -n (2 + n) without cancellation;
+//   a itself, 0 <= a < 0.61, beyond: 1 + n would lose the digits of a small a, and with
+//     them those of all that is a product with it (dgate_a, dh0, a state's last traces).
 #pragma once
 
 #include "common.hpp"
 
 namespace mss {
 
-// Of s, for the polynomials of exp_less_one.
+// Of s, for the polynomials of decay_of.
 constexpr float kPolySmall = 0.25f, kPolyMax = 0.5f;
 
 // E = exp(-v).  EXACT (fp32 tensors): with what the rounding of the argument
@@ -45,12 +48,12 @@ __device__ __forceinline__ float sigmoid_from(float e, float& rest) {
   return s;
 }
 
-// exp(-s) - 1 for s >= 0: s times a polynomial fitted to (exp(-s) - 1) / s at
-// Chebyshev points (off by 2.4e-9 of 1 up to 1/4, where decays of a trained layer
-// lie; by 1.2e-9 up to 1/2), beyond 1/2 the plain difference, which would lose
-// digits below.  SMALL: no s is above kPolySmall.
-template <bool SMALL>
-__device__ __forceinline__ float exp_less_one(float s) {
+// m for s >= 0.  n is s times a polynomial fitted to (exp(-s) - 1) / s at Chebyshev
+// points (off by 2.4e-9 of 1 up to 1/4, where decays of a trained
+// layer lie; by 1.2e-9 up to 1/2); a comes with the rounding of its argument put back
+// where the gates' are (EXACT).  SMALL: no s is above kPolySmall, so m is n.
+template <bool SMALL, bool EXACT>
+__device__ __forceinline__ float decay_of(float s) {
   if constexpr (SMALL) {
     float p = __builtin_fmaf(s, -0.007514301221817732f, 0.04149100184440613f);
     p = __builtin_fmaf(s, p, -0.16665112972259521f);
@@ -62,8 +65,28 @@ __device__ __forceinline__ float exp_less_one(float s) {
     p = __builtin_fmaf(s, p, -0.16666245460510254f);
     p = __builtin_fmaf(s, p, 0.4999998211860657f);
     p = __builtin_fmaf(s, p, -1.0f) * s;
-    return s > kPolyMax ? exp2_fast(-s * kLog2e) - 1.0f : p;
+    return s > kPolyMax ? exp_neg<EXACT>(s) : p;
   }
+}
+// Whether m is n.
+template <bool SMALL>
+__device__ __forceinline__ bool is_rest(float m) {
+  return SMALL || (int32_t)__float_as_uint(m) < 0;
+}
+// n, to a few units of it either way.
+template <bool SMALL>
+__device__ __forceinline__ float rest_of(float m) {
+  return is_rest<SMALL>(m) ? m : m - 1.0f;
+}
+// a, of which 1 + n keeps all digits while n > -1/2.
+template <bool SMALL>
+__device__ __forceinline__ float factor_of(float m) {
+  return is_rest<SMALL>(m) ? 1.0f + m : m;
+}
+// a v, of a state, a gradient or a product of decays.
+template <bool SMALL>
+__device__ __forceinline__ float decayed(float m, float v) {
+  return __builtin_fmaf(m, v, is_rest<SMALL>(m) ? v : 0.0f);
 }
 // beta = sqrt(1 - a^2).
 __device__ __forceinline__ float beta_of(float n) { return __builtin_amdgcn_sqrtf(-n * (2.0f + n)); }

@@ -85,8 +85,8 @@ __global__ void __launch_bounds__(kThreadsStep) recurrence_step_kernel(Recurrenc
   load4<false>(p.h + from * p.dim, d, n, h);
 #pragma unroll
   for (int j = 0; j < kChannels; ++j) {
-    const float m = exp_less_one<false>(decay_rate(p.c, lam[j]) * sigmoid_of<!BF16>(ga[j]));
-    h[j] = __builtin_fmaf(m, h[j], h[j]) + beta_of(m) * sigmoid_of<!BF16>(gx[j]) * x[j];
+    const float m = decay_of<false, !BF16>(decay_rate(p.c, lam[j]) * sigmoid_of<!BF16>(ga[j]));
+    h[j] = decayed<false>(m, h[j]) + beta_of(rest_of<false>(m)) * sigmoid_of<!BF16>(gx[j]) * x[j];
   }
   store4<false>(p.h_out + row * p.dim, d, n, h);
   store4<BF16>(static_cast<char*>(p.y) + row * p.y_stride * es, d, n, h);
