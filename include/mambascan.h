@@ -728,7 +728,13 @@ mss_status mss_gated_recurrence_step(const float* h, const int64_t* parents, con
 /* and the n_out largest over k and v are taken, in descending order, ties   */
 /* by the lower k, then the larger logit, then the lower v: out_scores       */
 /* (rounded to fp32), parents (k) and tokens (v), [batch, n_out] each.       */
-/* Totals are compared in 64 bits.                                           */
+/* Totals are compared in 64 bits, each formed from a beam's log sum, whose  */
+/* terms are added up in fp32: it is off by up to 140 units of 2^-24 (by some */
+/* 1e-7 mostly), the same for all candidates of the beam.  So a beam's own   */
+/* candidates keep the order of their logits whatever the totals' size, rows  */
+/* of the same bits tie exactly, and two different rows' totals nearer than   */
+/* that (the same logits in another order, say) come in an order that is      */
+/* repeatable but not defined.                                               */
 /*   A logit of -infinity (a banned token) has total -infinity.              */
 /*   finished[b, k] not zero: the beam's only candidate is the token eos,    */
 /*     with total scores[b, k]; its other totals are -infinity and its       */

@@ -19,7 +19,10 @@ def beam_select(logits, scores, n_out=None, *, finished=None, eos=None, stream=N
 
     total = scores + log_softmax(logits), over beams and vocabulary; in
     descending order, ties by the lower beam, then the larger logit (where 64 bits
-    of a total do not tell them apart), then the lower token.  logits: [batch,
+    of a total do not tell them apart), then the lower token.  A beam's log sum
+    is formed in fp32, so totals of two beams whose rows differ are told apart
+    down to some 1e-7 (8.4e-6 each at most); below, their order is repeatable but
+    not defined.  logits: [batch,
     beams, vocab] float32 or bfloat16 (rows may have a stride); scores: [batch,
     beams] float32, the beams' totals so far (-inf: not in use); finished:
     [batch, beams] bool or uint8, beams whose only candidate is the token
