@@ -11,7 +11,7 @@ import torch
 import selective_state_space_27_amd as _mss
 
 from .norms import _code, _on, _rows, _workspace_size
-from .recurrence import _address, _state
+from .recurrence import _address, _marks, _state
 
 
 def beam_select(logits, scores, n_out=None, *, finished=None, eos=None, stream=None):
@@ -42,9 +42,7 @@ def beam_select(logits, scores, n_out=None, *, finished=None, eos=None, stream=N
     if scores is None:
         raise TypeError("scores must be a torch.Tensor")
     sp = _state(scores, "scores", (batch, beams), dev)
-    if finished is not None:
-        _mss._check(finished, "finished", (batch, beams),
-                    torch.uint8 if finished.dtype == torch.uint8 else torch.bool, dev)
+    fp = _marks(finished, "finished", (batch, beams), dev)
     if eos is not None and not 0 <= eos < vocab:
         raise ValueError(f"eos {eos} is not in the vocabulary of {vocab}")
     if finished is not None and eos is None:
@@ -59,7 +57,7 @@ def beam_select(logits, scores, n_out=None, *, finished=None, eos=None, stream=N
         tokens = torch.empty_like(parents)
         done = torch.empty((batch, n), dtype=torch.bool, device=dev) if eos is not None else None
         ws = torch.empty(need, dtype=torch.uint8, device=dev)
-        st = _mss.lib().mss_beam_select(lp, ls, sp, _address(finished), -1 if eos is None else eos,
+        st = _mss.lib().mss_beam_select(lp, ls, sp, fp, -1 if eos is None else eos,
                                         best.data_ptr(), parents.data_ptr(), tokens.data_ptr(), _address(done), batch,
                                         beams, vocab, n, io, 0, ws.data_ptr(), need, handle)
     _mss._raise(st, "mss_beam_select")

@@ -43,10 +43,12 @@ def _address(t):
     return None if t is None else t.data_ptr()
 
 
-def _marks(t, shape, device):
+def _marks(t, name, shape, device):
+    """Pointer of a bool or uint8 tensor, or None."""
     if t is None:
         return None
-    _mss._check(t, "starts", shape, torch.uint8 if t.dtype == torch.uint8 else torch.bool, device)
+    dtype = torch.uint8 if isinstance(t, torch.Tensor) and t.dtype == torch.uint8 else torch.bool
+    _mss._check(t, name, shape, dtype, device)
     return t.data_ptr()
 
 
@@ -74,7 +76,7 @@ def gated_recurrence_fwd(x, gate_a, gate_x, lam, *, c=8.0, h0=None, starts=None,
     ap, as_ = _rows(gate_a, "gate_a", shape, x.dtype, dev)
     ip, is_ = _rows(gate_x, "gate_x", shape, x.dtype, dev)
     lp = _vec(lam, "lam", dim, dev)
-    hp, sp = _state(h0, "h0", (b, dim), dev), _marks(starts, (b, length), dev)
+    hp, sp = _state(h0, "h0", (b, dim), dev), _marks(starts, "starts", (b, length), dev)
     handle, here = _on(stream, dev)
     with here:
         out, op, os = _result(out, "out", shape, x.dtype, dev, x)
@@ -112,7 +114,7 @@ def gated_recurrence_bwd(dy, x, gate_a, gate_x, lam, states, *, c=8.0, starts=No
     ip, is_ = _rows(gate_x, "gate_x", shape, dy.dtype, dev)
     lp = _vec(lam, "lam", dim, dev)
     tp = _state(states, "states", (b, _chunks(length), dim), dev)
-    hp, sp = _state(dh_last, "dh_last", (b, dim), dev), _marks(starts, (b, length), dev)
+    hp, sp = _state(dh_last, "dh_last", (b, dim), dev), _marks(starts, "starts", (b, length), dev)
     handle, here = _on(stream, dev)
     with here:
         dx, dxp, dxs = _result(dx, "dx", shape, dy.dtype, dev, dy)
