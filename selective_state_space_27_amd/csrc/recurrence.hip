@@ -13,13 +13,21 @@
 // NaN: A is not multiplied in but skipped (a start is the same for all channels,
 // so the choice is a scalar one).
 //
-// Bound by memory where there is enough to do: 4 x 8192 x 5120 bf16 forward 257 us (1.34
-// GB at 5.2 TB/s; a 1 GiB copy reaches 5.13), backward 507 us (2.35 GB, 4.6 TB/s);
-// 131072 x 2560 forward 521 us (5.1); 4 x 8192 x 2560 fp32 235 and 431 us (5.7, 5.5).  The
-// vector unit follows: busy 60% of the forward and 71% of the backward (31 and 71
+// Bound by memory where there is enough to do: 4 x 8192 x 5120 bf16 forward 260 us (1.34
+// GB at 5.1 TB/s; a 1 GiB copy reaches 5.13), backward 507 us (2.35 GB, 4.6 TB/s);
+// 131072 x 2560 forward 525 us (5.1); 4 x 8192 x 2560 fp32 235 and 431 us (5.7, 5.5).  The
+// vector unit follows: busy 59% of the forward and 73% of the backward (31 and 72
 // instructions for 64 values, five and eight of them transcendental, at a quarter of the
-// rate).  Odd rows of fp32 with starts (3 x 4099 x 1001) run at 4 TB/s.  With
-// one piece (up to 128 steps) a call is a single launch of 5.5 us.
+// rate).  Odd rows of fp32 with starts (3 x 4099 x 1001) run at 4 TB/s.
+//
+// These are layers whose decays are slow (k up to kPolySmall).  A wave with a faster
+// channel takes the general code, for all of its channels the same time whether one of
+// them is fast or all: 4 x 8192 x 5120 bf16 270 and 553 us, 131072 x 2560 forward 562,
+// 4 x 8192 x 2560 fp32 244 and 437, 3 x 4099 x 1001 54 and 86 (slow: 52 and 87).
+//
+// Up to 128 steps the forward is a single launch of 5.5 us, and so is the backward of up
+// to 64 steps of one batch row; more steps take a launch more to clear the words that
+// pieces hand on, and dlam from more than one piece or row one to sum it.
 #include "launch.hpp"
 #include "norm_common.hpp"
 #include "recurrence.hpp"
@@ -777,7 +785,7 @@ Cut cut_of(int64_t batch, int64_t seqlen, int64_t dim, int v, int steps) {
   return c;
 }
 
-// 131072 x 512 bf16 (4 streams) 238 us forward and 467 backward, with groups 133 and 258; 65536
+// 131072 x 512 bf16 (4 streams) 238 us forward and 467 backward, with groups 137 and 258; 65536
 // x 1001 fp32 (16) 242 and 471, 234 and 466; with 20 to 160 streams groups take up to 6% longer
 // (4 x 8192 x 5120: 257 and 507, 269 and 539).
 constexpr int64_t kFewStreams = 16, kManyPieces = 32;
@@ -831,11 +839,16 @@ template <bool BF16>
 bool whole_lines(const void* p, int64_t stride) {
   return ((reinterpret_cast<uintptr_t>(p) | (uint64_t)stride * (BF16 ? 2 : 4)) & 63u) == 0;
 }
-// Gradients of other rows: a share of the streams for each die where there are many
-// (4 x 8192 x 2561 fp32 586 -> 532 us, 8 x 2048 x 1537 192 -> 165; few wait for each other,
-// 32768 x 770 bf16 139 -> 167), and plain stores once the tensors together are beyond the
-// last-level cache (706 -> 586 us, 6 x 11725 x 2099 1274 -> 1034; but 3 x 4099 x 1001 90 -> 99).
-// The forward, with one output beside three inputs, gains little or loses.
+// Gradients of other rows.  A share of the streams for each die where there are many
+// (25 to 100 MB a tensor: with 8 streams of fp32 shares take 9 to 14% more time, with 16 3
+// to 9% more, 24 and 32 2% less to 6% more, 48 2 to 5% less, 64 10 to 11%, 264 8 to 14%;
+// bf16 gains a third of that).  And plain stores for large tensors: up to 32 MB a tensor,
+// all seven in the 256 MB cache, they take 0 to 7% less time; from 40 to 64 MB, where some
+// of what is read next is still there, 9 to 21% more; from 80 MB on 6 to 23% less (24 to
+// 160 MB of 2099 and 1001 fp32 and 1537 bf16 channels).  The rule takes the upper border.
+// The forward, with one output beside three inputs, has neither: shares take up to 13% less
+// with 48 streams and more and 80 MB or less, but 0 to 6% more from 100 MB on, and with
+// fewer streams up to 19% more; plain stores 2% less to 13% more.
 constexpr int64_t kManyStreams = 48, kNearBytes = 64ll << 20;
 
 size_t bwd_part_offset(const Cut& c) { return (c.bytes + 255) / 256 * 256; }

@@ -49,9 +49,10 @@ __device__ __forceinline__ float sigmoid_from(float e, float& rest) {
 }
 
 // m for s >= 0.  n is s times a polynomial fitted to (exp(-s) - 1) / s at Chebyshev
-// points (off by 2.4e-9 of 1 up to 1/4, where decays of a trained
-// layer lie; by 1.2e-9 up to 1/2); a comes with the rounding of its argument put back
-// where the gates' are (EXACT).  SMALL: no s is above kPolySmall, so m is n.
+// points (with its fp32 coefficients off by 4.8e-9 of itself up to 1/4, where decays of
+// a trained layer lie; by 4.5e-9 up to 1/2: a twelfth of a unit); a comes with the
+// rounding of its argument put back where the gates' are (EXACT).  SMALL: no s is above
+// kPolySmall, so m is n.
 template <bool SMALL, bool EXACT>
 __device__ __forceinline__ float decay_of(float s) {
   if constexpr (SMALL) {
