@@ -14,9 +14,9 @@
 // before it.  Where more pass than there is room for (ties, a sorted row), the bound is
 // raised first, bit by bit where need be.
 //
-// 32 x 8 x 50277 bf16 (25.7 MB): 11 us the slices, 5 us the merge (all logits equal: 33
-// in all); 8 x 16 x 250001 fp32 (128 MB), n = 32: 28 us and 10 us (110).  The first is
-// bound by memory where logits are many (4.6 TB/s), else by the latency of its steps,
+// 32 x 8 x 50277 bf16 (25.7 MB): 10 us the slices, 7 us the merge (all logits equal: 33
+// in all); 8 x 16 x 250001 fp32 (128 MB), n = 32: 27 us and 12 us (110).  The first is
+// bound by memory where logits are many (4.8 TB/s), else by the latency of its steps,
 // as the second always is.
 #include "beam.hpp"
 #include "launch.hpp"

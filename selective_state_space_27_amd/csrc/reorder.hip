@@ -7,9 +7,10 @@
 // column's reads under way at once.  Rows that stay are neither read nor written.
 //
 // Bound by memory: 32 x 8 beams, four layers of 380 KB each, half of the rows moving
-// (388 MB read and written), 61 us or 6.3 TB/s with non-temporal stores, 80 us without
-// (what is written then takes the place of what is read next in the last-level cache);
-// holding eight beams in registers instead of LDS took 108 us.
+// (388 MB read and written), 76 us on inputs from memory (5.1 TB/s, what a large copy
+// reaches).  The same inputs again and again, partly in the last-level cache: 61 us with
+// non-temporal stores, 80 us without (what is written then takes the place of what is read
+// next in that cache), 108 us with eight beams in registers instead of LDS.
 #include "launch.hpp"
 #include "rows.hpp"
 
