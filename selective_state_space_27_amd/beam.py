@@ -1,6 +1,7 @@
 """Python binding of beam search on recurrent states (``include/mambascan.h``):
 selection over beams and vocabulary, and the beams' states following their
-parents.  Checks, streams and errors are as in norms.py.
+parents.  Checks, streams and errors are as in norms.py; there is no autograd, and
+it does not notice that reorder_states writes in place.
 """
 from __future__ import annotations
 

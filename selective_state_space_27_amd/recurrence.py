@@ -8,6 +8,12 @@ and its one-token step.
 Activations, checks, streams and errors are as in norms.py: tensors whose
 leading dimensions collapse to rows of one stride (x and the gates may be
 slices of one projection's output), outputs new and contiguous unless given.
+
+As everywhere in the package there is no autograd: results require no gradient
+whatever the inputs do, and a training step calls gated_recurrence_bwd itself (in
+a torch.autograd.Function around the layer, say).  Nor does autograd notice what
+is written in place (the step's state, given outputs): what a graph still needs of
+those has to be kept apart.
 """
 from __future__ import annotations
 
