@@ -644,8 +644,10 @@ size_t mss_wgrad8_workspace_size(const void* dy, int64_t dy_stride, int64_t toke
 /*   state before every chunk's first step (and before any start there),     */
 /*   which mss_gated_recurrence_bwd needs.                                   */
 /* h0, starts, h_last and states may be NULL.  States, sums and gates are in */
-/* fp32; y is rounded once.  The same call gives the same bits; with other   */
-/* batch or dim a sequence's may differ by roundings.                        */
+/* fp32: 1 - a to a few units of its own, and so is a (times its exponent,   */
+/* where that is above 1/2); y is rounded once.  The same call gives the same */
+/* bits; with other batch or dim, or another lam of a neighbouring channel,  */
+/* a channel's may differ by roundings.                                      */
 /* Supported: c > 0 and finite (else MSS_ERR_UNSUPPORTED); batch * seqlen *  */
 /* stride below 2^47, batch * ceil(seqlen / 64) * ceil(dim / 64) below 2^23  */
 /* (else MSS_ERR_SHAPE).  `flags` must be 0.  Outputs must not overlap       */
